@@ -86,6 +86,9 @@ extern "C" {
 #define LORA_STATUS_TIMEOUT 0x4u         /* a kernel's bounded wait for its own copies gave up;
                                             the outputs of that call are unspecified */
 #define LORA_STATUS_BAD_WEIGHT 0x8u      /* a paged weight address was not 16-byte aligned */
+#define LORA_STATUS_BAD_SLOT 0x10u       /* a cache slot or page id lay outside the cache */
+#define LORA_STATUS_BAD_POSITION 0x20u   /* a token's position lay outside the rotation table */
+#define LORA_STATUS_BAD_LENGTH 0x40u     /* a sequence's rows or keys did not fit their buffers */
 
 #define LORA_MAX_SLICES 3
 #define LORA_MAX_LORAS 1024
@@ -406,6 +409,190 @@ int lora_apply_noalloc(const int32_t *token_lora_mapping, const int32_t *num_tok
                        float *u, uint16_t *y, int64_t y_row_stride, int32_t *sorted_token_ids,
                        int32_t *num_tokens_per_lora, int32_t *lora_token_start_loc,
                        uint32_t *status, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The operators of a decoder layer around its LoRA products: the norm whose
+ * output a layer's product and lora_shrink read, and, behind the qkv product
+ * that lora_expand completes, the append of k and v to a paged cache of 4-bit
+ * values and the attention over it.  They keep the conventions above (device
+ * pointers, static buffers of max_num_tokens rows with n valid ones, n in
+ * device memory, stream order, no allocation, codes for bad arguments); where
+ * a call takes `status`, it is NULL or a device word into which the call ORs
+ * LORA_STATUS_* bits for what only the data reveals (lora_read_status reads and
+ * clears it; the word must be 16-byte aligned for that).  16-bit data is bf16, or fp16 in the *_f16 forms.
+ */
+
+#define LORA_NORM_MAX_HIDDEN 32768
+
+/*
+ * Residual addition and root-mean-square norm, with the result in 16 bits
+ * and / or in 8 bits with scales:
+ *   z[t][h]     = x[t][h] + residual[t][h]                      (fp32)
+ *   residual_out[t][h] = 16-bit(z[t][h])
+ *   n[t][h]     = z[t][h] / sqrt(mean_h(z[t][h]^2) + eps) * weight[h]  (fp32)
+ *   y[t][h]     = 16-bit(n[t][h])
+ *   y8_scale[t][g] = max(max_{h in group g} |n[t][h]| / 448, 2^-100)
+ *   y8[t][h]    = e4m3(n[t][h] / y8_scale[t][h / group]), to the nearest, ties
+ *                 to even, saturating at 448
+ * for t < n; rows t >= n are neither read nor written.  A NaN among a row's
+ * z makes the row's n, scales and codes NaN.
+ *
+ *   x             16-bit[max_num_tokens][x_row_stride]
+ *   residual      NULL (z = x), or 16-bit[max_num_tokens][residual_row_stride]
+ *   residual_out  NULL, or where z goes; may be residual or x itself
+ *   weight        16-bit[hidden]
+ *   y             NULL, or 16-bit[max_num_tokens][y_row_stride] (y may be x)
+ *   y8            NULL, or e4m3[max_num_tokens][y8_row_stride]
+ *   y8_scale      fp32[max_num_tokens][hidden / group], given with y8
+ *   group         columns per scale: hidden (one scale a row) or 128
+ *   num_tokens    device int32: n (clamped to [0, max_num_tokens], which sets
+ *                 LORA_STATUS_BAD_NUM_TOKENS)
+ * Sizes: hidden a multiple of 8 up to LORA_NORM_MAX_HIDDEN (a multiple of 128
+ * with groups of 128); 16-byte aligned pointers and row strides that are
+ * multiples of 8 (y8: 8-byte aligned).  At least one of y, y8 and
+ * residual_out is given.
+ */
+int lora_add_rmsnorm(const uint16_t *x, int64_t x_row_stride, const uint16_t *residual,
+                     int64_t residual_row_stride, const uint16_t *weight, float eps,
+                     int64_t hidden, uint16_t *residual_out, int64_t residual_out_row_stride,
+                     uint16_t *y, int64_t y_row_stride, uint8_t *y8, int64_t y8_row_stride,
+                     float *y8_scale, int64_t group, const int32_t *num_tokens,
+                     int64_t max_num_tokens, uint32_t *status, void *stream);
+int lora_add_rmsnorm_f16(const uint16_t *x, int64_t x_row_stride, const uint16_t *residual,
+                         int64_t residual_row_stride, const uint16_t *weight, float eps,
+                         int64_t hidden, uint16_t *residual_out,
+                         int64_t residual_out_row_stride, uint16_t *y, int64_t y_row_stride,
+                         uint8_t *y8, int64_t y8_row_stride, float *y8_scale, int64_t group,
+                         const int32_t *num_tokens, int64_t max_num_tokens, uint32_t *status,
+                         void *stream);
+
+/*
+ * The 4-bit paged cache.  One uint8 array, 16-byte aligned,
+ *   cache[num_pages][num_kv_heads][page_size / 16][18 * head_dim]
+ * where the last index is a block of 16 consecutive tokens of a page:
+ *   [0, 8 D)      K codes, token r at r * D / 2: two e2m1 codes a byte, the even
+ *                 dimension in the low nibble
+ *   [8 D, 16 D)   V codes, the same
+ *   [16 D, 17 D)  K scales, token r at r * D / 16: one e4m3 value for each 16
+ *                 consecutive dimensions
+ *   [17 D, 18 D)  V scales, the same
+ * (D = head_dim, 64 or 128; 4.5 bits a value).  A value is e2m1(code) *
+ * e4m3(scale) * k_scale or v_scale, a factor of the whole cache that the
+ * calls take: choose it so that typical magnitudes land around 6 * 2^0 (the
+ * scales cover 2^-9 .. 448).  Slot s of the cache is token s % page_size of page
+ * s / page_size.  page_size is a multiple of 16 up to LORA_KV4_MAX_PAGE_SIZE.
+ */
+#define LORA_KV4_MAX_PAGE_SIZE 1024
+#define LORA_KV4_MAX_SEQS 65536
+#define LORA_KV4_MAX_HEADS 256
+
+/*
+ * Rotation of q and k by position, and the append of k and v to the cache:
+ * for t < n with 0 <= position < max_positions
+ *   q_out[t] = 16-bit(rot(q[t])),  cache slot slots[t] <- 4-bit(rot(k[t])), 4-bit(v[t])
+ * rot turns the pair (a, b) of dimensions (i, i + rope_dim / 2), or (2 i, 2 i +
+ * 1) when interleaved, into (a c - b s, b c + a s) with c = rope[pos][i] and
+ * s = rope[pos][rope_dim / 2 + i], i < rope_dim / 2, in fp32 with each product
+ * and sum rounded once; dimensions from rope_dim on stay.  4-bit() takes
+ * 16 consecutive dimensions: with w = value * (1 / k_scale) (or v_scale),
+ *   scale = e4m3(min(max|w| / 6, 448)),   code = e2m1(w / scale)
+ * each to the nearest with ties to even, codes saturating at 6; where the
+ * scale is 0 or NaN the codes are 0.  (A NaN among the 16 makes the scale NaN,
+ * so all 16 read as NaN; an infinity reads as the largest value.)
+ *
+ *   q, q_out      NULL, or 16-bit[max_num_tokens][row stride], num_q_heads *
+ *                 head_dim columns used; q_out may be q
+ *   k, v          16-bit[max_num_tokens][row stride], num_kv_heads * head_dim
+ *   rope          NULL (no rotation), or fp32[max_positions][rope_dim]
+ *   positions     int32[max_num_tokens], given with rope
+ *   slots         int32[max_num_tokens]; -1: the token's k and v are not
+ *                 stored (its q is rotated all the same).  The slots of one
+ *                 call must differ.
+ *   k_held, v_held  NULL, or 16-bit[max_num_tokens][num_kv_heads * head_dim]
+ *                 out: the values that the cache now stands for, written for
+ *                 the stored tokens (for a caller that attends to the chunk it
+ *                 has just appended without reading it back)
+ * A position outside [0, max_positions) sets LORA_STATUS_BAD_POSITION and the
+ * token is skipped altogether; a slot that is neither -1 nor inside the cache
+ * sets LORA_STATUS_BAD_SLOT and the token's k and v are not stored.
+ * Sizes: rope_dim a multiple of 32 up to head_dim; strides multiples of 8;
+ * pointers 16-byte aligned; num_pages * page_size below 2^31; the scales finite
+ * and above 0.
+ */
+int lora_kv4_append(const uint16_t *q, int64_t q_row_stride, uint16_t *q_out,
+                    int64_t q_out_row_stride, int num_q_heads, const uint16_t *k,
+                    int64_t k_row_stride, const uint16_t *v, int64_t v_row_stride,
+                    const float *rope, int64_t max_positions, int rope_dim, int interleaved,
+                    const int32_t *positions, const int32_t *slots, uint8_t *cache,
+                    int64_t num_pages, int num_kv_heads, int page_size, int head_dim,
+                    float k_scale, float v_scale, uint16_t *k_held, uint16_t *v_held,
+                    const int32_t *num_tokens, int64_t max_num_tokens, uint32_t *status,
+                    void *stream);
+int lora_kv4_append_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *q_out,
+                        int64_t q_out_row_stride, int num_q_heads, const uint16_t *k,
+                        int64_t k_row_stride, const uint16_t *v, int64_t v_row_stride,
+                        const float *rope, int64_t max_positions, int rope_dim, int interleaved,
+                        const int32_t *positions, const int32_t *slots, uint8_t *cache,
+                        int64_t num_pages, int num_kv_heads, int page_size, int head_dim,
+                        float k_scale, float v_scale, uint16_t *k_held, uint16_t *v_held,
+                        const int32_t *num_tokens, int64_t max_num_tokens, uint32_t *status,
+                        void *stream);
+
+/*
+ * Causal attention of ragged rows of queries over the cache.  Sequence b has
+ * the rows q_start[b] <= t < q_start[b + 1] of q and kv_len[b] keys (its rows'
+ * own keys among them: they are appended first); its key j is slot
+ * page_table[b][j / page_size] * page_size + j % page_size.  Row i of its m rows
+ * stands at position p = kv_len[b] - m + i and sees the keys
+ *   0 <= j <= p, and j > p - window where window > 0:
+ *   x_j   = softmax_scale * q[t][h] . K[j][h / G]          G = num_q_heads / num_kv_heads
+ *   out[t][h] = 16-bit( sum_j exp(x_j - m) V[j][h / G] / sum_j exp(x_j - m) )
+ *   lse[t][h] = log sum_j exp(x_j)                         (fp32)
+ * A row that sees no key gets 0 and lse = -inf.  One call serves single-token
+ * decode, a few drafted tokens and chunks of prefill, mixed in one batch.
+ *
+ *   q, out        16-bit[max_num_tokens][row stride]; rows from
+ *                 q_start[num_seqs] on are neither read nor written
+ *   lse           NULL, or fp32[max_num_tokens][num_q_heads] out
+ *   q_start       device int32[num_seqs + 1], ascending from 0
+ *   kv_len        device int32[num_seqs]
+ *   page_table    device int32[num_seqs][table_stride]; entries behind a
+ *                 sequence's last page are not read
+ *   max_q_len     a bound on the sequences' rows (host): it picks the kernels
+ *   workspace     lora_kv4_attention_workspace_size bytes, 16-byte aligned,
+ *                 zero-filled before its first use (every call leaves its
+ *                 counters at zero); calls that share it run in one stream's order
+ * Data that does not fit: a page id outside the cache masks its keys
+ * (LORA_STATUS_BAD_SLOT); kv_len outside [0, table_stride * page_size] and rows
+ * outside [0, max_num_tokens] are clamped and rows beyond max_q_len get no
+ * output (LORA_STATUS_BAD_LENGTH).  What lies in the cache behind a sequence's
+ * keys may hold anything, NaN scales included.
+ * Sums, maxima and accumulators are fp32.  The products run on fp16 operands:
+ * a cached value (without the cache's factor) is exact in fp16, q is scaled by
+ * a power of two per row so that its largest element lies in [2^14, 2^15)
+ * (exact but for elements below 2^-29 of the row's largest), and a
+ * probability is rounded once to fp16.
+ */
+size_t lora_kv4_attention_workspace_size(int64_t num_seqs, int64_t max_num_tokens,
+                                         int64_t max_q_len, int num_q_heads, int num_kv_heads,
+                                         int head_dim);
+int lora_kv4_attention(const uint16_t *q, int64_t q_row_stride, uint16_t *out,
+                       int64_t out_row_stride, float *lse, int num_q_heads, const uint8_t *cache,
+                       int64_t num_pages, int num_kv_heads, int page_size, int head_dim,
+                       float k_scale, float v_scale, const int32_t *q_start,
+                       const int32_t *kv_len, const int32_t *page_table, int64_t table_stride,
+                       int64_t num_seqs, int64_t max_num_tokens, int64_t max_q_len,
+                       float softmax_scale, int64_t window, void *workspace,
+                       size_t workspace_bytes, uint32_t *status, void *stream);
+int lora_kv4_attention_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *out,
+                           int64_t out_row_stride, float *lse, int num_q_heads,
+                           const uint8_t *cache, int64_t num_pages, int num_kv_heads,
+                           int page_size, int head_dim, float k_scale, float v_scale,
+                           const int32_t *q_start, const int32_t *kv_len,
+                           const int32_t *page_table, int64_t table_stride, int64_t num_seqs,
+                           int64_t max_num_tokens, int64_t max_q_len, float softmax_scale,
+                           int64_t window, void *workspace, size_t workspace_bytes,
+                           uint32_t *status, void *stream);
 
 /* Static text for a LORA_OK / LORA_ERR_* code. */
 const char *lora_error_string(int code);

@@ -1,9 +1,9 @@
-// Causal attention of ragged query rows over the 4-bit paged cache (layout in
-// kv4.cuh): one warp per row and head walks the row's keys once, with the
+// Attention over the 4-bit paged cache (layout in kv4.cuh) for sequences with
+// many query rows: one warp per row and head walks the row's keys once, with the
 // running maximum and sum of the softmax in fp32.
-#include "kv4.cuh"
+#include "kv4_attention.cuh"
+#include "kv4_attention.h"
 #include "launch.h"
-#include "layer.h"
 
 namespace grg {
 
@@ -21,8 +21,17 @@ __device__ __forceinline__ int seq_of(const int32_t* q_start, int num_seqs, int 
 }
 }  // namespace
 
+namespace {
+struct PrefillParams {
+  Kv4AttnArgs a;
+  int max_packed_rows;
+};
+}  // namespace
+
 template <int D, bool F16>
-__global__ void __launch_bounds__(kAttnThreads) lora_kv4_attention_kernel(const Kv4AttnArgs p) {
+__global__ void __launch_bounds__(kAttnThreads) lora_kv4_prefill_kernel(const PrefillParams pp) {
+  const Kv4AttnArgs& p = pp.a;
+  const int max_packed_rows = pp.max_packed_rows;
   using B = Kv4Block<D>;
   constexpr int E = D / 32;  // dimensions of a lane
   pdl_wait();
@@ -32,19 +41,13 @@ __global__ void __launch_bounds__(kAttnThreads) lora_kv4_attention_kernel(const 
       (static_cast<long long>(blockIdx.x) * kAttnThreads + threadIdx.x) / 32;
   const int t = static_cast<int>(id / p.num_q_heads), h = static_cast<int>(id % p.num_q_heads);
   const int end = p.q_start[p.num_seqs];
-  if (id == 0 && lane == 0 && p.status && (end < 0 || end > p.max_num_tokens))
-    atomicOr(p.status, kStatusBadLength);
   if (t >= min(end, p.max_num_tokens)) return;
   const int b = seq_of(p.q_start, p.num_seqs, t);
-  const int q0 = p.q_start[b], rows = p.q_start[b + 1] - q0;
-  const long long capacity = p.table_stride * p.page_size;
-  const int kv_raw = p.kv_len[b];
-  const int kv = static_cast<int>(min(max(static_cast<long long>(kv_raw), 0ll), capacity));
-  if ((kv_raw != kv || rows > p.max_q_len) && lane == 0 && p.status)
-    atomicOr(p.status, kStatusBadLength);
-  if (t - q0 >= p.max_q_len || q0 < 0) return;
-  const int pos = kv - rows + (t - q0);
-  const int first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+  const Kv4Seq seq = Kv4Seq::of(p, b);
+  if (t < seq.q0 || t - seq.q0 >= seq.take ||
+      static_cast<long long>(seq.take) * (p.num_q_heads / p.num_kv_heads) <= max_packed_rows)
+    return;
+  const int kv = seq.kv, pos = seq.pos(t - seq.q0), first = seq.first_key(t - seq.q0, p.window);
   const int kvh = h / (p.num_q_heads / p.num_kv_heads);
   float q[E], acc[E], top = -INFINITY, sum = 0.0f;
   const uint16_t* qr = p.q + t * p.q_stride + h * D + lane * E;
@@ -100,19 +103,35 @@ __global__ void __launch_bounds__(kAttnThreads) lora_kv4_attention_kernel(const 
     p.lse[static_cast<long long>(t) * p.num_q_heads + h] = sum > 0.0f ? top + logf(sum) : sum == 0.0f ? -INFINITY : sum;
 }
 
-size_t kv4_attention_workspace(long long, long long, long long, int, int, int) { return 256; }
 
-int launch_kv4_attention(const Kv4AttnArgs& a, bool f16, cudaStream_t stream) {
+int launch_kv4_prefill(const Kv4AttnArgs& a, int max_packed_rows, bool f16, cudaStream_t stream) {
   const void* fn =
-      a.head_dim == 64 ? (f16 ? reinterpret_cast<const void*>(lora_kv4_attention_kernel<64, true>)
-                              : reinterpret_cast<const void*>(lora_kv4_attention_kernel<64, false>))
-                       : (f16 ? reinterpret_cast<const void*>(lora_kv4_attention_kernel<128, true>)
-                              : reinterpret_cast<const void*>(lora_kv4_attention_kernel<128, false>));
+      a.head_dim == 64 ? (f16 ? reinterpret_cast<const void*>(lora_kv4_prefill_kernel<64, true>)
+                              : reinterpret_cast<const void*>(lora_kv4_prefill_kernel<64, false>))
+                       : (f16 ? reinterpret_cast<const void*>(lora_kv4_prefill_kernel<128, true>)
+                              : reinterpret_cast<const void*>(lora_kv4_prefill_kernel<128, false>));
   const long long warps = static_cast<long long>(a.max_num_tokens) * a.num_q_heads;
   const long long grid = (warps * 32 + kAttnThreads - 1) / kAttnThreads;
   if (grid > 0x7FFFFFFFll) return -3;
-  Kv4AttnArgs p = a;
+  PrefillParams p{a, max_packed_rows};
   return launch_pdl(fn, dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, stream, 0, &p);
+}
+
+// Sequences of up to kDecodeRows packed rows take the decode kernel, the others
+// the prefill kernel; a batch whose bound allows no sequence of a kind does not
+// launch that kind's kernel.
+constexpr int kDecodeRows = 32;
+
+size_t kv4_attention_workspace(long long, long long, long long max_q_len, int num_q_heads,
+                               int num_kv_heads, int head_dim) {
+  return kv4_decode_workspace(max_q_len * (num_q_heads / num_kv_heads) > 8 ? 16 : 8, head_dim);
+}
+
+int launch_kv4_attention(const Kv4AttnArgs& a, bool f16, cudaStream_t stream) {
+  const int rc = launch_kv4_decode(a, kDecodeRows, f16, stream);
+  if (rc != 0) return rc;
+  const long long packed = static_cast<long long>(a.max_q_len) * (a.num_q_heads / a.num_kv_heads);
+  return packed > kDecodeRows ? launch_kv4_prefill(a, kDecodeRows, f16, stream) : 0;
 }
 
 }  // namespace grg

@@ -660,16 +660,18 @@ int run_decode(const DecodeParams& q, cudaStream_t stream) {
 constexpr size_t kCounterBytes = kDecCtasMax * kDecWarps * 4;
 }  // namespace
 
-size_t kv4_decode_workspace(int rows, int head_dim) {
-  return kCounterBytes + static_cast<size_t>(kPartialSlots) * rows * (head_dim * 4 + 8);
+size_t kv4_decode_counter_bytes() { return kCounterBytes; }
+size_t kv4_decode_partial_bytes(int rows, int head_dim) {
+  return static_cast<size_t>(kPartialSlots) * rows * (head_dim * 4 + 8);
 }
 
-int launch_kv4_decode(const Kv4AttnArgs& a, int max_packed_rows, bool f16, cudaStream_t stream) {
+int launch_kv4_decode(const Kv4AttnArgs& a, int max_packed_rows, size_t counters_at, bool f16,
+                      cudaStream_t stream) {
   const int group = a.num_q_heads / a.num_kv_heads;
   const bool wide = static_cast<long long>(a.max_q_len) * group > 8;
   DecodeParams p;
   p.a = a;
-  char* w = static_cast<char*>(a.workspace);
+  char* w = static_cast<char*>(a.workspace) + counters_at;
   const int rows = wide ? 16 : 8;
   p.counters = reinterpret_cast<uint32_t*>(w);
   p.part_o = reinterpret_cast<float*>(w + kCounterBytes);

@@ -1,8 +1,9 @@
 // Residual addition and root-mean-square norm with 16-bit and 8-bit outputs:
 //   z = x + r;  n = z * rsqrt(mean(z^2) + eps) * w;  y = 16-bit(n);
 //   scale = max(max|n| / 448, 2^-100) over a row or 128 columns;  y8 = e4m3(n / scale)
-// One CTA per row; the row's z is held in shared memory in fp32 between the
-// sum of squares, the maximum and the stores, so x and r are read once.
+// Bound by HBM (9 bytes an element with every output): one CTA per row, the row
+// in registers between its one read and its one write, 16-byte accesses.  A
+// scale of 128 columns is the maximum over 16 neighbouring lanes.
 #include "kv4.cuh"
 #include "launch.h"
 #include "layer.h"
@@ -10,20 +11,10 @@
 namespace grg {
 
 namespace {
-constexpr int kNormThreads = 256;
+constexpr int kNormMaxThreads = 1024;
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 constexpr float kInv448 = 1.0f / 448.0f;
 
-template <bool F16>
-__device__ __forceinline__ float load16(const uint16_t* p) {
-  if constexpr (F16) return __half2float(*reinterpret_cast<const __half*>(p));
-  return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
-}
-template <bool F16>
-__device__ __forceinline__ uint16_t round16(float v) {
-  if constexpr (F16) return __half_as_ushort(__float2half_rn(v));
-  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
 // max(a / 448, 2^-100) of a maximum taken over abs_bits: NaN stays NaN.
 __device__ __forceinline__ float scale_of(uint32_t bits) {
   const float s = __uint_as_float(bits) * kInv448;
@@ -31,76 +22,141 @@ __device__ __forceinline__ float scale_of(uint32_t bits) {
 }
 }  // namespace
 
-template <bool F16>
-__global__ void __launch_bounds__(kNormThreads) lora_add_rmsnorm_kernel(const NormArgs p) {
-  extern __shared__ float z[];
-  __shared__ float s_sum[kNormThreads / 32];
-  __shared__ uint32_t s_max[kNormThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// Thread i of a CTA holds the row's chunks (of 8 columns) i, i + threads, ... , CH of them.
+template <int CH, bool F16>
+__global__ void __launch_bounds__(kNormMaxThreads) lora_add_rmsnorm_kernel(const NormArgs p) {
+  __shared__ float s_sum[32];
+  __shared__ uint32_t s_max[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  const int chunks = p.hidden >> 3;
   pdl_wait();
   pdl_launch_dependents();
-  const int t = blockIdx.x;
+  const long long t = blockIdx.x;
   const int raw = *p.num_tokens;
   const int n = min(max(raw, 0), p.max_num_tokens);
   if (raw != n && p.status && t == 0 && tid == 0) atomicOr(p.status, kStatusBadNumTokens);
   if (t >= n) return;
-  const uint16_t* x = p.x + t * p.x_stride;
-  const uint16_t* r = p.residual ? p.residual + t * p.residual_stride : nullptr;
-  uint16_t* ro = p.residual_out ? p.residual_out + t * p.residual_out_stride : nullptr;
-  float sum = 0.0f;
-  for (int h = tid; h < p.hidden; h += kNormThreads) {
-    float v = load16<F16>(x + h);
-    if (r) v += load16<F16>(r + h);
-    z[h] = v;
-    sum += v * v;
+  const uint4* x = reinterpret_cast<const uint4*>(p.x + t * p.x_stride);
+  const uint4* r = p.residual ? reinterpret_cast<const uint4*>(p.residual + t * p.residual_stride) : nullptr;
+  const uint4* w = reinterpret_cast<const uint4*>(p.weight);
+  uint4 xv[CH], rv[CH], wv[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * blockDim.x;
+    const bool in = c < chunks;
+    xv[i] = in ? __ldcs(x + c) : make_uint4(0, 0, 0, 0);
+    rv[i] = in && r ? __ldcs(r + c) : make_uint4(0, 0, 0, 0);
   }
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * blockDim.x;
+    wv[i] = c < chunks ? __ldg(w + c) : make_uint4(0, 0, 0, 0);
+  }
+  float z[CH][8], sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const uint32_t a[4] = {xv[i].x, xv[i].y, xv[i].z, xv[i].w};
+    const uint32_t b[4] = {rv[i].x, rv[i].y, rv[i].z, rv[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 f = unpack_t<F16>(a[e]), g = unpack_t<F16>(b[e]);
+      z[i][2 * e] = r ? f.x + g.x : f.x;
+      z[i][2 * e + 1] = r ? f.y + g.y : f.y;
+      sum += z[i][2 * e] * z[i][2 * e] + z[i][2 * e + 1] * z[i][2 * e + 1];
+    }
+  }
+#pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
+  if (p.residual_out) {
+    uint4* ro = reinterpret_cast<uint4*>(p.residual_out + t * p.residual_out_stride);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * blockDim.x;
+      if (c < chunks)
+        ro[c] = make_uint4(pack_t<F16>(z[i][0], z[i][1]), pack_t<F16>(z[i][2], z[i][3]),
+                           pack_t<F16>(z[i][4], z[i][5]), pack_t<F16>(z[i][6], z[i][7]));
+    }
+  }
   __syncthreads();
-  sum = 0.0f;
-  for (int i = 0; i < kNormThreads / 32; ++i) sum += s_sum[i];
+  sum = lane < warps ? s_sum[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = rsqrtf(sum / static_cast<float>(p.hidden) + p.eps);
-  for (int h = tid; h < p.hidden; h += kNormThreads) {
-    const float v = z[h];
-    const float m = v * inv * load16<F16>(p.weight + h);
-    z[h] = m;
-    if (ro) ro[h] = round16<F16>(v);
-    if (p.y) p.y[t * p.y_stride + h] = round16<F16>(m);
+  uint32_t top = 0, tops[CH];
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const uint32_t b[4] = {wv[i].x, wv[i].y, wv[i].z, wv[i].w};
+    tops[i] = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float2 g = unpack_t<F16>(b[e]);
+      z[i][2 * e] *= inv * g.x;
+      z[i][2 * e + 1] *= inv * g.y;
+      tops[i] = max(tops[i], max(abs_bits(z[i][2 * e]), abs_bits(z[i][2 * e + 1])));
+    }
+    if (tid + i * blockDim.x >= chunks) tops[i] = 0;  // 0 * inv may be a NaN
+    top = max(top, tops[i]);
+  }
+  if (p.y) {
+    uint4* y = reinterpret_cast<uint4*>(p.y + t * p.y_stride);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int c = tid + i * blockDim.x;
+      if (c < chunks)
+        y[c] = make_uint4(pack_t<F16>(z[i][0], z[i][1]), pack_t<F16>(z[i][2], z[i][3]),
+                          pack_t<F16>(z[i][4], z[i][5]), pack_t<F16>(z[i][6], z[i][7]));
+    }
   }
   if (!p.y8) return;
-  __syncthreads();
-  uint8_t* y8 = p.y8 + t * p.y8_stride;
+  float scale[CH];
   if (p.group == p.hidden) {
-    uint32_t top = 0;
-    for (int h = tid; h < p.hidden; h += kNormThreads) top = max(top, abs_bits(z[h]));
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) s_max[warp] = top;
     __syncthreads();
-    for (int i = 0; i < kNormThreads / 32; ++i) top = max(top, s_max[i]);
-    const float scale = scale_of(top);
-    if (tid == 0) p.y8_scale[t] = scale;
-    for (int h = tid; h < p.hidden; h += kNormThreads)
-      y8[h] = static_cast<uint8_t>(f32x2_to_e4m3(z[h] / scale, 0.0f));
+    top = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) scale[i] = scale_of(top);
+    if (tid == 0) p.y8_scale[t] = scale[0];
   } else {
-    const int groups = p.hidden / 128;
-    for (int g = warp; g < groups; g += kNormThreads / 32) {
-      uint32_t top = 0;
-      for (int i = lane; i < 128; i += 32) top = max(top, abs_bits(z[g * 128 + i]));
-      const float scale = scale_of(__reduce_max_sync(0xffffffffu, top));
-      if (lane == 0) p.y8_scale[static_cast<long long>(t) * groups + g] = scale;
-      for (int i = lane; i < 128; i += 32)
-        y8[g * 128 + i] = static_cast<uint8_t>(f32x2_to_e4m3(z[g * 128 + i] / scale, 0.0f));
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+#pragma unroll
+      for (int o = 8; o; o >>= 1) tops[i] = max(tops[i], __shfl_xor_sync(0xffffffffu, tops[i], o));
+      scale[i] = scale_of(tops[i]);
+      const int c = tid + i * blockDim.x;
+      if (c < chunks && (lane & 15) == 0) p.y8_scale[t * (chunks >> 4) + (c >> 4)] = scale[i];
     }
+  }
+  uint2* y8 = reinterpret_cast<uint2*>(p.y8 + t * p.y8_stride);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) {
+    const int c = tid + i * blockDim.x;
+    const float f = 1.0f / scale[i];
+    uint32_t b[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) b[e] = f32x2_to_e4m3(z[i][2 * e] * f, z[i][2 * e + 1] * f);
+    if (c < chunks) y8[c] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
   }
 }
 
-int launch_add_rmsnorm(const NormArgs& a, bool f16, cudaStream_t stream) {
-  const void* fn = f16 ? reinterpret_cast<const void*>(lora_add_rmsnorm_kernel<true>)
-                       : reinterpret_cast<const void*>(lora_add_rmsnorm_kernel<false>);
-  const size_t smem = static_cast<size_t>(a.hidden) * 4;
-  if (ensure_smem_attr(fn, smem) != 0) return -6;
+namespace {
+template <int CH>
+int run_norm(const NormArgs& a, bool f16, cudaStream_t stream) {
+  const void* fn = f16 ? reinterpret_cast<const void*>(lora_add_rmsnorm_kernel<CH, true>)
+                       : reinterpret_cast<const void*>(lora_add_rmsnorm_kernel<CH, false>);
+  const int chunks = a.hidden / 8;
+  const int threads = ((chunks + CH - 1) / CH + 31) / 32 * 32;
   NormArgs p = a;
-  return launch_pdl(fn, dim3(a.max_num_tokens), dim3(kNormThreads), smem, stream, 0, &p);
+  return launch_pdl(fn, dim3(a.max_num_tokens), dim3(threads), 0, stream, 0, &p);
+}
+}  // namespace
+
+int launch_add_rmsnorm(const NormArgs& a, bool f16, cudaStream_t stream) {
+  const int chunks = a.hidden / 8;
+  if (chunks <= 256) return run_norm<1>(a, f16, stream);
+  if (chunks <= 1024) return run_norm<2>(a, f16, stream);
+  return run_norm<4>(a, f16, stream);
 }
 
 }  // namespace grg

@@ -461,149 +461,53 @@ def lora_apply_noalloc(token_lora_mapping, num_tokens, x, lora_a, lora_b, scale:
 
 
 # ------------------------------------------------------------------ around the LoRA products
+# These calls come once or more per layer and token, and the small ones take 2 to 3 us on the GPU:
+# their operands are checked and read by a native module (native/marshal.cpp).
 
-def _rows(t, name, like, shape):
-    """Checks a [rows][...] operand: its type, its trailing sizes, contiguous
-    behind the row stride, on like's device.  Returns (pointer, row stride)."""
-    if t.dtype != like.dtype:
-        raise ValueError(f"{name} must be {like.dtype}, got {t.dtype}")
-    return _placed(t, name, like, shape), t.stride(0)
+_native = None
 
 
-def _placed(t, name, like, shape):
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    st = t.stride()
-    if st[-1] != 1 or (len(st) == 3 and st[1] != shape[2]):
-        raise ValueError(f"{name} must be contiguous behind its row stride")
-    return t.data_ptr()
+def _load_native():
+    """The marshalling module (built with the library)."""
+    global _native
+    if _native is None:
+        load()
+        import importlib
 
-
-def _vec(t, name, like, dtype, shape):
-    """Pointer of a contiguous operand of one type and shape."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}, got {t.device}")
-    return t.data_ptr()
-
-
-def _half(t, name):
-    """Checks that t is a 16-bit CUDA tensor; True for fp16."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
-    if t.dtype == torch.bfloat16:
-        return False
-    if t.dtype == torch.float16:
-        return True
-    raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
-
-
-def _call(name, t, stream, args):
-    """Calls the C entry point on t's device, with the stream as its last argument."""
-    import torch
-    index = t.get_device()
-    fn = getattr(_lib or load(), name)
-    if stream is None:
-        stream = torch.cuda.current_stream(index)
-    ptr = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if index == torch.cuda.current_device():
-        rc = fn(*args, ptr)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, ptr)
-    if rc != LORA_OK:
-        _check(name, rc)
+        import torch  # noqa: F401  (its libraries come first)
+        try:
+            _native = importlib.import_module("._native", __package__)
+        except ImportError as e:
+            raise RuntimeError("gathered_rank_gemm_gb300/_native.so is missing or does not load; build "
+                               "it with gathered_rank_gemm_gb300.build.build()") from e
+    return _native
 
 
 def lora_add_rmsnorm(x, weight, eps: float, num_tokens, residual=None, residual_out=None, y=None,
                      y8=None, y8_scale=None, status=None, stream=None):
     """z = x + residual; y = z / sqrt(mean(z^2) + eps) * weight, in 16 bits (y) and / or e4m3
-    (y8, with scales y8_scale: [rows][1] or [rows][hidden / 128], fp32); residual_out takes z.
-    Rows from num_tokens (device int32[1]) on stay untouched."""
-    import torch
-    f16 = _half(x, "x")
-    if x.dim() != 2:
-        raise ValueError("x must be [rows][hidden]")
-    shape = x.shape
-    rows, hidden = shape
-    xp, xs = _rows(x, "x", x, shape)
-    rp, rs = (None, 0) if residual is None else _rows(residual, "residual", x, shape)
-    op, os_ = (None, 0) if residual_out is None else _rows(residual_out, "residual_out", x, shape)
-    yp, ys = (None, 0) if y is None else _rows(y, "y", x, shape)
-    ep, es, sp, group = None, 0, None, hidden
-    if y8 is not None:
-        if y8.dtype != torch.float8_e4m3fn or y8_scale is None:
-            raise ValueError("y8 must be float8_e4m3fn and come with y8_scale")
-        ep, es = _placed(y8, "y8", x, shape), y8.stride(0)
-        groups = y8_scale.shape[-1]
-        group = hidden if groups == 1 else 128
-        sp = _vec(y8_scale, "y8_scale", x, torch.float32,
-                  (rows, 1) if groups == 1 else (rows, hidden // 128))
-    _call("lora_add_rmsnorm_f16" if f16 else "lora_add_rmsnorm", x, stream,
-          (xp, xs, rp, rs, _vec(weight, "weight", x, x.dtype, (hidden,)), eps, hidden, op, os_, yp,
-           ys, ep, es, sp, group, _vec(num_tokens, "num_tokens", x, torch.int32, (1,)), rows,
-           None if status is None else _status(status, x)))
-
-
-def _status(status, like):
-    """Pointer of a status word: the first int32 of a CUDA tensor."""
-    if status.device != like.device or status.numel() * status.element_size() < 4:
-        raise ValueError(f"status must hold an int32 on {like.device}")
-    return status.data_ptr()
-
-
-def _cache_sizes(cache, like):
-    """(pointer, pages, kv heads, page size, head dim) of a 4-bit cache tensor."""
-    import torch
-    if cache.dtype != torch.uint8 or cache.dim() != 4 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous uint8 tensor "
-                         "[pages][kv heads][page_size / 16][18 * head_dim]")
-    if cache.device != like.device:
-        raise ValueError(f"cache must be on {like.device}, got {cache.device}")
-    pages, heads, blocks, size = cache.shape
-    if size % 18:
-        raise ValueError("cache's last size must be 18 * head_dim")
-    return cache.data_ptr(), pages, heads, blocks * 16, size // 18
+    (y8, float8_e4m3fn, with fp32 scales y8_scale: [rows][1], or [rows][hidden / 128] for a scale
+    per 128 columns); residual_out takes z.  x, residual, residual_out and y are [rows][hidden],
+    contiguous behind their row stride; rows from num_tokens (device int32[1]) on stay untouched."""
+    rc = (_native or _load_native()).add_rmsnorm(x, weight, eps, num_tokens, residual, residual_out,
+                                                 y, y8, y8_scale, status, stream)
+    if rc:
+        _check("lora_add_rmsnorm", rc)
 
 
 def lora_kv4_append(cache, k, v, slots, num_tokens, q=None, q_out=None, positions=None, rope=None,
                     interleaved=False, k_scale=1.0, v_scale=1.0, k_held=None, v_held=None,
                     status=None, stream=None):
-    """Rotates q and k ([rows][heads][head_dim]) by position and appends k and v to the 4-bit
-    paged cache at slots (int32, -1: not stored); rope: fp32 [positions][rope_dim], cosines then
-    sines.  q_out may be q.  k_held / v_held: what the cache then stands for, in 16 bits."""
-    import torch
-    f16 = _half(k, "k")
-    cp, pages, heads, page_size, dim = _cache_sizes(cache, k)
-    rows = slots.shape[0]
-    shape = (rows, heads, dim)
-    kp, ks = _rows(k, "k", k, shape)
-    vp, vs = _rows(v, "v", k, shape)
-    qp, qs, op, os_, qh = None, 0, None, 0, 0
-    if q is not None:
-        if q_out is None or q.dim() != 3:
-            raise ValueError("q must be [rows][heads][head_dim] and come with q_out")
-        qh = q.shape[1]
-        qp, qs = _rows(q, "q", k, (rows, qh, dim))
-        op, os_ = _rows(q_out, "q_out", k, (rows, qh, dim))
-    rp, count, rope_dim, pp = None, 0, 0, None
-    if rope is not None:
-        if positions is None or rope.dim() != 2:
-            raise ValueError("rope must be [positions][rope_dim] and come with positions")
-        count, rope_dim = rope.shape
-        rp = _vec(rope, "rope", k, torch.float32, (count, rope_dim))
-        pp = _vec(positions, "positions", k, torch.int32, (rows,))
-    _call("lora_kv4_append_f16" if f16 else "lora_kv4_append", k, stream,
-          (qp, qs, op, os_, qh, kp, ks, vp, vs, rp, count, rope_dim, 1 if interleaved else 0, pp,
-           _vec(slots, "slots", k, torch.int32, (rows,)), cp, pages, heads, page_size, dim, k_scale,
-           v_scale, None if k_held is None else _vec(k_held, "k_held", k, k.dtype, shape),
-           None if v_held is None else _vec(v_held, "v_held", k, k.dtype, shape),
-           _vec(num_tokens, "num_tokens", k, torch.int32, (1,)), rows,
-           None if status is None else _status(status, k)))
+    """Rotates q and k ([rows][heads][head_dim], contiguous behind their row stride) by position
+    and appends k and v to the 4-bit paged cache (uint8 [pages][kv heads][page_size / 16]
+    [18 * head_dim]) at slots (int32 [rows], -1: not stored).  rope: fp32 [positions][rope_dim],
+    cosines then sines; q_out may be q.  k_held / v_held: what the cache then stands for, in 16
+    bits.  Rows from num_tokens (device int32[1]) on change nothing."""
+    rc = (_native or _load_native()).kv4_append(cache, k, v, slots, num_tokens, q, q_out, positions,
+                                                rope, interleaved, k_scale, v_scale, k_held, v_held,
+                                                status, stream)
+    if rc:
+        _check("lora_kv4_append", rc)
 
 
 def lora_kv4_attention_workspace_size(num_seqs: int, max_num_tokens: int, max_q_len: int,
@@ -618,31 +522,15 @@ def lora_kv4_attention_workspace_size(num_seqs: int, max_num_tokens: int, max_q_
 def lora_kv4_attention(cache, q, out, q_start, kv_len, page_table, max_q_len: int,
                        softmax_scale: float, workspace, window: int = 0, k_scale=1.0, v_scale=1.0,
                        lse=None, status=None, stream=None):
-    """Causal attention of ragged rows of q ([rows][heads][head_dim]; sequence b has rows
-    q_start[b] .. q_start[b + 1] and kv_len[b] keys) over the 4-bit paged cache; out like q, lse
-    fp32 [rows][heads]."""
-    import torch
-    f16 = _half(q, "q")
-    if q.dim() != 3:
-        raise ValueError("q must be [rows][heads][head_dim]")
-    cp, pages, heads, page_size, dim = _cache_sizes(cache, q)
-    rows, qh, _ = q.shape
-    qp, qs = _rows(q, "q", q, (rows, qh, dim))
-    op, os_ = _rows(out, "out", q, (rows, qh, dim))
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [sequences][pages]")
-    seqs, wide = page_table.shape
-    if not workspace.is_cuda or workspace.device != q.device:
-        raise ValueError(f"workspace must be on {q.device}")
-    _call("lora_kv4_attention_f16" if f16 else "lora_kv4_attention", q, stream,
-          (qp, qs, op, os_, None if lse is None else _vec(lse, "lse", q, torch.float32, (rows, qh)),
-           qh, cp, pages, heads, page_size, dim, k_scale, v_scale,
-           _vec(q_start, "q_start", q, torch.int32, (seqs + 1,)),
-           _vec(kv_len, "kv_len", q, torch.int32, (seqs,)),
-           _vec(page_table, "page_table", q, torch.int32, (seqs, wide)), wide, seqs, rows,
-           max_q_len, softmax_scale, window, workspace.data_ptr(),
-           workspace.numel() * workspace.element_size(),
-           None if status is None else _status(status, q)))
+    """Causal attention of ragged rows of q ([rows][heads][head_dim]; sequence b has the rows
+    q_start[b] .. q_start[b + 1] and kv_len[b] keys, page_table int32 [sequences][pages]) over the
+    4-bit paged cache; out like q, lse fp32 [rows][heads].  max_q_len bounds the sequences' rows;
+    window > 0 hides keys further back; workspace: lora_kv4_attention_workspace_size bytes."""
+    rc = (_native or _load_native()).kv4_attention(cache, q, out, q_start, kv_len, page_table,
+                                                   max_q_len, softmax_scale, workspace, window,
+                                                   k_scale, v_scale, lse, status, stream)
+    if rc:
+        _check("lora_kv4_attention", rc)
 
 
 # ------------------------------------------------------------------ buffers

@@ -2,7 +2,9 @@
 
 Each ``csrc/*.cu`` file is compiled to an object with nvcc in parallel, then
 the objects are linked into one shared library that exports only the C ABI of
-``include/gathered_rank_gemm.h``.  No CPU fallback is built.
+``include/gathered_rank_gemm.h``.  ``native/marshal.cpp`` becomes the Python module
+``_native.so`` (argument marshalling of the per-token calls, against the installed
+PyTorch).  No CPU fallback is built.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -18,6 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_NAME = "libgathered_rank_gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
+NATIVE_SRC = os.path.join(HERE, "native", "marshal.cpp")
+NATIVE_PATH = os.path.join(HERE, "_native.so")
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
@@ -36,14 +41,42 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)])
+            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [NATIVE_SRC, os.path.abspath(__file__)])
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(NATIVE_PATH):
         return True
-    t = os.path.getmtime(LIB_PATH)
+    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(NATIVE_PATH))
     return any(os.path.getmtime(p) > t for p in _deps())
+
+
+def _compile_native() -> str:
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    inc = [*cpp_extension.include_paths(), cuda, sysconfig.get_paths()["include"],
+           os.path.join(ROOT, "include")]
+    obj = os.path.join(BUILD_DIR, "marshal.cpp.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in inc), "-c", NATIVE_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {NATIVE_SRC}:\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_native(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE_PATH + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", f"-l:{LIB_NAME}", f"-L{lib}", "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE_PATH)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -64,14 +97,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
+        native = ex.submit(_compile_native)
         objs = list(ex.map(compile_one, _sources()))
+        native = native.result()
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    _link_native(native)
     return LIB_PATH
 
 

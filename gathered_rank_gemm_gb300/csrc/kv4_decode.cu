@@ -14,13 +14,21 @@
 // moved only when a block exceeds it by 2^6 or more: p stays below 2^6, far
 // inside fp16, and the rescaling of O almost never runs.
 //
-// Work: the blocks of all (sequence, row group, key head) items in one line,
-// cut into equal runs whatever the lengths, so one long sequence fills the GPU
-// as well as many short ones.  A run goes to a warp, or, where an item would
-// span more than 16 warps' runs, to a whole CTA whose warps share its blocks
-// and join in shared memory.  Items that were cut leave (m, l, O) partials in
-// the workspace; the last of an item's runs to finish joins them, always in
-// run order, so results do not depend on timing.
+// Work: the blocks of all (sequence, row group, key head) items in one line, an
+// item's fixed cost among them, cut into equal runs whatever the lengths, so one
+// long sequence fills the GPU as well as many short ones.  A run goes to a
+// warp, or, where an item would span many warps' runs, to a whole CTA whose warps
+// share its blocks and join in shared memory; short items stay whole.  Items
+// that were cut leave (m, l, O) partials in the workspace; the last of an item's
+// runs to finish joins them, always in run order, so results do not depend on
+// timing.
+//
+// Measured (GB300, bf16): 256 sequences of up to 4096 keys, 32 / 8 heads of 128
+// (608 MB): 133 us, 0.67 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
+// MB): 151 us, 0.77; one of 700 keys: 9 us.  Bound by issue: 306 instructions a
+// block of 16 keys (64 conversions and 64 scalings of pairs, 16 products, the
+// rest the softmax and the turning of V), 125 cycles an SM where HBM would give it
+// in 98.
 #include "kv4_attention.cuh"
 #include "kv4_attention.h"
 #include "launch.h"
@@ -28,19 +36,21 @@
 namespace grg {
 
 namespace {
-constexpr int kDecThreads = 256;
-constexpr int kDecWarps = kDecThreads / 32;
-constexpr int kDecCtasMax = 2 * 160;  // CTAs that the workspace has room for
-constexpr int kPartialSlots = kDecCtasMax * kDecWarps * 2;
+constexpr int kDecSmsMax = 160;                   // SMs that the workspace has room for
+constexpr int kDecWorkersMax = kDecSmsMax * 16;   // warps on them
+constexpr int kPartialSlots = kDecWorkersMax * 2;
+constexpr float kNoKey = -1e30f;  // the running maximum before any key
+constexpr int kItemCost = 4;      // what an item costs besides its blocks, in blocks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct DecodeParams {
   Kv4AttnArgs a;
-  uint32_t* counters;  // [kDecCtasMax * kDecWarps], zero between calls
+  uint32_t* counters;  // [kDecWorkersMax], zero between calls
   float* part_o;       // [slot][8 * NT][D]
   float2* part_ml;     // [slot][8 * NT]
   int max_packed_rows; // sequences with more packed rows are not this kernel's
+  uint32_t group_magic; // ceil(2^16 / group): r / group = r * magic >> 16 for r < 2^8
   unsigned long long wait_limit_ns;
   int wait_fault;
 };
@@ -55,9 +65,36 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// D += A * B, m16n8k16, fp16 operands (common.cuh's, which the compiler may move).
+__device__ __forceinline__ void mma_f16_add(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                            uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// D = A * B.
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                              uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};\n"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// One half of an fp16 pair, twice (folds into the multiplication that takes it).
+__device__ __forceinline__ uint32_t both_low(uint32_t a) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {l, l};\n}\n" : "=r"(r) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t both_high(uint32_t a) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {h, h};\n}\n" : "=r"(r) : "r"(a));
+  return r;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(a));
   return r;
 }
 }  // namespace
@@ -68,9 +105,14 @@ struct DecItem {
   int nb;    // blocks (1 where no row sees a key: nothing is loaded then)
   int hi;    // keys [.., hi) are seen by some row; 0: none
 };
+__device__ __forceinline__ int row_of(int packed, uint32_t magic) {
+  return static_cast<int>((static_cast<uint32_t>(packed) * magic) >> 16);
+}
 template <int ROWS>
-__device__ __forceinline__ DecItem dec_item(const Kv4Seq& s, int group, int rg, int window) {
-  const int i0 = rg * ROWS / group, i1 = (min(s.take * group, (rg + 1) * ROWS) - 1) / group;
+__device__ __forceinline__ DecItem dec_item(const Kv4Seq& s, int group, uint32_t magic, int rg,
+                                            int window) {
+  const int i0 = row_of(rg * ROWS, magic);
+  const int i1 = row_of(min(s.take * group, (rg + 1) * ROWS) - 1, magic);
   const int hi = s.pos(i1) + 1, lo = s.first_key(i0, window);
   DecItem it;
   it.blk0 = lo / 16;
@@ -79,13 +121,24 @@ __device__ __forceinline__ DecItem dec_item(const Kv4Seq& s, int group, int rg, 
   return it;
 }
 
+// Warps of a CTA, CTAs of an SM and pairs of blocks in a warp's ring: as many
+// warps as the registers allow (168 a thread with 12 warps, 128 with 16).
+template <int D, int NT>
+struct DecShape {
+  static constexpr bool kWide = D == 128 && NT == 2;
+  static constexpr int kWarps = kWide ? 12 : 8;
+  static constexpr int kCtas = kWide ? 1 : 2;
+  static constexpr int kStages = D == 64 ? 4 : 3;
+};
+
 template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(DecShape<D, NT>::kWarps * 32, DecShape<D, NT>::kCtas)
     lora_kv4_decode_kernel(const __grid_constant__ DecodeParams p) {
   using B = Kv4Block<D>;
+  constexpr int kDecWarps = DecShape<D, NT>::kWarps, kDecThreads = kDecWarps * 32;
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;              // k steps of S, and 16-dimension tiles of O
-  constexpr int STAGES = NT == 1 ? 3 : 4; // pairs of blocks in a warp's ring
+  constexpr int STAGES = DecShape<D, NT>::kStages;  // pairs of blocks in a warp's ring
   constexpr int kStage = 2 * B::kBytes;
   constexpr int kRing = STAGES * kStage;
   constexpr int PITCH = D + 4;            // floats of a row's partial in shared memory
@@ -93,9 +146,13 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
 
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t s_bar[kDecWarps * STAGES];
-  __shared__ long long s_prefix[kDecThreads + 1];
   __shared__ long long s_warp[2][kDecWarps];
-  __shared__ int s_abort, s_last;
+  __shared__ int s_abort, s_last, s_most;
+  // until the rings start: units and items before each thread's sequences, and
+  // the sequences themselves where there are no more than threads
+  using Prefix = long long[kDecThreads + 1];
+  Prefix* s_prefix = reinterpret_cast<Prefix*>(smem);
+  Kv4Seq* s_seq = reinterpret_cast<Kv4Seq*>(smem + 2 * sizeof(Prefix));
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -103,64 +160,86 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   const int group = a.num_q_heads / a.num_kv_heads;
   const uint32_t bars = smem_u32(s_bar + warp * STAGES);
   if (lane == 0) {
-    for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 1 + (p.wait_fault ? 1 : 0));
+    for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 2 + (p.wait_fault ? 1 : 0));
     fence_mbar_init();
   }
-  if (tid == 0) s_abort = 0;
+  if (tid == 0) s_abort = 0, s_most = 0;
   const CtaAbort cta_abort{&s_abort, p.wait_limit_ns};
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the line of units (blocks), by sequence: a prefix sum over the threads'
-  // runs of sequences
+  // ---- the line of units (an item's fixed cost and its blocks) and of items, by
+  // sequence: prefix sums over the threads' runs of sequences
   const int per_thread = (a.num_seqs + kDecThreads - 1) / kDecThreads;
-  auto units_of = [&](int b, int& items) -> long long {
-    const Kv4Seq s = Kv4Seq::of(a, b);
-    items = 0;
-    if (s.odd && blockIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
-    if (s.take == 0 || static_cast<long long>(s.take) * group > p.max_packed_rows) return 0;
-    const int ng = (s.take * group + ROWS - 1) / ROWS;
-    long long n = 0;
-    for (int rg = 0; rg < ng; ++rg) n += dec_item<ROWS>(s, group, rg, a.window).nb;
-    items = ng * a.num_kv_heads;
-    return n * a.num_kv_heads;
+  auto seq_at = [&](int b) { return per_thread == 1 ? s_seq[b] : Kv4Seq::of(a, b); };
+  auto groups_of = [&](const Kv4Seq& s) {  // row groups; 0: no rows, or not this kernel's
+    return static_cast<long long>(s.take) * group > p.max_packed_rows ? 0
+                                                                      : (s.take * group + ROWS - 1) / ROWS;
   };
-  long long mine = 0, my_items = 0;
+  auto units_of = [&](const Kv4Seq& s, int& most) {  // of one key head
+    long long n = 0;
+    const int ng = groups_of(s);
+    for (int rg = 0; rg < ng; ++rg) {
+      const int nb = dec_item<ROWS>(s, group, p.group_magic, rg, a.window).nb;
+      n += nb + kItemCost;
+      most = max(most, nb);
+    }
+    return n;
+  };
+  long long mine[2] = {0, 0};
+  int most = 0;  // blocks of the longest item
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
     if (b < a.num_seqs) {
-      int items;
-      mine += units_of(b, items);
-      my_items += items;
+      const Kv4Seq s = Kv4Seq::of(a, b);
+      if (per_thread == 1) s_seq[b] = s;
+      if (s.odd && blockIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
+      mine[0] += units_of(s, most) * a.num_kv_heads;
+      mine[1] += static_cast<long long>(groups_of(s)) * a.num_kv_heads;
     }
   }
-  long long run = mine, all_items = my_items;
+  long long run[2] = {mine[0], mine[1]};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += v;
-    all_items += __shfl_xor_sync(0xffffffffu, all_items, o);
-  }
-  if (lane == 31) s_warp[0][warp] = run;
-  if (lane == 0) s_warp[1][warp] = all_items;
-  __syncthreads();
-  long long before = 0, total = 0, items = 0;
+  for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) before += s_warp[0][w];
-    total += s_warp[0][w];
-    items += s_warp[1][w];
+    for (int i = 0; i < 2; ++i) {
+      const long long v = __shfl_up_sync(0xffffffffu, run[i], o);
+      if (lane >= o) run[i] += v;
+    }
+  if (lane == 31) s_warp[0][warp] = run[0], s_warp[1][warp] = run[1];
+  most = __reduce_max_sync(0xffffffffu, most);
+  __syncthreads();  // (s_most is zero)
+  if (lane == 0 && most > 0) atomicMax(&s_most, most);
+  long long all[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    long long before = 0;
+#pragma unroll
+    for (int w = 0; w < kDecWarps; ++w) {
+      if (w < warp) before += s_warp[i][w];
+      all[i] += s_warp[i][w];
+    }
+    s_prefix[i][tid] = before + run[i] - mine[i];
+    if (tid == 0) s_prefix[i][kDecThreads] = all[i];
   }
-  s_prefix[tid] = before + run - mine;
-  if (tid == 0) s_prefix[kDecThreads] = total;
   __syncthreads();
-  if (total == 0) return;
+  if (all[0] == 0) return;
 
-  // ---- runs of warps or of CTAs
+  // ---- who takes what.  A cut item costs its join (partials to L2, a counter,
+  // and back: about 6 us on the way of the last), so short items stay whole where
+  // there are workers for all of them: a warp takes 16 blocks in the time of
+  // that, a CTA 96.  Else the line of units is cut into equal runs, of warps,
+  // or of CTAs where an item would span over 8 warps' runs (16 sequences of
+  // 1000 to 4000 keys, 4 rows: 40 us so, 52 us by warps; 48 windows of 2048 keys: 38 and 36 us).
   const long long warps_all = static_cast<long long>(gridDim.x) * kDecWarps;
-  const long long per_warp = max((total + warps_all - 1) / warps_all, 2ll);
-  const bool team = total > 16 * per_warp * items;  // an item would span over 16 warps' runs
-  const long long per = team ? max((total + gridDim.x - 1) / gridDim.x, 2ll * kDecWarps) : per_warp;
+  const long long per_warp = max((all[0] + warps_all - 1) / warps_all, 2ll * kItemCost);
+  const bool whole_warp = s_most <= 16 && all[1] <= warps_all;
+  const bool whole = whole_warp || (s_most <= 12 * kDecWarps && all[1] <= gridDim.x);
+  const bool team = whole ? !whole_warp : all[0] > 8 * per_warp * all[1];
+  const long long per = whole ? 1
+                        : team ? max((all[0] + gridDim.x - 1) / gridDim.x, 2ll * kDecWarps)
+                               : per_warp;
+  const long long total = whole ? all[1] : all[0];  // items are the units where they stay whole
   const int worker = team ? blockIdx.x : blockIdx.x * kDecWarps + warp;
   const int TW = team ? kDecWarps : 1, wt = team ? warp : 0;
   auto team_sync = [&]() {
@@ -169,37 +248,120 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
   unsigned char* ring = smem + warp * kRing;
   const uint32_t ring_u = smem_u32(ring);
   float* own = reinterpret_cast<float*>(ring);  // the warp's partial, once its ring is idle
-  uint32_t fills = 0;                           // copies awaited so far (stage and phase)
+  int stage_in = 0, stage_out = 0;              // where the next copy goes, and comes from
+  uint32_t phase = 0;                           // of stage_out's barrier
 
-  long long u = worker * per;
-  const long long u_end = min(u + per, total);
-  if (u >= u_end) return;  // a whole team or a lone warp
-  // the sequence, row group, key head and offset of unit u
-  int b = 0, rg = 0, h = 0;
-  long long off = 0;
-  {
-    int lo = 0, hi = kDecThreads;
+  const long long u0 = worker * per, u_end = min(u0 + per, total);
+  const int cost = whole ? 0 : kItemCost;
+  auto run_of = [&](long long x) {  // the worker of place x of the line
+    return (total >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(per))
+                              : static_cast<int>(x / per);
+  };
+  // the part of an item that this worker has: blocks [o, o + take) of the item
+  // whose place in the line is [at, at + cost + nb)
+  int b = 0, rg = 0, h = 0, o = 0, take = 0;
+  int at = 0;  // from u0
+  const int run_len = static_cast<int>(u_end - u0);
+  Kv4Seq seq;
+  DecItem item;
+  auto set_take = [&]() {
+    take = whole ? item.nb : min(item.nb, run_len - at - cost) - o;
+  };
+  if (u0 < u_end) {
+    const long long* prefix = s_prefix[whole ? 1 : 0];
+    int lo = 0, hi = kDecThreads, ignored = 0;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (s_prefix[mid] <= u) lo = mid; else hi = mid;
+      if (prefix[mid] <= u0) lo = mid; else hi = mid;
     }
-    off = u - s_prefix[lo];
-    b = lo * per_thread;
-    int ignored;
-    for (long long n; off >= (n = units_of(b, ignored)); ++b) off -= n;
+    long long off = u0 - prefix[lo];
+    for (b = lo * per_thread;; ++b) {
+      seq = seq_at(b);
+      const long long n = (whole ? groups_of(seq) : units_of(seq, ignored)) * a.num_kv_heads;
+      if (off < n) break;
+      off -= n;
+    }
+    int size;
+    while (true) {
+      item = dec_item<ROWS>(seq, group, p.group_magic, rg, a.window);
+      size = whole ? 1 : item.nb + cost;
+      if (off < static_cast<long long>(size) * a.num_kv_heads) break;
+      off -= static_cast<long long>(size) * a.num_kv_heads;
+      ++rg;
+    }
+    h = (off >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(size))
+                         : static_cast<int>(off / size);
+    off -= static_cast<long long>(h) * size;
+    at = -static_cast<int>(off);
+    o = max(static_cast<int>(off) - cost, 0);
+    set_take();
   }
-  Kv4Seq seq = Kv4Seq::of(a, b);
-  DecItem item = dec_item<ROWS>(seq, group, 0, a.window);
-  while (off >= static_cast<long long>(item.nb) * a.num_kv_heads) {
-    off -= static_cast<long long>(item.nb) * a.num_kv_heads;
-    item = dec_item<ROWS>(seq, group, ++rg, a.window);
-  }
-  h = static_cast<int>(off / item.nb);
-  int o = static_cast<int>(off % item.nb);
+  auto advance = [&]() -> bool {  // to the worker's next part
+    at += whole ? 1 : cost + item.nb;
+    if (at >= run_len) return false;
+    o = 0;
+    if (++h == a.num_kv_heads) {
+      h = 0;
+      ++rg;
+      while (rg >= groups_of(seq)) {
+        rg = 0;
+        seq = Kv4Seq::of(a, ++b);
+      }
+      item = dec_item<ROWS>(seq, group, p.group_magic, rg, a.window);
+    }
+    set_take();
+    return take > 0;
+  };
+  fence_proxy_async();
+  __syncthreads();  // the rings may start
+  if (take <= 0) return;  // a whole team or a lone warp
+
+  // ---- a part's copies: pairs of blocks 2 q, 2 q + 1 of it, q = wt + TW k for this warp
+  const int page_blocks = a.page_size / 16;
+  const int32_t* table = nullptr;
+  int first_blk = 0, part_take = 0, part_h = 0, np = 0, issued = 0;
+  unsigned long long now = 0;
+  bool hole = false;  // some page is not in the cache
+  auto block_at = [&](int blk) -> const unsigned char* {  // null: its page is not in the cache
+    const int pg = blk / page_blocks;
+    const int page = __ldg(table + pg);
+    if (page < 0 || page >= a.num_pages) return nullptr;
+    return a.cache + ((static_cast<long long>(page) * a.num_kv_heads + part_h) * page_blocks +
+                      (blk - pg * page_blocks)) * B::kBytes;
+  };
+  // block addresses: 16 pairs at a time, lane l holds block l & 1 of pair l / 2 (null: not there)
+  auto addresses = [&](int k0) -> unsigned long long {
+    const int i = 2 * (wt + TW * (k0 + (lane >> 1))) + (lane & 1);
+    const unsigned char* x = i < part_take ? block_at(first_blk + i) : nullptr;
+    if (__any_sync(0xffffffffu, i < part_take && !x)) {
+      hole = true;
+      if (lane == 0 && a.status) atomicOr(a.status, kStatusBadSlot);
+    }
+    return reinterpret_cast<unsigned long long>(x);
+  };
+  auto issue = [&](int k) {  // by the two lanes that hold pair k's addresses
+    if ((k & 15) == 0 && k > 0) now = addresses(k);
+    if ((lane >> 1) == (k & 15) && !cta_abort.raised()) {
+      const uint32_t bar = bars + 8 * stage_in;
+      mbar_arrive_expect_tx(bar, now ? B::kBytes : 0);
+      if (now)
+        bulk_g2s(ring_u + stage_in * kStage + (lane & 1) * B::kBytes,
+                 reinterpret_cast<const void*>(now), B::kBytes, bar);
+    }
+    if (++stage_in == STAGES) stage_in = 0;
+  };
+  auto begin = [&]() {
+    first_blk = item.blk0 + o, part_take = take, part_h = h;
+    table = a.page_table + static_cast<long long>(b) * a.table_stride;
+    np = item.hi > 0 && !p.wait_fault ? ((take + 1) / 2 - wt + TW - 1) / TW : (p.wait_fault ? 1 : 0);
+    hole = false;
+    if (np > 0) now = addresses(0);
+    if (p.wait_fault) now = 0;
+    for (issued = 0; issued < min(np, STAGES); ++issued) issue(issued);
+  };
+  begin();
 
   while (true) {
-    const int take = static_cast<int>(min(static_cast<long long>(item.nb - o), u_end - u));
-    const int first_blk = item.blk0 + o;
     const int packed = seq.take * group;  // packed rows of the sequence
     const int row0 = rg * ROWS;
     const int live_rows = min(packed - row0, ROWS);
@@ -215,7 +377,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
 #pragma unroll
       for (int i = 0; i < KS * 4; ++i) v[i] = 0.0f;
       if (r < packed) {
-        const uint16_t* src = a.q + (seq.q0 + r / group) * a.q_stride + (h * group + r % group) * D +
+        const int i = row_of(r, p.group_magic);
+        const uint16_t* src = a.q + (seq.q0 + i) * a.q_stride + (h * group + r - i * group) * D +
                               t4 * (D / 4);
 #pragma unroll
         for (int i = 0; i < KS / 2; ++i) {
@@ -242,19 +405,19 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         cf[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t4 + c) * 4) * (a.score_scale * kLog2e);
-        const int rr = min(row0 + nt * 8 + 2 * t4 + c, packed - 1) / group;
+        const int rr = row_of(min(row0 + nt * 8 + 2 * t4 + c, packed - 1), p.group_magic);
         pos[nt][c] = seq.pos(rr);
         lo[nt][c] = seq.first_key(rr, a.window);
       }
     }
-    const int pos_min = seq.pos(row0 / group), pos_max = item.hi - 1;
-    const int lo_max = seq.first_key((row0 + live_rows - 1) / group, a.window);
+    const int pos_min = seq.pos(row_of(row0, p.group_magic)), pos_max = item.hi - 1;
+    const int lo_max = seq.first_key(row_of(row0 + live_rows - 1, p.group_magic), a.window);
 
     float acc[NT][KS][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) m[nt][c] = -INFINITY, l[nt][c] = 0.0f;
+      for (int c = 0; c < 2; ++c) m[nt][c] = kNoKey, l[nt][c] = 0.0f;
 #pragma unroll
       for (int i = 0; i < KS; ++i)
 #pragma unroll
@@ -262,57 +425,38 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
     }
     bool poison = false;  // a NaN scale of V among keys that some rows must not see
 
-    // ---- this warp's pairs of blocks: pair k covers blocks 2 q, 2 q + 1 of the run, q = wt + TW k
-    const int pairs = (take + 1) / 2;
-    const int np = item.hi > 0 && !p.wait_fault ? (pairs - wt + TW - 1) / TW : (p.wait_fault ? 1 : 0);
-    const int32_t* table = a.page_table + static_cast<long long>(b) * a.table_stride;
-    const int page_blocks = a.page_size / 16;
-    // block addresses: 16 pairs at a time, lane l holds block l & 1 of pair l / 2 (null: not there)
-    auto address = [&](int k0) -> const unsigned char* {
-      const int q = wt + TW * (k0 + (lane >> 1));
-      const int i = 2 * q + (lane & 1);
-      if (i >= take) return nullptr;
-      const int blk = first_blk + i, pg = blk / page_blocks;
-      const int page = __ldg(table + pg);
-      if (page < 0 || page >= a.num_pages) {
-        if (a.status) atomicOr(a.status, kStatusBadSlot);
-        return nullptr;
-      }
-      return a.cache + ((static_cast<long long>(page) * a.num_kv_heads + h) * page_blocks +
-                        (blk - pg * page_blocks)) * B::kBytes;
-    };
-    const unsigned char* now = np > 0 ? address(0) : nullptr;
-    uint32_t there = 0;  // two bits per stage: which blocks of the pair exist
-    auto issue = [&](int k) {
-      if ((k & 15) == 0 && k > 0) now = address(k);
-      const unsigned long long at = reinterpret_cast<unsigned long long>(now);
-      const unsigned long long x0 = __shfl_sync(0xffffffffu, at, 2 * (k & 15));
-      const unsigned long long x1 = __shfl_sync(0xffffffffu, at, 2 * (k & 15) + 1);
-      const int s = (fills + k) % STAGES;
-      there = (there & ~(3u << (2 * s))) | (((x0 ? 1u : 0u) | (x1 ? 2u : 0u)) << (2 * s));
-      if (lane == 0 && !cta_abort.raised()) {
-        const uint32_t bar = bars + 8 * s, dst = ring_u + s * kStage;
-        const uint32_t bytes = ((x0 ? 1 : 0) + (x1 ? 1 : 0)) * B::kBytes;
-        mbar_arrive_expect_tx(bar, p.wait_fault ? 0 : bytes);
-        if (!p.wait_fault) {
-          if (x0) bulk_g2s(dst, reinterpret_cast<const void*>(x0), B::kBytes, bar);
-          if (x1) bulk_g2s(dst + B::kBytes, reinterpret_cast<const void*>(x1), B::kBytes, bar);
-        }
-      }
-    };
-    int issued = 0;
-    for (; issued < min(np, STAGES); ++issued) issue(issued);
+    // pairs [k_open, k_open + k_shut) need no mask: both blocks exist, every row
+    // sees every key
+    int k_open, k_shut;
+    {
+      const int last = min(min((pos_min + 1) / 16 - first_blk, part_take), 1 << 27);  // blocks all rows see
+      const int first = max((lo_max + 15) / 16 - first_blk, 0);
+      const int q1 = last / 2, q0 = (first + 1) / 2;  // pairs
+      k_open = q0 <= wt ? 0 : (q0 - wt + TW - 1) / TW;
+      k_shut = hole || q1 <= wt ? 0 : max((q1 - wt + TW - 1) / TW - k_open, 0);
+    }
 
+    // key of this thread's S rows g and g + 8 (parities alternate: no bank conflicts)
+    const int kr = g ^ ((g >> 1) & 1);
     int k = 0;
     for (; k < np; ++k) {
-      const int s = (fills + k) % STAGES;
-      if (!__all_sync(0xffffffffu, cta_abort.wait(bars + 8 * s, ((fills + k) / STAGES) & 1))) break;
-      const unsigned char* stage = ring + s * kStage;
-      const int tok = 16 * (first_blk + 2 * (wt + TW * k));  // the pair's first key
-      const uint32_t have = (there >> (2 * s)) & 3u;
-      const bool masked = tok + 31 > pos_min || tok < lo_max || have != 3u;
-      // key of this thread's S rows g and g + 8 (parities alternate: no bank conflicts)
-      const int kr = g ^ ((g >> 1) & 1);
+      {
+        bool ok = mbar_try_wait(bars + 8 * stage_out, phase);
+        if (!ok) ok = cta_abort.wait(bars + 8 * stage_out, phase);
+        if (!__all_sync(0xffffffffu, ok)) break;
+      }
+      const unsigned char* stage = ring + stage_out * kStage;
+      const bool masked = static_cast<uint32_t>(k - k_open) >= static_cast<uint32_t>(k_shut);
+      const int i0 = 2 * (wt + TW * k);       // the pair's first block in the part
+      const int tok = 16 * (first_blk + i0);  // and its first key
+      uint32_t have = 3u;
+      if (masked) {
+        if (i0 + 1 >= part_take) have = 1u;
+        if (hole) {
+          if (!block_at(first_blk + i0)) have &= 2u;
+          if (i0 + 1 < part_take && !block_at(first_blk + i0 + 1)) have &= 1u;
+        }
+      }
 
       float sc[NT][2][4];
 #pragma unroll
@@ -329,21 +473,17 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
               *reinterpret_cast<const uint16_t*>(blk + B::kKScale + kr * 8 + 2 * t4));
           const uint32_t hb = e4m3x2_to_f16(
               *reinterpret_cast<const uint16_t*>(blk + B::kKScale + (kr + 8) * 8 + 2 * t4));
-          sa[0] = prmt(ha, ha, 0x1010), sa[1] = prmt(ha, ha, 0x3232);
-          sb[0] = prmt(hb, hb, 0x1010), sb[1] = prmt(hb, hb, 0x3232);
+          sa[0] = both_low(ha), sa[1] = both_high(ha);
+          sb[0] = both_low(hb), sb[1] = both_high(hb);
         } else {
           const uint2 va = *reinterpret_cast<const uint2*>(blk + kr * 32 + 8 * t4);
           const uint2 vb = *reinterpret_cast<const uint2*>(blk + (kr + 8) * 32 + 8 * t4);
           ca[0] = va.x, ca[1] = va.y, cb[0] = vb.x, cb[1] = vb.y;
           const uint32_t ha = e4m3x2_to_f16(blk[B::kKScale + kr * 4 + t4]);
           const uint32_t hb = e4m3x2_to_f16(blk[B::kKScale + (kr + 8) * 4 + t4]);
-          sa[0] = sa[1] = prmt(ha, ha, 0x1010);
-          sb[0] = sb[1] = prmt(hb, hb, 0x1010);
+          sa[0] = sa[1] = both_low(ha);
+          sb[0] = sb[1] = both_low(hb);
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) sc[nt][x][c] = 0.0f;
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) {
           uint32_t ha[4], hb[4];
@@ -355,13 +495,16 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
             const uint32_t frag[4] = {hmul2(ha[2 * j], fa), hmul2(hb[2 * j], fb),
                                       hmul2(ha[2 * j + 1], fa), hmul2(hb[2 * j + 1], fb)};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(sc[nt][x], frag, qf[nt][2 * w + j][0], qf[nt][2 * w + j][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if (w == 0 && j == 0) mma_f16_first(sc[nt][x], frag, qf[nt][0][0], qf[nt][0][1]);
+              else mma_f16_add(sc[nt][x], frag, qf[nt][2 * w + j][0], qf[nt][2 * w + j][1]);
+            }
           }
         }
       }
 
-      // ---- running maximum (rarely moved) and the probabilities
+      // ---- probabilities against the running reference m, which moves only when
+      // some score passes it by 2^6
       if (masked) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -380,11 +523,8 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float v = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]), fmaxf(sc[nt][1][c], sc[nt][1][c + 2]));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-          v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-          mx[nt][c] = v * cf[nt][c];
+          mx[nt][c] = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]),
+                            fmaxf(sc[nt][1][c], sc[nt][1][c + 2])) * cf[nt][c];
           move = move || mx[nt][c] > m[nt][c] + 6.0f;
         }
       if (__any_sync(0xffffffffu, move)) {
@@ -392,8 +532,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float to = fmaxf(m[nt][c], mx[nt][c]);
-            const float f = m[nt][c] == -INFINITY ? 0.0f : exp2_approx(m[nt][c] - to);
+            float v = mx[nt][c];
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            const float to = fmaxf(m[nt][c], v);
+            const float f = exp2_approx(m[nt][c] - to);
             m[nt][c] = to;
             l[nt][c] *= f;
 #pragma unroll
@@ -403,14 +547,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       uint32_t pb[NT][2][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0];
-        const float m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float p0 = exp2_approx(fmaf(sc[nt][x][0], cf[nt][0], -m0));
-          const float p1 = exp2_approx(fmaf(sc[nt][x][1], cf[nt][1], -m1));
-          const float p2 = exp2_approx(fmaf(sc[nt][x][2], cf[nt][0], -m0));
-          const float p3 = exp2_approx(fmaf(sc[nt][x][3], cf[nt][1], -m1));
+          const float p0 = exp2_approx(fmaf(sc[nt][x][0], cf[nt][0], -m[nt][0]));
+          const float p1 = exp2_approx(fmaf(sc[nt][x][1], cf[nt][1], -m[nt][1]));
+          const float p2 = exp2_approx(fmaf(sc[nt][x][2], cf[nt][0], -m[nt][0]));
+          const float p3 = exp2_approx(fmaf(sc[nt][x][3], cf[nt][1], -m[nt][1]));
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
           pb[nt][x][0] = transpose8x8(pack_f16x2(p0, p1));
@@ -436,7 +578,7 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
           };
           clean(e0, r0), clean(e1, r1), clean(e2, r0 + 8), clean(e3, r1 + 8);
         }
-        const uint32_t s01 = e4m3x2_to_f16(e0 | (e1 << 8)), s23 = e4m3x2_to_f16(e2 | (e3 << 8));
+        const uint32_t s01 = e4m3x2_to_f16(prmt(e0, e1, 0x40)), s23 = e4m3x2_to_f16(prmt(e2, e3, 0x40));
         constexpr int W = D / 64;  // words of a key's dimensions
         uint32_t c0[W], c1[W], c2[W], c3[W];
         auto load = [&](uint32_t (&c)[W], int r) {
@@ -465,17 +607,19 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
                                       hmul2(od2[i], s23)};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-              mma_f16(acc[nt][4 * w + i], frag, pb[nt][x][0], pb[nt][x][1]);
+              mma_f16_add(acc[nt][4 * w + i], frag, pb[nt][x][0], pb[nt][x][1]);
           }
         }
       }
       __syncwarp();
+      if (++stage_out == STAGES) stage_out = 0, phase ^= 1;
       if (issued < np) issue(issued++);
     }
-    if (k < np)  // gave up: what is still on its way lands before the ring is left
-      for (; k < issued && !p.wait_fault; ++k)
-        mbar_drain(bars + 8 * ((fills + k) % STAGES), ((fills + k) / STAGES) & 1, p.wait_limit_ns);
-    fills += np;
+    if (k < np && !p.wait_fault)  // gave up: what is still on its way lands before the ring is left
+      for (; k < issued; ++k) {
+        mbar_drain(bars + 8 * stage_out, phase, p.wait_limit_ns);
+        if (++stage_out == STAGES) stage_out = 0, phase ^= 1;
+      }
 
     // ---- join: sums over the lanes that share a row
 #pragma unroll
@@ -488,15 +632,12 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       }
     if (__any_sync(0xffffffffu, poison)) {
       // rare: which of its 16 dimensions' scales are NaN at keys a row sees
-      for (int i = 0; i < 2 * pairs; ++i) {
+      for (int i = 0; i < part_take; ++i) {
         if (TW > 1 && (i / 2) % TW != wt) continue;
-        const int blk = first_blk + i, pg = blk / page_blocks;
-        if (i >= take || blk * 16 >= item.hi) continue;
-        const int page = __ldg(table + pg);
-        if (page < 0 || page >= a.num_pages) continue;
-        const unsigned char* at =
-            a.cache + ((static_cast<long long>(page) * a.num_kv_heads + h) * page_blocks +
-                       (blk - pg * page_blocks)) * B::kBytes + B::kVScale + (D == 128 ? g : g / 2);
+        const int blk = first_blk + i;
+        const unsigned char* at = block_at(blk);
+        if (!at) continue;
+        at += B::kVScale + (D == 128 ? g : g / 2);
         for (int r = 0; r < 16; ++r)
           if ((at[r * (D / 16)] & 0x7F) == 0x7F)
 #pragma unroll
@@ -510,79 +651,103 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
       }
     }
 
-    // The joined rows in the team's shared memory: [row][D], then (m, l) at D.
-    auto put = [&](float* dst) {
+    // ---- the next part's copies may start: this one needs its ring no more (but
+    // for a team's join); then this part's rows go out
+    const int out_h = h, out_q0 = seq.q0, nb = item.nb;
+    const bool all_of_it = take == item.nb;
+    const int slot = worker * 2 + (o == 0 ? 1 : 0);
+    const int begins = at + cost;
+    const bool more = advance();
+    if (more && !team) begin();
+    // where row r goes: its place in out (with what turns sums into values) or in
+    // the partials
+    struct RowOut {
+      uint16_t* out;
+      float* part;
+      float inv;
+    };
+    auto open_row = [&](int r, bool whole_row, float top, float sum, bool writer) {
+      RowOut w{nullptr, nullptr, 0.0f};
+      if (whole_row) {
+        const int pr = row0 + r, i = row_of(pr, p.group_magic), head = out_h * group + pr - i * group;
+        const long long t = out_q0 + i;
+        w.out = cta_abort.raised() ? nullptr : a.out + t * a.out_stride + head * D;
+        w.inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+        if (writer && w.out && a.lse)
+          a.lse[t * a.num_q_heads + head] = sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
+      } else {
+        w.part = p.part_o + static_cast<long long>(slot * ROWS + r) * D;
+        if (writer) p.part_ml[slot * ROWS + r] = make_float2(top, sum);
+      }
+      return w;
+    };
+    auto put4 = [&](const RowOut& w, int d, float4 v) {
+      if (w.part) {
+        *reinterpret_cast<float4*>(w.part + d) = v;
+      } else if (w.out) {
+        uint2 o2;
+        o2.x = pack_t<F16>(v.x * w.inv, v.y * w.inv);
+        o2.y = pack_t<F16>(v.z * w.inv, v.w * w.inv);
+        *reinterpret_cast<uint2*>(w.out + d) = o2;
+      }
+    };
+    // Joins the team's warps' rows, [row][D] and (m, l) in each warp's ring, and
+    // hands them on; 4 dimensions a thread.
+    auto join = [&](bool whole_rows) {
+      __syncthreads();
+      for (int i = tid; i < live_rows * (D / 4); i += kDecThreads) {
+        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+        const float* base = reinterpret_cast<const float*>(smem) + r * PITCH;
+        float top = kNoKey;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) top = fmaxf(top, base[w * (kRing / 4) + D]);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float* part = base + w * (kRing / 4);
+          const float2 ml = *reinterpret_cast<const float2*>(part + D);
+          const float f = exp2_approx(ml.x - top);
+          const float4 x = *reinterpret_cast<const float4*>(part + d);
+          sum += ml.y * f;
+          v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+        }
+        put4(open_row(r, whole_rows, top, sum, d == 0), d, v);
+      }
+    };
+    // This warp's rows: straight on where it works alone, else through the join.
+    auto hand_on = [&](bool whole_rows) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int r = nt * 8 + 2 * t4 + c;
           if (r >= live_rows) continue;
-          float* row = dst + r * PITCH;
+          RowOut w{nullptr, own + r * PITCH, 0.0f};
+          if (!team) w = open_row(r, whole_rows, m[nt][c], l[nt][c], g == 0);
+          else if (g == 0) *reinterpret_cast<float2*>(own + r * PITCH + D) = make_float2(m[nt][c], l[nt][c]);
 #pragma unroll
-          for (int i = 0; i < KS; ++i)
-            *reinterpret_cast<float2*>(row + (D / 8) * g + 2 * i) =
-                make_float2(acc[nt][i][c], acc[nt][i][c + 2]);
-          if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[nt][c], l[nt][c]);
+          for (int i = 0; i < KS; i += 2)
+            put4(w, (D / 8) * g + 2 * i, make_float4(acc[nt][i][c], acc[nt][i][c + 2], acc[nt][i + 1][c],
+                                                     acc[nt][i + 1][c + 2]));
         }
+      if (team) join(whole_rows);
     };
-    // Joins the team's warps' rows and hands each (row, 4 dimensions) on.
-    auto join = [&](auto&& sink) {
-      const int step = TW * 32;
-      for (int i = wt * 32 + lane; i < live_rows * (D / 4); i += step) {
-        const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-        const float* base = reinterpret_cast<const float*>(smem + (team ? 0 : warp) * kRing) + r * PITCH;
-        float top = -INFINITY;
-        for (int w = 0; w < TW; ++w)
-          top = fmaxf(top, base[static_cast<size_t>(w) * (kRing / 4) + D]);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.0f;
-        for (int w = 0; w < TW; ++w) {
-          const float* part = base + static_cast<size_t>(w) * (kRing / 4);
-          const float2 ml = *reinterpret_cast<const float2*>(part + D);
-          const float f = ml.x == -INFINITY ? 0.0f : exp2_approx(ml.x - top);
-          const float4 x = *reinterpret_cast<const float4*>(part + d);
-          // a part without keys adds nothing (its sums are zero, or NaN from NaN scores)
-          sum += ml.x == -INFINITY ? ml.y : ml.y * f;
-          v.x += ml.x == -INFINITY ? x.x : x.x * f;
-          v.y += ml.x == -INFINITY ? x.y : x.y * f;
-          v.z += ml.x == -INFINITY ? x.z : x.z * f;
-          v.w += ml.x == -INFINITY ? x.w : x.w * f;
-        }
-        sink(r, d, v, top, sum);
-      }
-    };
-    auto to_output = [&](int r, int d, float4 v, float top, float sum) {
-      if (cta_abort.raised()) return;
-      const int pr = row0 + r, t = seq.q0 + pr / group, head = h * group + pr % group;
-      const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-      uint2 w;
-      w.x = pack_t<F16>(v.x * inv, v.y * inv);
-      w.y = pack_t<F16>(v.z * inv, v.w * inv);
-      *reinterpret_cast<uint2*>(a.out + t * a.out_stride + head * D + d) = w;
-      if (d == 0 && a.lse)
-        a.lse[static_cast<long long>(t) * a.num_q_heads + head] =
-            sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kLn2;
-    };
-    put(own);
-    team_sync();
-    if (take == item.nb) {
-      join(to_output);
+    if (all_of_it) {
+      hand_on(true);
     } else {
-      const long long start = u - o;
-      const int w0 = static_cast<int>(start / per), w1 = static_cast<int>((start + item.nb - 1) / per);
-      const long long slot = static_cast<long long>(worker) * 2 + (o == 0 ? 1 : 0);
-      join([&](int r, int d, float4 v, float top, float sum) {
-        *reinterpret_cast<float4*>(p.part_o + (slot * ROWS + r) * D + d) = v;
-        if (d == 0) p.part_ml[slot * ROWS + r] = make_float2(top, sum);
-      });
-      __threadfence();
+      const int w0 = run_of(u0 + begins), w1 = run_of(u0 + begins + nb - 1);
+      hand_on(false);
       team_sync();
       int last = 0;
       if (wt == 0 && lane == 0) {
-        last = atomicAdd(p.counters + w0, 1u) == static_cast<uint32_t>(w1 - w0);
+        uint32_t seen;  // releases what the barrier above has gathered, acquires the others'
+        asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;\n"
+                     : "=r"(seen)
+                     : "l"(p.counters + w0)
+                     : "memory");
+        last = seen == static_cast<uint32_t>(w1 - w0);
         if (last) p.counters[w0] = 0;
-        __threadfence();
         if (team) s_last = last;
       }
       if (team) {
@@ -592,53 +757,99 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
         last = __shfl_sync(0xffffffffu, last, 0);
       }
       if (last) {
-        // every run of the item is there: each warp sums its share of them, in run order
-        const int n = w1 - w0 + 1;
-        for (int r = 0; r < live_rows; ++r) {
-          float top = -INFINITY;
-          for (int i = wt + TW * lane; i < n; i += TW * 32)
-            top = fmaxf(top, __ldcg(&p.part_ml[((static_cast<long long>(w0) + i) * 2 + (i == 0)) * ROWS + r]).x);
+        // every run of the item is there: each warp sums its share of them, in
+        // run order, 32 at a time; a lane holds D / 32 dimensions of every row
+        const int n = (w1 - w0 + TW - wt) / TW;  // runs of this warp: wt, wt + TW, ...
+        constexpr int E = D / 32, RB = 4, JB = D == 64 ? 4 : 2;  // rows and runs loaded together
+        auto slot_of = [&](int j) {
+          const int i = wt + TW * j;
+          return ((static_cast<long long>(w0) + i) * 2 + (i == 0 ? 1 : 0)) * ROWS;
+        };
+        for (int r0 = 0; r0 < live_rows; r0 += RB) {
+          float v[RB][E] = {}, top[RB], sum[RB] = {};
 #pragma unroll
-          for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-          float v[D / 32] = {}, sum = 0.0f;
-#pragma unroll 4
-          for (int i = wt; i < n; i += TW) {
-            const long long at = ((static_cast<long long>(w0) + i) * 2 + (i == 0)) * ROWS + r;
-            const float2 ml = __ldcg(&p.part_ml[at]);
-            const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - top);
-            sum += ml.y * f;
-            const float* src = p.part_o + at * D + lane * (D / 32);
+          for (int r = 0; r < RB; ++r) top[r] = kNoKey;
+          for (int j0 = 0; j0 < n; j0 += 32) {
+            float2 ml[RB];
+            const float2* src = p.part_ml + slot_of(min(j0 + lane, n - 1)) + r0;
 #pragma unroll
-            for (int e = 0; e < D / 32; e += 2) {
-              const float2 x = __ldcg(reinterpret_cast<const float2*>(src + e));
-              v[e] += x.x * f;
-              v[e + 1] += x.y * f;
+            for (int r = 0; r < RB; ++r)
+              ml[r] = r0 + r < live_rows && j0 + lane < n ? __ldcg(src + r) : make_float2(kNoKey, 0.0f);
+            const int some = min(32, n - j0);
+            float x[JB][RB][E];
+            auto fetch = [&](int j) {
+#pragma unroll
+              for (int i = 0; i < JB; ++i) {
+                const float* o_src = p.part_o + (slot_of(min(j0 + j + i, n - 1)) + r0) * D + lane * E;
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                  const bool in = r0 + r < live_rows && j + i < some;
+                  if constexpr (E == 4) {
+                    const float4 q = in ? __ldcg(reinterpret_cast<const float4*>(o_src + r * D))
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    x[i][r][0] = q.x, x[i][r][1] = q.y, x[i][r][2] = q.z, x[i][r][3] = q.w;
+                  } else {
+                    const float2 q = in ? __ldcg(reinterpret_cast<const float2*>(o_src + r * D))
+                                        : make_float2(0.f, 0.f);
+                    x[i][r][0] = q.x, x[i][r][1] = q.y;
+                  }
+                }
+              }
+            };
+            fetch(0);  // on its way together with the maxima
+#pragma unroll
+            for (int r = 0; r < RB; ++r) {
+              float to = ml[r].x;
+#pragma unroll
+              for (int s = 16; s; s >>= 1) to = fmaxf(to, __shfl_xor_sync(0xffffffffu, to, s));
+              to = fmaxf(to, top[r]);
+              const float f = exp2_approx(top[r] - to);
+              top[r] = to;
+              sum[r] *= f;
+#pragma unroll
+              for (int e = 0; e < E; ++e) v[r][e] *= f;
+              ml[r].x = exp2_approx(ml[r].x - to);
+            }
+            for (int j = 0; j < some; j += JB) {
+#pragma unroll
+              for (int i = 0; i < JB; ++i)
+#pragma unroll
+                for (int r = 0; r < RB; ++r) {
+                  const float f = __shfl_sync(0xffffffffu, ml[r].x, (j + i) & 31);
+                  const float s = __shfl_sync(0xffffffffu, ml[r].y, (j + i) & 31);
+                  sum[r] += j + i < some ? s * f : 0.0f;
+#pragma unroll
+                  for (int e = 0; e < E; ++e) v[r][e] += j + i < some ? x[i][r][e] * f : 0.0f;
+                }
+              if (j + JB < some) fetch(j + JB);
             }
           }
-          float* row = own + r * PITCH;
 #pragma unroll
-          for (int e = 0; e < D / 32; ++e) row[lane * (D / 32) + e] = v[e];
-          if (lane == 0) *reinterpret_cast<float2*>(row + D) = make_float2(top, sum);
+          for (int r = 0; r < RB; ++r) {
+            if (r0 + r >= live_rows) break;
+            if (team) {
+              float* row = own + (r0 + r) * PITCH;
+#pragma unroll
+              for (int e = 0; e < E; ++e) row[lane * E + e] = v[r][e];
+              if (lane == 0) *reinterpret_cast<float2*>(row + D) = make_float2(top[r], sum[r]);
+            } else {
+              const RowOut w = open_row(r0 + r, true, top[r], sum[r], lane == 0);
+              if (w.out)
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                  *reinterpret_cast<uint32_t*>(w.out + lane * E + e) =
+                      pack_t<F16>(v[r][e] * w.inv, v[r][e + 1] * w.inv);
+            }
+          }
         }
-        team_sync();
-        join(to_output);
+        if (team) join(true);
       }
     }
-    fence_proxy_async();  // the rings' next writes are bulk copies
-    team_sync();
-
-    u += take;
-    if (u >= u_end) break;
-    o = 0;
-    if (++h == a.num_kv_heads) {
-      h = 0;
-      ++rg;
-      while (rg * ROWS >= seq.take * group) {  // the next sequence with rows of this kernel's
-        rg = 0;
-        do seq = Kv4Seq::of(a, ++b);
-        while (static_cast<long long>(seq.take) * group > p.max_packed_rows);
-      }
-      item = dec_item<ROWS>(seq, group, rg, a.window);
+    if (!more) break;
+    if (team) {
+      fence_proxy_async();  // the rings' next writes are bulk copies
+      __syncthreads();
+      begin();
     }
   }
   if (lane == 0 && cta_abort.raised() && a.status) atomicOr(a.status, kStatusTimeout);
@@ -647,17 +858,17 @@ __global__ void __launch_bounds__(kDecThreads, NT == 1 ? 2 : 1)
 namespace {
 template <int D, int NT, bool F16>
 int run_decode(const DecodeParams& q, cudaStream_t stream) {
+  using S = DecShape<D, NT>;
   DecodeParams p = q;
-  constexpr int stages = NT == 1 ? 3 : 4;
   const void* fn = reinterpret_cast<const void*>(lora_kv4_decode_kernel<D, NT, F16>);
-  const size_t smem = static_cast<size_t>(kDecWarps) * stages * 2 * Kv4Block<D>::kBytes;
+  const size_t smem = static_cast<size_t>(S::kWarps) * S::kStages * 2 * Kv4Block<D>::kBytes;
   if (ensure_smem_attr(fn, smem) != 0) return -6;
   const int sms = device_sm_count();
   if (sms <= 0) return -6;
-  const int grid = min((NT == 1 ? 2 : 1) * sms, kDecCtasMax);
-  return launch_pdl(fn, dim3(grid), dim3(kDecThreads), smem, stream, 0, &p);
+  return launch_pdl(fn, dim3(S::kCtas * min(sms, kDecSmsMax)), dim3(S::kWarps * 32), smem, stream,
+                    0, &p);
 }
-constexpr size_t kCounterBytes = kDecCtasMax * kDecWarps * 4;
+constexpr size_t kCounterBytes = kDecWorkersMax * 4;
 }  // namespace
 
 size_t kv4_decode_counter_bytes() { return kCounterBytes; }
@@ -678,6 +889,7 @@ int launch_kv4_decode(const Kv4AttnArgs& a, int max_packed_rows, size_t counters
   p.part_ml = reinterpret_cast<float2*>(w + kCounterBytes +
                                         static_cast<size_t>(kPartialSlots) * rows * a.head_dim * 4);
   p.max_packed_rows = max_packed_rows;
+  p.group_magic = (65536u + group - 1) / group;
   p.wait_fault = wait_fault() ? 1 : 0;
   p.wait_limit_ns = p.wait_fault ? kTestWaitLimitNs : kWaitLimitNs;
   if (a.head_dim == 64)

@@ -29,35 +29,72 @@
 namespace grg {
 
 namespace {
-constexpr int kPreThreads = 13 * 32;
+constexpr int kPreThreads = 12 * 32;  // (168 registers each)
+constexpr int kPreWarps = kPreThreads / 32;
 constexpr int kPreCtasMax = 160;  // CTAs that the workspace has room for
 constexpr int kPreRows = 256;     // packed rows of an item
 constexpr int kPreKeys = 128;     // keys of a tile
+// What the line counts: a key tile of two row tiles, of one, and an item's start and end.
+constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 4;
+constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
 constexpr float kPreLog2e = 1.4426950408889634f;
 constexpr float kPreLn2 = 0.6931471805599453f;
+constexpr float kPreNoKey = -1e30f;  // the running maximum before any key
 
 struct PrefillParams {
   Kv4AttnArgs a;
   uint32_t* counters;   // [kPreCtasMax], zero between calls
-  float* part_o;        // [2 * kPreCtasMax][256][D]
+  float4* part_o;       // [2 * kPreCtasMax][2 tiles][D / 4][128 rows]
   float2* part_ml;      // [2 * kPreCtasMax][256]
   int max_packed_rows;  // sequences with no more packed rows are not this kernel's
   unsigned long long wait_limit_ns;
   int wait_fault;
 };
 
+// An item's key tiles: [kt0, kt0 + nt); hi = 0 where no row sees a key.
+struct PreItem {
+  int kt0, nt, hi;
+  int cost;  // of a key tile
+  __device__ __forceinline__ int size() const { return kCostItem + nt * cost; }
+};
+__device__ __forceinline__ PreItem pre_item(const Kv4Seq& s, int group, int rt, int window) {
+  const int rows = static_cast<int>(min(static_cast<long long>(s.take) * group -
+                                            static_cast<long long>(rt) * kPreRows,
+                                        static_cast<long long>(kPreRows)));
+  const int i0 = static_cast<int>(static_cast<long long>(rt) * kPreRows / group);
+  const int i1 = static_cast<int>((static_cast<long long>(rt) * kPreRows + rows - 1) / group);
+  const int hi = s.pos(i1) + 1, lo = s.first_key(i0, window);
+  PreItem it;
+  it.kt0 = lo / kPreKeys;
+  it.hi = hi > lo ? hi : 0;
+  it.nt = hi > lo ? (hi + kPreKeys - 1) / kPreKeys - it.kt0 : 1;
+  it.cost = rows > 128 ? kCostTwo : kCostOne;
+  return it;
+}
+// What a CTA does of an item.
+struct PrePart {
+  Kv4Seq seq;
+  PreItem item;
+  int b, h, rt;
+  int o, take;   // key tiles [o, o + take) of the item
+  long long at;  // the item's place in the line
+};
+
 // Shared memory behind the operand tiles.
 struct PreShared {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t s_full[2], o_full[2];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t drain;
+  uint64_t drain[2];
   // keys of a tile that exist; four tiles deep: a tile's words are rewritten only
   // after both softmaxes have taken the tile two further on
-  uint32_t valid[4][4];
+  __align__(16) uint32_t valid[4][4];
   uint32_t taddr;
   int abort, poison, last;
+  PrePart part[8][2];    // the softmax warps' parts (their registers are needed for S)
+  long long u0, u_end, per;
+  __align__(16) unsigned char staged[8][32 * kStagePitch];  // of the softmax warps
   long long prefix[kPreThreads + 1];
-  long long warp_sum[13];
+  long long warp_sum[kPreWarps];
 };
 
 __device__ __forceinline__ uint32_t pre_hmul2(uint32_t a, uint32_t b) {
@@ -80,7 +117,7 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d, uint32_t a, uint64_t b, 
       : "memory");
 }
 // 16 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
       "%14,%15,%16};\n" ::"r"(taddr),
@@ -88,28 +125,78 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
+// 32 consecutive 32-bit columns of this thread's TMEM lane: the load, and the
+// wait for every load so far (the registers hold nothing before it).
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld32_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// (a0, a1) * (b, b) + (c, c) and (a0, a1) + (b0, b1), two fp32 at a time.
+__device__ __forceinline__ void fma2(float& x, float& y, uint32_t a0, uint32_t a1, float b, float c) {
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 c, {%5, %5};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "r"(a0), "r"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b) {
+  asm("{\n .reg .b64 a, b;\n mov.b64 a, {%0, %1};\n mov.b64 b, {%2, %3};\n add.rn.f32x2 a, a, b;\n"
+      " mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(x), "+f"(y)
+      : "f"(a), "f"(b));
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+}
+// A 16-byte load that stays where it is written: several of them go out together.
+__device__ __forceinline__ uint4 load_now(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+// The same, and whether any of the threads says so.
+__device__ __forceinline__ bool pre_barrier_any(int id, int threads, bool says) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
+      " selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(says ? 1u : 0u), "r"(id), "r"(threads)
+      : "memory");
+  return r != 0;
 }
 __device__ __forceinline__ void pre_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(threads) : "memory");
 }
 
-// An item's key tiles: [kt0, kt0 + nt); hi = 0 where no row sees a key.
-struct PreItem {
-  int kt0, nt, hi;
-};
-__device__ __forceinline__ PreItem pre_item(const Kv4Seq& s, int group, int rt, int window) {
-  const int i0 = rt * kPreRows / group;
-  const int i1 = (static_cast<int>(min(static_cast<long long>(s.take) * group,
-                                       static_cast<long long>(rt + 1) * kPreRows)) - 1) / group;
-  const int hi = s.pos(i1) + 1, lo = s.first_key(i0, window);
-  PreItem it;
-  it.kt0 = lo / kPreKeys;
-  it.hi = hi > lo ? hi : 0;
-  it.nt = hi > lo ? (hi + kPreKeys - 1) / kPreKeys - it.kt0 : 1;
-  return it;
-}
 }  // namespace
 
 template <int D, bool F16>
@@ -132,26 +219,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   unsigned char* smem = smem_raw + (sbase - raw);
   PreShared& sh = *reinterpret_cast<PreShared*>(smem + kOffShared);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform, and known to be
   const Kv4AttnArgs& a = p.a;
   const int group = a.num_q_heads / a.num_kv_heads;
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.q_full[i]), 128 + (p.wait_fault ? 1 : 0));
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.p_full[i]), 128);
       mbar_init(smem_u32(&sh.o_full[i]), 1);
-      mbar_init(smem_u32(&sh.k_full[i]), 128);
-      mbar_init(smem_u32(&sh.k_empty[i]), 1);
+      mbar_init(smem_u32(&sh.k_full[i]), 128 + (p.wait_fault ? 1 : 0));
+      mbar_init(smem_u32(&sh.k_empty[i]), 2);
       mbar_init(smem_u32(&sh.v_full[i]), 128);
-      mbar_init(smem_u32(&sh.v_empty[i]), 1);
+      mbar_init(smem_u32(&sh.v_empty[i]), 2);
     }
-    mbar_init(smem_u32(&sh.drain), 1);
+    mbar_init(smem_u32(&sh.drain[0]), 1);
+    mbar_init(smem_u32(&sh.drain[1]), 1);
     fence_mbar_init();
     sh.abort = 0;
     sh.poison = 0;
   }
-  if (warp == 12) {
+  if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      smem_u32(&sh.taddr)),
                  "r"(kCols)
@@ -174,7 +261,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     long long n = 0;
     if (mine_of(s)) {
       const int nr = tiles_of(s);
-      for (int rt = 0; rt < nr; ++rt) n += pre_item(s, group, rt, a.window).nt;
+      for (int rt = 0; rt < nr; ++rt) n += pre_item(s, group, rt, a.window).size();
     }
     return n;
   };
@@ -195,7 +282,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   tc_fence_after();
   long long before = 0, total = 0;
 #pragma unroll
-  for (int w = 0; w < 13; ++w) {
+  for (int w = 0; w < kPreWarps; ++w) {
     if (w < warp) before += sh.warp_sum[w];
     total += sh.warp_sum[w];
   }
@@ -204,22 +291,47 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   __syncthreads();
   const uint32_t taddr = sh.taddr;
 
-  const long long per = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x), 1ll);
-  const long long u0 = blockIdx.x * per, u_end = min(u0 + per, total);
+  // (a run is no shorter than a tile, so every run inside an item has one of its tiles)
+  const long long per = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x),
+                            static_cast<long long>(kCostTwo));
+  if (tid == 0) {
+    sh.per = per;
+    sh.u0 = blockIdx.x * per;
+    sh.u_end = min(sh.u0 + per, total);
+  }
+  __syncthreads();
 
   // The CTA's parts of items, in order; every role walks the same list.
-  struct Part {
-    Kv4Seq seq;
-    PreItem item;
-    int b, h, rt;
-    int o, take;  // key tiles [o, o + take) of the item
-    long long u;  // first unit
-  };
-  auto set_part = [&](Part& q) {
+  // A tile is the run's in which its place begins.
+  auto set_part = [&](PrePart& q) {
     q.item = pre_item(q.seq, group, q.rt, a.window);
-    q.take = static_cast<int>(min(static_cast<long long>(q.item.nt - q.o), u_end - q.u));
+    auto tiles_before = [&](long long x) {  // tiles that begin before place x
+      const long long n = x - q.at - kCostItem;
+      return n <= 0 ? 0 : static_cast<int>(min((n + q.item.cost - 1) / q.item.cost,
+                                               static_cast<long long>(q.item.nt)));
+    };
+    q.o = tiles_before(sh.u0);
+    q.take = tiles_before(sh.u_end) - q.o;
   };
-  auto first_part = [&](Part& q) {
+  auto next_part = [&](PrePart& q) -> bool {
+    do {
+      q.at += q.item.size();
+      if (q.at >= sh.u_end) return false;
+      if (++q.rt == tiles_of(q.seq)) {
+        q.rt = 0;
+        if (++q.h == a.num_kv_heads) {
+          q.h = 0;
+          do q.seq = Kv4Seq::of(a, ++q.b);
+          while (!mine_of(q.seq));
+        }
+      }
+      set_part(q);
+    } while (q.take == 0);
+    return true;
+  };
+  auto first_part = [&](PrePart& q) -> bool {
+    const long long u0 = sh.u0;
+    if (u0 >= sh.u_end) return false;
     int lo = 0, hi = kPreThreads;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
@@ -238,345 +350,447 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     off -= q.h * n;
     q.rt = 0;
     while (true) {
-      const int nt = pre_item(q.seq, group, q.rt, a.window).nt;
-      if (off < nt) break;
-      off -= nt;
+      const int size = pre_item(q.seq, group, q.rt, a.window).size();
+      if (off < size) break;
+      off -= size;
       ++q.rt;
     }
-    q.o = static_cast<int>(off);
-    q.u = u0;
+    q.at = u0 - off;
     set_part(q);
+    return q.take > 0 || next_part(q);
   };
-  auto next_part = [&](Part& q) -> bool {
-    q.u += q.take;
-    if (q.u >= u_end) return false;
-    q.o = 0;
-    if (++q.rt == tiles_of(q.seq)) {
-      q.rt = 0;
-      if (++q.h == a.num_kv_heads) {
-        q.h = 0;
-        do q.seq = Kv4Seq::of(a, ++q.b);
-        while (!mine_of(q.seq));
-      }
-    }
-    set_part(q);
-    return true;
-  };
-  auto live_rows = [&](const Part& q) {
+  auto live_rows = [&](const PrePart& q) {
     return static_cast<int>(min(static_cast<long long>(q.seq.take) * group - static_cast<long long>(q.rt) * kPreRows,
                                 static_cast<long long>(kPreRows)));
   };
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
-  if (u0 < u_end) {
-    Part q;
-    first_part(q);
+  PrePart q;
+  if (first_part(q)) {
     if (warp < 8) {
       // -------------------------------------------------------------- softmax
       const int t = warp >> 2;                    // tile
-      const int row = (warp & 3) * 32 + lane;     // row of the tile, and TMEM lane
+      const int row_in_tile = (warp & 3) * 32 + lane;  // and TMEM lane
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t tS = taddr + lane_base + kColS + t * kPreKeys;
       const uint32_t tO = taddr + lane_base + kColO + t * D;
-      uint32_t ns = 0, no = 0;  // S tiles and second products so far
-      int stage_it = 0;         // key tiles so far (the stage's valid bits)
-      do {
-        const int live = live_rows(q);
-        const int nact = live > 128 ? 2 : 1;
-        if (t < nact) {
-          const int packed0 = q.rt * kPreRows;
-          const int pr = packed0 + min(t * 128 + row, live - 1);  // rows past the end repeat the last
-          const int i = pr / group, head = q.h * group + pr % group, tok = q.seq.q0 + i;
-          const int pos = q.seq.pos(i), lo = q.seq.first_key(i, a.window);
-          // ---- the row of q, in fp16
-          float down;
-          {
-            const uint16_t* src = a.q + tok * a.q_stride + head * D;
-            uint4 w[D / 8];
-            float top = 0.0f;
+      const uint32_t sS = taddr + kColS + t * kPreKeys, sO = taddr + kColO + t * D;
+      uint32_t ns = 0, no = 0;  // first products, and second ones, of this tile so far
+      uint32_t it = 0;  // key tiles so far (the stages of K and V)
+      // The products, issued by one thread of the tile's first warp, in the order
+      // S(0), O(0), S(1), O(1), ...: the tensor core takes one tile's in turn, so S
+      // never overwrites a P still to be read.  A key tile's stages of K and V are free
+      // when the second products of both tiles (all that are active) are done: until
+      // then its scores can be formed once more.
+      auto scores = [&](uint32_t i) {  // of key tile i
+        const uint32_t st = __shfl_sync(0xffffffffu, i & 1, 0);
+        if (!__all_sync(0xffffffffu, cta_abort.wait(bar(sh.k_full[st]), (i >> 1) & 1))) return;
+        tc_fence_after();
+        const uint64_t dq = umma_desc_sw128(sbase + t * kTile, 16, 1024);
+        const uint64_t dk = umma_desc_sw128(sbase + kOffK + st * kTile, 16, 1024);
+        if (elect_one()) {
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              w[c] = __ldg(reinterpret_cast<const uint4*>(src) + c);
-              const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_t<F16>(x[e]);
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-            }
-            float up;
-            row_factor(top, up, down);
-            unsigned char* tile = smem + t * kTile;
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c) {
-              const uint32_t x[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
-              uint32_t y[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = unpack_t<F16>(x[e]);
-                y[e] = pack_f16x2(f.x * up, f.y * up);
-              }
-              *reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + swz128(row, c & 7)) =
-                  make_uint4(y[0], y[1], y[2], y[3]);
-            }
-            fence_proxy_async();
-            mbar_arrive(bar(sh.q_full[t]));
+          for (int kk = 0; kk < D / 16; ++kk) {  // (addresses count in 16 bytes)
+            const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
+            umma_f16(sS, dq + off, dk + off, kIdescS, kk != 0 ? 1u : 0u);
           }
-          const float cf = down * (a.score_scale * kPreLog2e);
-          float m = -INFINITY, l = 0.0f;
-          for (int j = 0; j < q.take; ++j) {
-            const int key0 = (q.item.kt0 + q.o + j) * kPreKeys;
+          umma_commit(bar(sh.s_full[t]));
+        }
+      };
+      auto values = [&](uint32_t i, bool add, int nact) {
+        const uint32_t st = __shfl_sync(0xffffffffu, i & 1, 0);
+        if (!__all_sync(0xffffffffu, cta_abort.wait(bar(sh.v_full[st]), (i >> 1) & 1))) return;
+        tc_fence_after();
+        const uint64_t dv = umma_desc_sw128(sbase + kOffV + st * kTile, kAtom, 1024);
+        if (elect_one()) {
+          umma_f16_ts(sO, sS, dv, kIdescO, add ? 1u : 0u);
+#pragma unroll
+          for (int kk = 1; kk < kPreKeys / 16; ++kk)
+            umma_f16_ts(sO, sS + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdescO, 1u);
+          umma_commit(bar(sh.o_full[t]));
+          for (int c = nact; c <= 2; ++c) {
+            umma_commit(bar(sh.k_empty[st]));
+            umma_commit(bar(sh.v_empty[st]));
+          }
+        }
+      };
+      // This thread's row of a part.
+      struct Row {
+        int nact;     // tiles of the part that have rows
+        int pos, lo;  // its position, and the first key that it sees
+        float cf;     // what turns its products into scores in units of log2
+      };
+      // Where it lies in q and out (rows past the end repeat the last).
+      struct Place {
+        int i, tok, head;
+        bool live;
+      };
+      auto place = [&](const PrePart& w) {
+        Place x;
+        const int live = live_rows(w), r = t * 128 + row_in_tile;
+        x.live = r < live;
+        const int pr = w.rt * kPreRows + min(r, live - 1);
+        x.i = pr / group;
+        x.head = w.h * group + pr - x.i * group;
+        x.tok = w.seq.q0 + x.i;
+        return x;
+      };
+      // Starts a part: q in fp16 to shared memory, the first product under way.
+      auto open_part = [&](const PrePart& w) {
+        Row x;
+        const Place mine_p = place(w);
+        x.nact = live_rows(w) > 128 ? 2 : 1;
+        x.pos = w.seq.pos(mine_p.i);
+        x.lo = w.seq.first_key(mine_p.i, a.window);
+        x.cf = 0.0f;
+        if (t >= x.nact) return x;
+        // the warp's 32 rows, D / 8 lanes a row and 256 / D rows at a time, so that
+        // a row's reads are neighbours
+        constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, PASSES = 32 / AT_ONCE;
+        unsigned char* tile = smem + t * kTile;
+        float down = 0.0f;
+        uint4 raw_q[PASSES];
+#pragma unroll
+        for (int i2 = 0; i2 < PASSES; ++i2) {
+          const int r = i2 * AT_ONCE + lane / LANES;
+          const long long tok = __shfl_sync(0xffffffffu, mine_p.tok, r);
+          const int head = __shfl_sync(0xffffffffu, mine_p.head, r);
+          raw_q[i2] = load_now(reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + head * D) + lane % LANES);
+        }
+        pre_barrier(2 + t, 128);  // (keeps the loads together, ahead of their first use)
+#pragma unroll
+        for (int i2 = 0; i2 < PASSES; ++i2) {
+          const int r = i2 * AT_ONCE + lane / LANES, c = lane % LANES;
+          const uint32_t y[4] = {raw_q[i2].x, raw_q[i2].y, raw_q[i2].z, raw_q[i2].w};
+          float2 f[4];
+          float top = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[e] = unpack_t<F16>(y[e]);
+            top = fmaxf(top, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+          }
+#pragma unroll
+          for (int sft = LANES / 2; sft; sft >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
+          float up, dn;
+          row_factor(top, up, dn);
+          uint32_t z[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[e] = pack_f16x2(f[e].x * up, f[e].y * up);
+          *reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + swz128((warp & 3) * 32 + r, c & 7)) =
+              make_uint4(z[0], z[1], z[2], z[3]);
+          dn = __shfl_sync(0xffffffffu, dn, (lane % AT_ONCE) * LANES);
+          if (lane / AT_ONCE == i2) down = dn;
+        }
+        x.cf = down * (a.score_scale * kPreLog2e);
+        fence_proxy_async();
+        pre_barrier(2 + t, 128);
+        if ((warp & 3) == 0) scores(it);
+        __syncwarp();
+        return x;
+      };
+      Row row = open_part(q);
+      int slot_of_part = 0, take = q.take, first_key = (q.item.kt0 + q.o) * kPreKeys;
+      if (lane == 0) sh.part[warp][0] = q;
+      __syncwarp();
+      while (true) {
+        float m = kPreNoKey, l0 = 0.0f, l1 = 0.0f;
+        const bool on = t < row.nact;
+        for (int j = 0; on && j < take; ++j) {
+          const int key0 = first_key + j * kPreKeys;
+          const int hi_j = row.pos - key0, lo_j = row.lo - key0;
+          // p = 2^(s c - m) against the running reference m, in one pass over S, 32
+          // keys at a time; where some score passes m by 2^15 (fp16 would end) the
+          // tile is done again with m moved, and so is a part's first tile
+          const float l0_was = l0, l1_was = l1;
+          bool again = j == 0;
+          while (true) {
             cta_abort.wait(bar(sh.s_full[t]), ns & 1);
             ++ns;
             __syncwarp();
             tc_fence_after();
-            // keys of the tile that this row sees
-            uint32_t seen[4];
-            {
-              const int hi_j = pos - key0, lo_j = lo - key0;
-              const volatile uint32_t* valid = sh.valid[(stage_it + j) & 3];
-              bool all = true;
+            const uint4 valid = *reinterpret_cast<const uint4*>(sh.valid[(it + j) & 3]);
+            const bool masked = __any_sync(0xffffffffu, hi_j < 127 || lo_j > 0 ||
+                                                            (valid.x & valid.y & valid.z & valid.w) != ~0u);
+            auto hide = [&](int c, uint32_t (&v)[32]) {  // keys that this row does not see
+              const int h = hi_j - 32 * c, g = lo_j - 32 * c;
+              uint32_t seen = c == 0 ? valid.x : c == 1 ? valid.y : c == 2 ? valid.z : valid.w;
+              if (h < 31) seen &= h < 0 ? 0u : (2u << h) - 1u;
+              if (g > 0) seen &= g > 31 ? 0u : ~0u << g;
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const int h = hi_j - 32 * c, g = lo_j - 32 * c;
-                uint32_t s = valid[c];
-                if (h < 31) s &= h < 0 ? 0u : (2u << h) - 1u;
-                if (g > 0) s &= g > 31 ? 0u : ~0u << g;
-                seen[c] = s;
-                all = all && s == ~0u;
+              for (int e = 0; e < 32; ++e)
+                if (!((seen >> e) & 1u)) v[e] = 0xFF800000u;  // -infinity
+            };
+            auto top_of = [&](float x, const uint32_t (&v)[32]) {
+              float y = __uint_as_float(v[31]);
+#pragma unroll
+              for (int e = 0; e < 30; e += 4) {
+                x = max3(x, __uint_as_float(v[e]), __uint_as_float(v[e + 1]));
+                if (e < 28) y = max3(y, __uint_as_float(v[e + 2]), __uint_as_float(v[e + 3]));
               }
-              const bool masked = __any_sync(0xffffffffu, !all);
+              return max3(x, y, __uint_as_float(v[30]));
+            };
+            if (again) {  // the tile's maximum first
               float mx = -INFINITY;
-#pragma unroll
+#pragma unroll 1
               for (int c = 0; c < 4; ++c) {
-                float v[32];
-                tmem_ld32(tS + 32 * c, v);
-                if (masked) {
-#pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((seen[c] >> e) & 1u)) v[e] = -INFINITY;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e) mx = fmaxf(mx, v[e]);
+                uint32_t v[32];
+                tmem_ld32_start(tS + 32 * c, v);
+                tmem_ld32_wait(v);
+                if (masked) hide(c, v);
+                mx = top_of(mx, v);
               }
-              mx *= cf;
-              const bool move = mx > m + 6.0f;
-              if (__any_sync(0xffffffffu, move && m != -INFINITY)) {
-                // rare: O takes the new maximum
+              mx *= row.cf;
+              if (__any_sync(0xffffffffu, mx > m && m != kPreNoKey)) {
+                // O takes the new reference
                 cta_abort.wait(bar(sh.o_full[t]), (no - 1) & 1);
                 __syncwarp();
                 tc_fence_after();
-                const float to = move ? mx : m;
-                const float f = m == -INFINITY ? 1.0f : exp2_approx(m - to);
-                l *= f;
+                const float f = exp2_approx(m - fmaxf(m, mx));
+                l0 *= f, l1 *= f;
 #pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                  uint32_t r[16];
-                  asm volatile(
-                      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,"
-                      "%12,%13,%14,%15}, [%16];\n"
-                      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
-                        "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-                        "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                      : "r"(tO + 16 * c));
-                  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+                for (int c = 0; c < D / 32; ++c) {
+                  uint32_t r[32];
+                  tmem_ld32_start(tO + 32 * c, r);
+                  tmem_ld32_wait(r);
 #pragma unroll
-                  for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-                  tmem_st16(tO + 16 * c, r);
+                  for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+                  tmem_st16(tO + 32 * c, r);
+                  tmem_st16(tO + 32 * c + 16, r + 16);
                 }
               }
-              if (move) m = mx;
-              const float mm = m == -INFINITY ? 0.0f : m;
+              m = fmaxf(m, mx);
+            }
+            float mx = -INFINITY;
+            uint32_t v[2][32];
+            tmem_ld32_start(tS, v[0]);
 #pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                float v[32];
-                tmem_ld32(tS + 32 * c, v);
-                if (masked) {
+            for (int c = 0; c < 4; ++c) {
+              uint32_t (&x)[32] = v[c & 1];
+              tmem_ld32_wait(x);
+              if (c < 3) tmem_ld32_start(tS + 32 * (c + 1), v[(c + 1) & 1]);
+              if (masked) hide(c, x);
+              mx = top_of(mx, x);
+              uint32_t w[16];
 #pragma unroll
-                  for (int e = 0; e < 32; ++e)
-                    if (!((seen[c] >> e) & 1u)) v[e] = -INFINITY;
-                }
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                  const float p0 = exp2_approx(fmaf(v[e], cf, -mm));
-                  const float p1 = exp2_approx(fmaf(v[e + 1], cf, -mm));
-                  l += p0 + p1;
-                  w[e / 2] = pack_f16x2(p0, p1);
-                }
-                tmem_st16(tS + 16 * c, w);
+              for (int e = 0; e < 32; e += 2) {
+                float y, z;
+                fma2(y, z, x[e], x[e + 1], row.cf, -m);
+                y = exp2_approx(y), z = exp2_approx(z);
+                add2(l0, l1, y, z);
+                w[e / 2] = pack_f16x2(y, z);
               }
+              tmem_st16(tS + 16 * c, w);
             }
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(bar(sh.p_full[t]));
-            ++no;
+            // the tile's P is there, or some row wants it again
+            again = pre_barrier_any(2 + t, 128, mx * row.cf > m + 15.0f);
+            if (!again) break;
+            l0 = l0_was, l1 = l1_was;
+            if ((warp & 3) == 0) scores(it + j);
+            __syncwarp();
           }
-          // ---- the row of O
+          if ((warp & 3) == 0) {
+            values(it + j, j > 0, row.nact);
+            if (j + 1 < take) scores(it + j + 1);
+          }
+          __syncwarp();
+          ++no;
+        }
+        // ---- the next part starts (neither tile's warps run ahead by a part);
+        // while its first product runs, this one's rows go out
+        it += take;
+        const PrePart done = sh.part[warp][slot_of_part];
+        const int done_lo = row.lo, done_pos = row.pos, done_nact = row.nact;
+        PrePart q2 = done;
+        const bool more = next_part(q2);
+        if (more) {
+          pre_barrier(1, 256);
+          row = open_part(q2);
+          slot_of_part ^= 1;
+          take = q2.take, first_key = (q2.item.kt0 + q2.o) * kPreKeys;
+          if (lane == 0) sh.part[warp][slot_of_part] = q2;
+          __syncwarp();
+        }
+        if (on) {
+          const Place out = place(done);
+          const float l = l0 + l1;
           cta_abort.wait(bar(sh.o_full[t]), (no - 1) & 1);
           __syncwarp();
           tc_fence_after();
           uint32_t nan_blocks = 0;  // 16-dimension blocks with a NaN scale at a key of the row
           if (*reinterpret_cast<volatile int*>(&sh.poison)) {
-            const int32_t* table = a.page_table + static_cast<long long>(q.b) * a.table_stride;
-            const int k0 = max(lo, (q.item.kt0 + q.o) * kPreKeys);
-            const int k1 = min(pos, (q.item.kt0 + q.o + q.take) * kPreKeys - 1);
+            const int32_t* table = a.page_table + static_cast<long long>(done.b) * a.table_stride;
+            const int k0 = max(done_lo, (done.item.kt0 + done.o) * kPreKeys);
+            const int k1 = min(done_pos, (done.item.kt0 + done.o + done.take) * kPreKeys - 1);
             for (int key = k0; key <= k1; ++key) {
               const int page = __ldg(table + key / a.page_size), in = key % a.page_size;
               if (page < 0 || page >= a.num_pages) continue;
-              const uint8_t* at = a.cache + ((static_cast<long long>(page) * a.num_kv_heads + q.h) *
+              const uint8_t* at = a.cache + ((static_cast<long long>(page) * a.num_kv_heads + done.h) *
                                                  (a.page_size / 16) + in / 16) * B::kBytes +
                                   B::kVScale + (in % 16) * B::kScaleRow;
               for (int e = 0; e < D / 16; ++e)
                 if ((at[e] & 0x7F) == 0x7F) nan_blocks |= 1u << e;
             }
           }
-          const bool store = t * 128 + row < live && !cta_abort.raised();
-          if (q.take == q.item.nt) {
-            const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
-            uint16_t* dst = a.out + tok * a.out_stride + head * D;
+          const bool all_of_it = done.take == done.item.nt;
+          const int slot = static_cast<int>(blockIdx.x) * 2 + (done.o == 0 ? 1 : 0);
+          unsigned char* staged = sh.staged[warp];
+          // 32 dimensions of the warp's 32 rows: through shared memory, so that a
+          // row's stores are neighbours (8 rows of 64 bytes at a time)
+          auto rows_out = [&](int c, const float (&v)[32], float inv) {
+            unsigned char* mine_s = staged + lane * kStagePitch;
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float v[32];
-              tmem_ld32(tO + 32 * c, v);
-#pragma unroll
-              for (int e = 0; e < 32; ++e) {
-                v[e] *= inv;
-                if ((nan_blocks >> (2 * c + e / 16)) & 1u) v[e] = __uint_as_float(0x7FC00000u);
-              }
-              if (store) {
-#pragma unroll
-                for (int e = 0; e < 32; e += 8) {
-                  uint4 w;
-                  w.x = pack_t<F16>(v[e], v[e + 1]);
-                  w.y = pack_t<F16>(v[e + 2], v[e + 3]);
-                  w.z = pack_t<F16>(v[e + 4], v[e + 5]);
-                  w.w = pack_t<F16>(v[e + 6], v[e + 7]);
-                  *reinterpret_cast<uint4*>(dst + 32 * c + e) = w;
-                }
-              }
+            for (int e = 0; e < 32; e += 8) {
+              uint4 w;
+              w.x = pack_t<F16>(v[e] * inv, v[e + 1] * inv);
+              w.y = pack_t<F16>(v[e + 2] * inv, v[e + 3] * inv);
+              w.z = pack_t<F16>(v[e + 4] * inv, v[e + 5] * inv);
+              w.w = pack_t<F16>(v[e + 6] * inv, v[e + 7] * inv);
+              *reinterpret_cast<uint4*>(mine_s + 2 * e) = w;
             }
-            if (store && a.lse)
-              a.lse[static_cast<long long>(tok) * a.num_q_heads + head] =
-                  l == 0.0f ? -INFINITY : (m + log2f(l)) * kPreLn2;
-          } else {
-            const long long slot = static_cast<long long>(blockIdx.x) * 2 + (q.o == 0 ? 1 : 0);
-            float* dst = p.part_o + (slot * kPreRows + t * 128 + row) * D;
+            __syncwarp();
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-              float v[32];
-              tmem_ld32(tO + 32 * c, v);
+            for (int i2 = 0; i2 < 4; ++i2) {
+              const int r = 8 * i2 + (lane >> 2);
+              const long long tok = __shfl_sync(0xffffffffu, out.tok, r);
+              const int head = __shfl_sync(0xffffffffu, out.head, r);
+              const bool store = __shfl_sync(0xffffffffu, out.live ? 1 : 0, r) && !cta_abort.raised();
+              const uint4 w = *reinterpret_cast<const uint4*>(staged + r * kStagePitch + 16 * (lane & 3));
+              if (store)
+                *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + head * D + 32 * c + 8 * (lane & 3)) = w;
+            }
+            __syncwarp();
+          };
+          auto lse_out = [&](float top, float sum) {
+            if (out.live && !cta_abort.raised() && a.lse)
+              a.lse[static_cast<long long>(out.tok) * a.num_q_heads + out.head] =
+                  sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kPreLn2;
+          };
+          // the place of 4 dimensions of this row in a slot's partials
+          auto part_of = [&](long long at_slot, int c4) {
+            return p.part_o + ((at_slot * 2 + t) * (D / 4) + c4) * 128 + row_in_tile;
+          };
+          const float inv = l == 0.0f ? 0.0f : a.v_scale / l;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float v[32];
+            tmem_ld32(tO + 32 * c, v);
+            if (nan_blocks) {
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if ((nan_blocks >> (2 * c + e / 16)) & 1u) v[e] = __uint_as_float(0x7FC00000u);
+            }
+            if (all_of_it) {
+              rows_out(c, v, inv);
+            } else {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
-                *reinterpret_cast<float4*>(dst + 32 * c + e) =
-                    make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                *part_of(slot, 8 * c + e / 4) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
             }
-            p.part_ml[slot * kPreRows + t * 128 + row] = make_float2(m, l);
-            __threadfence();
-            const int threads = 128 * nact;
-            const int w0 = static_cast<int>((q.u - q.o) / per);
-            const int w1 = static_cast<int>((q.u - q.o + q.item.nt - 1) / per);
-            pre_barrier(nact, threads);
-            if (tid == 0) {
-              const int last = atomicAdd(p.counters + w0, 1u) == static_cast<uint32_t>(w1 - w0);
-              if (last) p.counters[w0] = 0;
-              __threadfence();
-              sh.last = last;
-            }
-            pre_barrier(nact, threads);
-            if (*reinterpret_cast<volatile int*>(&sh.last)) {
-              // every part is there: a warp takes a row at a time, in run order
-              const int n = w1 - w0 + 1;
-              for (int r = warp; r < live; r += 4 * nact) {
-                auto at = [&](int i) {
-                  return ((static_cast<long long>(w0) + i) * 2 + (i == 0)) * kPreRows + r;
-                };
-                float top = -INFINITY;
-                for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(&p.part_ml[at(i)]).x);
-#pragma unroll
-                for (int s = 16; s; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-                float v[D / 32] = {}, sum = 0.0f;
-#pragma unroll 4
-                for (int i = 0; i < n; ++i) {
-                  const float2 ml = __ldcg(&p.part_ml[at(i)]);
-                  const float f = ml.x == -INFINITY ? 1.0f : exp2_approx(ml.x - top);
-                  sum += ml.y * f;
-                  const float* src = p.part_o + at(i) * D + lane * (D / 32);
-#pragma unroll
-                  for (int e = 0; e < D / 32; e += 2) {
-                    const float2 x = __ldcg(reinterpret_cast<const float2*>(src + e));
-                    v[e] += x.x * f;
-                    v[e + 1] += x.y * f;
-                  }
-                }
-                const int prr = packed0 + r, hh = q.h * group + prr % group;
-                const long long tt = q.seq.q0 + prr / group;
-                const float inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
-                if (!cta_abort.raised()) {
-#pragma unroll
-                  for (int e = 0; e < D / 32; e += 2)
-                    *reinterpret_cast<uint32_t*>(a.out + tt * a.out_stride + hh * D + lane * (D / 32) + e) =
-                        pack_t<F16>(v[e] * inv, v[e + 1] * inv);
-                  if (lane == 0 && a.lse)
-                    a.lse[tt * a.num_q_heads + hh] =
-                        sum == 0.0f ? -INFINITY : (top + log2f(sum)) * kPreLn2;
-                }
-              }
-            }
-            pre_barrier(nact, threads);  // sh.last may change again
           }
           tc_fence_before();
+          if (all_of_it) {
+            lse_out(m, l);
+          } else {
+            p.part_ml[static_cast<long long>(slot) * kPreRows + t * 128 + row_in_tile] = make_float2(m, l);
+            const int threads = 128 * done_nact;
+            const long long begins = done.at + kCostItem;
+            const int w0 = static_cast<int>(begins / sh.per);
+            const int w1 = static_cast<int>((begins + static_cast<long long>(done.item.nt - 1) * done.item.cost) / sh.per);
+            pre_barrier(3 + done_nact, threads);
+            if (tid == 0) {
+              uint32_t seen;  // releases what the barrier has gathered, acquires the others'
+              asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;\n"
+                           : "=r"(seen)
+                           : "l"(p.counters + w0)
+                           : "memory");
+              sh.last = seen == static_cast<uint32_t>(w1 - w0);
+              if (sh.last) p.counters[w0] = 0;
+            }
+            pre_barrier(3 + done_nact, threads);
+            const bool last = *reinterpret_cast<volatile int*>(&sh.last) != 0;
+            pre_barrier(3 + done_nact, threads);  // sh.last may change again
+            if (last) {
+              // every part is there: they are joined in run order
+              const int runs = w1 - w0 + 1;
+              auto slot_of = [&](int i) { return (static_cast<long long>(w0) + i) * 2 + (i == 0 ? 1 : 0); };
+              auto ml_of = [&](int i) { return __ldcg(p.part_ml + slot_of(i) * kPreRows + t * 128 + row_in_tile); };
+              float top = kPreNoKey, sum = 0.0f;
+              for (int i = 0; i < runs; ++i) {
+                const float2 ml = ml_of(i);
+                const float to = fmaxf(top, ml.x);
+                sum = sum * exp2_approx(top - to) + ml.y * exp2_approx(ml.x - to);
+                top = to;
+              }
+              const float all_inv = sum == 0.0f ? 0.0f : a.v_scale / sum;
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                float v[32] = {};
+#pragma unroll 2
+                for (int i = 0; i < runs; ++i) {
+                  const float f = exp2_approx(ml_of(i).x - top);
+#pragma unroll
+                  for (int e = 0; e < 32; e += 4) {
+                    const float4 x = __ldcg(part_of(slot_of(i), 8 * c + e / 4));
+                    v[e] += x.x * f, v[e + 1] += x.y * f, v[e + 2] += x.z * f, v[e + 3] += x.w * f;
+                  }
+                }
+                rows_out(c, v, all_inv);
+              }
+              lse_out(top, sum);
+            }
+          }
         }
-        stage_it += q.take;
-      } while (next_part(q));
-    } else if (warp < 12) {
+        if (!more) break;
+      }
+      if (cta_abort.raised()) {  // the products still running end before the TMEM goes
+        if ((warp & 3) == 0 && elect_one()) {  // (the thread that issued them)
+          umma_commit(bar(sh.drain[t]));
+          mbar_drain(bar(sh.drain[t]), 0, p.wait_limit_ns);
+        }
+        __syncwarp();
+      }
+    } else {
       // -------------------------------------------------------------- keys and values
       const int r = tid - 256;  // key of the tile
       uint4 kc[D / 32], vc[D / 32];
       uint32_t ks[D / 64], vs[D / 64];  // scale bytes
-      bool ok = false;
-      Part w = q;  // the tile whose loads go out next
+      // the next tiles' places: of the tile whose K, then V, is loaded next, and
+      // the page of the tile behind it
+      PrePart w = q;
       int wj = 0;
-      bool more = true;
-      auto load = [&]() {
-        // codes and scales of this thread's key of tile wj of part w
+      bool more = true;  // the next tile to look up exists
+      const uint8_t* blk = nullptr;  // this thread's key's block (null: not there)
+      auto look_up = [&](const uint8_t*& at) -> bool {  // tile wj of part w; then on to the next
+        at = nullptr;
+        if (!more) return false;
         const int key = (w.item.kt0 + w.o + wj) * kPreKeys + r;
-        ok = key < w.item.hi;
-        const uint8_t* blk = nullptr;
-        if (ok) {
-          const int page = __ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride +
-                                 key / a.page_size);
-          ok = page >= 0 && page < a.num_pages;
-          if (!ok && a.status) atomicOr(a.status, kStatusBadSlot);
-          const int in = key % a.page_size;
-          blk = a.cache + ((static_cast<long long>(page) * a.num_kv_heads + w.h) * (a.page_size / 16) +
-                           in / 16) * B::kBytes;
-        }
-        if (ok) {
-          const int i = key & 15;
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            kc[c] = __ldg(reinterpret_cast<const uint4*>(blk + B::kK + i * B::kCodeRow) + c);
-            vc[c] = __ldg(reinterpret_cast<const uint4*>(blk + B::kV + i * B::kCodeRow) + c);
-          }
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            ks[c] = __ldg(reinterpret_cast<const uint32_t*>(blk + B::kKScale + i * B::kScaleRow) + c);
-            vs[c] = __ldg(reinterpret_cast<const uint32_t*>(blk + B::kVScale + i * B::kScaleRow) + c);
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) kc[c] = vc[c] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) ks[c] = vs[c] = 0;
+        if (key < w.item.hi) {
+          const int pg = key / a.page_size, in = key - pg * a.page_size;
+          const int page = __ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride + pg);
+          if (page >= 0 && page < a.num_pages)
+            at = a.cache + ((static_cast<long long>(page) * a.num_kv_heads + w.h) * (a.page_size / 16) +
+                            in / 16) * B::kBytes;
+          else if (a.status)
+            atomicOr(a.status, kStatusBadSlot);
         }
         if (++wj == w.take) {
           wj = 0;
           more = next_part(w);
         }
+        return true;
+      };
+      const int key16 = r & 15;
+      auto load = [&](uint4 (&codes)[D / 32], uint32_t (&scales)[D / 64], int c0, int s0) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+          codes[c] = blk ? __ldg(reinterpret_cast<const uint4*>(blk + c0 + key16 * B::kCodeRow) + c)
+                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          scales[c] = blk ? __ldg(reinterpret_cast<const uint32_t*>(blk + s0 + key16 * B::kScaleRow) + c)
+                          : 0u;
       };
       auto put = [&](unsigned char* tile, const uint4 (&codes)[D / 32], const uint32_t (&scales)[D / 64]) {
 #pragma unroll
@@ -595,10 +809,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
         }
       };
-      load();
-      uint32_t it = 0;
-      long long left = u_end - u0;
-      for (; left > 0; --left, ++it) {
+      look_up(blk);
+      load(kc, ks, B::kK, B::kKScale);
+      load(vc, vs, B::kV, B::kVScale);
+      bool ok = blk != nullptr;
+      const uint8_t* next;
+      bool here = true, behind = look_up(next);  // this tile and the next exist
+      for (uint32_t it = 0; here; ++it) {
         const int st = it & 1;
         if (it >= 2) cta_abort.wait(bar(sh.k_empty[st]), ((it >> 1) - 1) & 1);
         __syncwarp();
@@ -608,6 +825,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         fence_proxy_async();
         __syncwarp();
         mbar_arrive(bar(sh.k_full[st]));
+        blk = next;  // the next tile's K is on its way while V is written
+        ok = blk != nullptr;
+        load(kc, ks, B::kK, B::kKScale);
         if (it >= 2) cta_abort.wait(bar(sh.v_empty[st]), ((it >> 1) - 1) & 1);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)  // a NaN scale must not reach rows that do not see its key
@@ -620,80 +840,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         put(smem + kOffV + st * kTile, vc, vs);
         fence_proxy_async();
         mbar_arrive(bar(sh.v_full[st]));
-        if (more) load();
-      }
-    } else {
-      // -------------------------------------------------------------- products
-      uint32_t it = 0, nq[2] = {0, 0}, np[2] = {0, 0};
-      auto scores = [&](int t, int st) {
-        if (lane == 0 && !cta_abort.raised()) {
-          const uint32_t sq = sbase + t * kTile, sk = sbase + kOffK + st * kTile;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kAtom + (kk & 3) * 32;
-            umma_f16(taddr + kColS + t * kPreKeys, umma_desc_sw128(sq + off, 16, 1024),
-                     umma_desc_sw128(sk + off, 16, 1024), kIdescS, kk != 0 ? 1u : 0u);
-          }
-          umma_commit(bar(sh.s_full[t]));
-        }
-        __syncwarp();
-      };
-      do {
-        const int nact = live_rows(q) > 128 ? 2 : 1;
-        for (int t = 0; t < nact; ++t) {
-          cta_abort.wait(bar(sh.q_full[t]), nq[t] & 1);
-          ++nq[t];
-        }
-        cta_abort.wait(bar(sh.k_full[it & 1]), (it >> 1) & 1);
-        __syncwarp();
-        tc_fence_after();
-        for (int t = 0; t < nact; ++t) scores(t, it & 1);
-        if (lane == 0 && !cta_abort.raised()) umma_commit(bar(sh.k_empty[it & 1]));
-        for (int j = 0; j < q.take; ++j, ++it) {
-          const int st = it & 1;
-          for (int t = 0; t < nact; ++t) {
-            cta_abort.wait(bar(sh.p_full[t]), np[t] & 1);
-            ++np[t];
-            if (t == 0) cta_abort.wait(bar(sh.v_full[st]), (it >> 1) & 1);
-            __syncwarp();
-            tc_fence_after();
-            if (lane == 0 && !cta_abort.raised()) {
-              const uint32_t sv = sbase + kOffV + st * kTile;
-#pragma unroll
-              for (int kk = 0; kk < kPreKeys / 16; ++kk)
-                umma_f16_ts(taddr + kColO + t * D, taddr + kColS + t * kPreKeys + 8 * kk,
-                            umma_desc_sw128(sv + kk * 16 * 128, kAtom, 1024), kIdescO,
-                            (j | kk) != 0 ? 1u : 0u);
-              umma_commit(bar(sh.o_full[t]));
-              if (t == nact - 1) umma_commit(bar(sh.v_empty[st]));
-            }
-            __syncwarp();
-            if (j + 1 < q.take) {
-              const uint32_t nx = it + 1;
-              if (t == 0) {
-                cta_abort.wait(bar(sh.k_full[nx & 1]), (nx >> 1) & 1);
-                __syncwarp();
-                tc_fence_after();
-              }
-              scores(t, nx & 1);
-              if (t == nact - 1 && lane == 0 && !cta_abort.raised()) umma_commit(bar(sh.k_empty[nx & 1]));
-            }
-          }
-        }
-      } while (next_part(q));
-      if (cta_abort.raised()) {  // the products still running end before the TMEM goes
-        if (lane == 0) {
-          umma_commit(bar(sh.drain));
-          mbar_drain(bar(sh.drain), 0, p.wait_limit_ns);
-        }
-        __syncwarp();
+        load(vc, vs, B::kV, B::kVScale);
+        here = behind;
+        behind = look_up(next);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 12)
+  if (warp == 8)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(kCols)
                  : "memory");
   if (tid == 0 && cta_abort.raised() && a.status) atomicOr(a.status, kStatusTimeout);
@@ -729,7 +885,7 @@ int launch_kv4_prefill(const Kv4AttnArgs& a, int max_packed_rows, bool f16, cuda
   p.a = a;
   char* w = static_cast<char*>(a.workspace);
   p.counters = reinterpret_cast<uint32_t*>(w);
-  p.part_o = reinterpret_cast<float*>(w + kPreCounterBytes + kv4_decode_counter_bytes());
+  p.part_o = reinterpret_cast<float4*>(w + kPreCounterBytes + kv4_decode_counter_bytes());
   p.part_ml = reinterpret_cast<float2*>(reinterpret_cast<char*>(p.part_o) +
                                         static_cast<size_t>(2) * kPreCtasMax * kPreRows * a.head_dim * 4);
   p.max_packed_rows = max_packed_rows;

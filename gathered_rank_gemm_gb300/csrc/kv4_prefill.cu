@@ -35,7 +35,7 @@ constexpr int kPreCtasMax = 160;  // CTAs that the workspace has room for
 constexpr int kPreRows = 256;     // packed rows of an item
 constexpr int kPreKeys = 128;     // keys of a tile
 // What the line counts: a key tile of two row tiles, of one, and an item's start and end.
-constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 4;
+constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 12;
 constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
 constexpr float kPreLog2e = 1.4426950408889634f;
 constexpr float kPreLn2 = 0.6931471805599453f;
@@ -58,11 +58,11 @@ struct PreItem {
   __device__ __forceinline__ int size() const { return kCostItem + nt * cost; }
 };
 __device__ __forceinline__ PreItem pre_item(const Kv4Seq& s, int group, int rt, int window) {
-  const int rows = static_cast<int>(min(static_cast<long long>(s.take) * group -
-                                            static_cast<long long>(rt) * kPreRows,
-                                        static_cast<long long>(kPreRows)));
-  const int i0 = static_cast<int>(static_cast<long long>(rt) * kPreRows / group);
-  const int i1 = static_cast<int>((static_cast<long long>(rt) * kPreRows + rows - 1) / group);
+  // (packed rows fit 32 bits: 2^22 tokens of 2^8 heads)
+  const uint32_t first = static_cast<uint32_t>(rt) * kPreRows;
+  const uint32_t rows = min(static_cast<uint32_t>(s.take * group) - first, static_cast<uint32_t>(kPreRows));
+  const int i0 = static_cast<int>(first / static_cast<uint32_t>(group));
+  const int i1 = static_cast<int>((first + rows - 1) / static_cast<uint32_t>(group));
   const int hi = s.pos(i1) + 1, lo = s.first_key(i0, window);
   PreItem it;
   it.kt0 = lo / kPreKeys;
@@ -252,10 +252,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   // ---- the line of units (key tiles): a prefix sum over the threads' runs of sequences
   const int per_thread = (a.num_seqs + kPreThreads - 1) / kPreThreads;
   auto mine_of = [&](const Kv4Seq& s) {
-    return static_cast<long long>(s.take) * group > p.max_packed_rows;
+    return s.take * group > p.max_packed_rows;
   };
   auto tiles_of = [&](const Kv4Seq& s) {
-    return static_cast<int>((static_cast<long long>(s.take) * group + kPreRows - 1) / kPreRows);
+    return (s.take * group + kPreRows - 1) / kPreRows;
   };
   auto head_units = [&](const Kv4Seq& s) -> long long {  // units of one key head
     long long n = 0;
@@ -306,9 +306,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   auto set_part = [&](PrePart& q) {
     q.item = pre_item(q.seq, group, q.rt, a.window);
     auto tiles_before = [&](long long x) {  // tiles that begin before place x
-      const long long n = x - q.at - kCostItem;
-      return n <= 0 ? 0 : static_cast<int>(min((n + q.item.cost - 1) / q.item.cost,
-                                               static_cast<long long>(q.item.nt)));
+      const long long far = x - q.at - kCostItem;
+      if (far <= 0) return 0;
+      const uint32_t n = far > (1 << 30) ? 1u << 30 : static_cast<uint32_t>(far);
+      const uint32_t k = q.item.cost == kCostTwo ? (n + kCostTwo - 1) / kCostTwo : (n + kCostOne - 1) / kCostOne;
+      return min(static_cast<int>(k), q.item.nt);
     };
     q.o = tiles_before(sh.u0);
     q.take = tiles_before(sh.u_end) - q.o;
@@ -360,8 +362,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     return q.take > 0 || next_part(q);
   };
   auto live_rows = [&](const PrePart& q) {
-    return static_cast<int>(min(static_cast<long long>(q.seq.take) * group - static_cast<long long>(q.rt) * kPreRows,
-                                static_cast<long long>(kPreRows)));
+    return min(q.seq.take * group - q.rt * kPreRows, kPreRows);
   };
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
 
@@ -448,7 +449,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         // a row's reads are neighbours
         constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, PASSES = 32 / AT_ONCE;
         unsigned char* tile = smem + t * kTile;
-        float down = 0.0f;
+        float down = 1.0f;  // (fp16 rows need no factor)
         uint4 raw_q[PASSES];
 #pragma unroll
         for (int i2 = 0; i2 < PASSES; ++i2) {
@@ -461,25 +462,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 #pragma unroll
         for (int i2 = 0; i2 < PASSES; ++i2) {
           const int r = i2 * AT_ONCE + lane / LANES, c = lane % LANES;
-          const uint32_t y[4] = {raw_q[i2].x, raw_q[i2].y, raw_q[i2].z, raw_q[i2].w};
-          float2 f[4];
-          float top = 0.0f;
+          uint32_t z[4] = {raw_q[i2].x, raw_q[i2].y, raw_q[i2].z, raw_q[i2].w};
+          if constexpr (!F16) {
+            // the row's largest magnitude, as 16-bit patterns (they order like the numbers)
+            uint32_t top = __vmaxu2(__vmaxu2(z[0] & 0x7FFF7FFFu, z[1] & 0x7FFF7FFFu),
+                                    __vmaxu2(z[2] & 0x7FFF7FFFu, z[3] & 0x7FFF7FFFu));
+            top = max(top >> 16, top & 0xFFFFu);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[e] = unpack_t<F16>(y[e]);
-            top = fmaxf(top, fmaxf(fabsf(f[e].x), fabsf(f[e].y)));
+            for (int sft = LANES / 2; sft; sft >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, sft));
+            float up, dn;
+            row_factor(__uint_as_float(top << 16), up, dn);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack_bf16x2(z[e]);
+              z[e] = pack_f16x2(f.x * up, f.y * up);
+            }
+            dn = __shfl_sync(0xffffffffu, dn, (lane % AT_ONCE) * LANES);
+            if (lane / AT_ONCE == i2) down = dn;
           }
-#pragma unroll
-          for (int sft = LANES / 2; sft; sft >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, sft));
-          float up, dn;
-          row_factor(top, up, dn);
-          uint32_t z[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[e] = pack_f16x2(f[e].x * up, f[e].y * up);
           *reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + swz128((warp & 3) * 32 + r, c & 7)) =
               make_uint4(z[0], z[1], z[2], z[3]);
-          dn = __shfl_sync(0xffffffffu, dn, (lane % AT_ONCE) * LANES);
-          if (lane / AT_ONCE == i2) down = dn;
         }
         x.cf = down * (a.score_scale * kPreLog2e);
         fence_proxy_async();
@@ -638,6 +640,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           unsigned char* staged = sh.staged[warp];
           // 32 dimensions of the warp's 32 rows: through shared memory, so that a
           // row's stores are neighbours (8 rows of 64 bytes at a time)
+          uint16_t* dst[4];
+#pragma unroll
+          for (int i2 = 0; i2 < 4; ++i2) {
+            const int r = 8 * i2 + (lane >> 2);
+            const long long tok = __shfl_sync(0xffffffffu, out.tok, r);
+            const int head = __shfl_sync(0xffffffffu, out.head, r);
+            const bool store = __shfl_sync(0xffffffffu, out.live ? 1 : 0, r) && !cta_abort.raised();
+            dst[i2] = store ? a.out + tok * a.out_stride + head * D + 8 * (lane & 3) : nullptr;
+          }
           auto rows_out = [&](int c, const float (&v)[32], float inv) {
             unsigned char* mine_s = staged + lane * kStagePitch;
 #pragma unroll
@@ -652,13 +663,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             __syncwarp();
 #pragma unroll
             for (int i2 = 0; i2 < 4; ++i2) {
-              const int r = 8 * i2 + (lane >> 2);
-              const long long tok = __shfl_sync(0xffffffffu, out.tok, r);
-              const int head = __shfl_sync(0xffffffffu, out.head, r);
-              const bool store = __shfl_sync(0xffffffffu, out.live ? 1 : 0, r) && !cta_abort.raised();
-              const uint4 w = *reinterpret_cast<const uint4*>(staged + r * kStagePitch + 16 * (lane & 3));
-              if (store)
-                *reinterpret_cast<uint4*>(a.out + tok * a.out_stride + head * D + 32 * c + 8 * (lane & 3)) = w;
+              const uint4 w = *reinterpret_cast<const uint4*>(staged + (8 * i2 + (lane >> 2)) * kStagePitch +
+                                                              16 * (lane & 3));
+              if (dst[i2]) *reinterpret_cast<uint4*>(dst[i2] + 32 * c) = w;
             }
             __syncwarp();
           };

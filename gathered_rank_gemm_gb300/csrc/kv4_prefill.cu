@@ -82,8 +82,9 @@ struct PrePart {
 
 // Shared memory behind the operand tiles.
 struct PreShared {
-  uint64_t s_full[2], o_full[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+  uint64_t s_full[2];     // a tile's scores are there
+  uint64_t o_done[2][2];  // [tile][stage]: its second product on that stage is done
+  uint64_t k_full[2], v_full[2];
   uint64_t drain[2];
   // keys of a tile that exist; four tiles deep: a tile's words are rewritten only
   // after both softmaxes have taken the tile two further on
@@ -226,11 +227,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s_full[i]), 1);
-      mbar_init(smem_u32(&sh.o_full[i]), 1);
+      mbar_init(smem_u32(&sh.o_done[0][i]), 1);
+      mbar_init(smem_u32(&sh.o_done[1][i]), 1);
       mbar_init(smem_u32(&sh.k_full[i]), 128 + (p.wait_fault ? 1 : 0));
-      mbar_init(smem_u32(&sh.k_empty[i]), 2);
       mbar_init(smem_u32(&sh.v_full[i]), 128);
-      mbar_init(smem_u32(&sh.v_empty[i]), 2);
     }
     mbar_init(smem_u32(&sh.drain[0]), 1);
     mbar_init(smem_u32(&sh.drain[1]), 1);
@@ -376,44 +376,43 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const uint32_t tS = taddr + lane_base + kColS + t * kPreKeys;
       const uint32_t tO = taddr + lane_base + kColO + t * D;
       const uint32_t sS = taddr + kColS + t * kPreKeys, sO = taddr + kColO + t * D;
-      uint32_t ns = 0, no = 0;  // first products, and second ones, of this tile so far
-      uint32_t it = 0;  // key tiles so far (the stages of K and V)
+      uint32_t ns = 0;          // first products of this tile so far
+      uint32_t no[2] = {0, 0};  // and second ones, by stage
+      uint32_t it = 0;          // key tiles so far (the stages of K and V)
       // The products, issued by one thread of the tile's first warp, in the order
       // S(0), O(0), S(1), O(1), ...: the tensor core takes one tile's in turn, so S
       // never overwrites a P still to be read.  A key tile's stages of K and V are free
       // when the second products of both tiles (all that are active) are done: until
       // then its scores can be formed once more.
-      auto scores = [&](uint32_t i) {  // of key tile i
-        const uint32_t st = __shfl_sync(0xffffffffu, i & 1, 0);
-        if (!__all_sync(0xffffffffu, cta_abort.wait(bar(sh.k_full[st]), (i >> 1) & 1))) return;
-        tc_fence_after();
+      auto scores = [&](uint32_t st) {  // on stage st
         const uint64_t dq = umma_desc_sw128(sbase + t * kTile, 16, 1024);
         const uint64_t dk = umma_desc_sw128(sbase + kOffK + st * kTile, 16, 1024);
-        if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {  // (addresses count in 16 bytes)
-            const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
-            umma_f16(sS, dq + off, dk + off, kIdescS, kk != 0 ? 1u : 0u);
-          }
-          umma_commit(bar(sh.s_full[t]));
+        for (int kk = 0; kk < D / 16; ++kk) {  // (addresses count in 16 bytes)
+          const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
+          umma_f16(sS, dq + off, dk + off, kIdescS, kk != 0 ? 1u : 0u);
         }
+        umma_commit(bar(sh.s_full[t]));
       };
-      auto values = [&](uint32_t i, bool add, int nact) {
-        const uint32_t st = __shfl_sync(0xffffffffu, i & 1, 0);
-        if (!__all_sync(0xffffffffu, cta_abort.wait(bar(sh.v_full[st]), (i >> 1) & 1))) return;
-        tc_fence_after();
+      auto values = [&](uint32_t st, bool add) {
         const uint64_t dv = umma_desc_sw128(sbase + kOffV + st * kTile, kAtom, 1024);
-        if (elect_one()) {
-          umma_f16_ts(sO, sS, dv, kIdescO, add ? 1u : 0u);
+        umma_f16_ts(sO, sS, dv, kIdescO, add ? 1u : 0u);
 #pragma unroll
-          for (int kk = 1; kk < kPreKeys / 16; ++kk)
-            umma_f16_ts(sO, sS + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdescO, 1u);
-          umma_commit(bar(sh.o_full[t]));
-          for (int c = nact; c <= 2; ++c) {
-            umma_commit(bar(sh.k_empty[st]));
-            umma_commit(bar(sh.v_empty[st]));
-          }
-        }
+        for (int kk = 1; kk < kPreKeys / 16; ++kk)
+          umma_f16_ts(sO, sS + 8 * kk, dv + ((kk * 16 * 128) >> 4), kIdescO, 1u);
+        umma_commit(bar(sh.o_done[t][st]));
+      };
+      auto have_k = [&](uint32_t i) {
+        return __all_sync(0xffffffffu, cta_abort.wait(bar(sh.k_full[i & 1]), (i >> 1) & 1));
+      };
+      auto have_v = [&](uint32_t i) {
+        return __all_sync(0xffffffffu, cta_abort.wait(bar(sh.v_full[i & 1]), (i >> 1) & 1));
+      };
+      // waits for the second product on stage st that was issued last
+      auto settled = [&](uint32_t st) {
+        cta_abort.wait(bar(sh.o_done[t][st]), ((st ? no[1] : no[0]) - 1) & 1);
+        __syncwarp();
+        tc_fence_after();
       };
       // This thread's row of a part.
       struct Row {
@@ -486,7 +485,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         x.cf = down * (a.score_scale * kPreLog2e);
         fence_proxy_async();
         pre_barrier(2 + t, 128);
-        if ((warp & 3) == 0) scores(it);
+        if ((warp & 3) == 0 && have_k(it)) {
+          tc_fence_after();
+          const uint32_t st = __shfl_sync(0xffffffffu, it & 1, 0);
+          if (elect_one()) scores(st);
+        }
         __syncwarp();
         return x;
       };
@@ -544,9 +547,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               mx *= row.cf;
               if (__any_sync(0xffffffffu, mx > m && m != kPreNoKey)) {
                 // O takes the new reference
-                cta_abort.wait(bar(sh.o_full[t]), (no - 1) & 1);
-                __syncwarp();
-                tc_fence_after();
+                settled((it + j + 1) & 1);
                 const float f = exp2_approx(m - fmaxf(m, mx));
                 l0 *= f, l1 *= f;
 #pragma unroll 1
@@ -583,21 +584,30 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               }
               tmem_st16(tS + 16 * c, w);
             }
+            // what the products need is waited for while the other warps finish
+            const bool ready = (warp & 3) != 0 || (have_v(it + j) && (j + 1 == take || have_k(it + j + 1)));
             tmem_wait_st();
             tc_fence_before();
             // the tile's P is there, or some row wants it again
             again = pre_barrier_any(2 + t, 128, mx * row.cf > m + 15.0f);
+            if ((warp & 3) == 0 && ready) {
+              tc_fence_after();
+              const uint32_t st = __shfl_sync(0xffffffffu, (it + j) & 1, 0);
+              const bool add = j > 0, more_keys = j + 1 < take;
+              if (elect_one()) {
+                if (again) {
+                  scores(st);
+                } else {
+                  values(st, add);
+                  if (more_keys) scores(st ^ 1);
+                }
+              }
+            }
+            __syncwarp();
             if (!again) break;
             l0 = l0_was, l1 = l1_was;
-            if ((warp & 3) == 0) scores(it + j);
-            __syncwarp();
           }
-          if ((warp & 3) == 0) {
-            values(it + j, j > 0, row.nact);
-            if (j + 1 < take) scores(it + j + 1);
-          }
-          __syncwarp();
-          ++no;
+          if ((it + j) & 1) ++no[1]; else ++no[0];
         }
         // ---- the next part starts (neither tile's warps run ahead by a part);
         // while its first product runs, this one's rows go out
@@ -617,9 +627,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (on) {
           const Place out = place(done);
           const float l = l0 + l1;
-          cta_abort.wait(bar(sh.o_full[t]), (no - 1) & 1);
-          __syncwarp();
-          tc_fence_after();
+          settled((it - 1) & 1);
           uint32_t nan_blocks = 0;  // 16-dimension blocks with a NaN scale at a key of the row
           if (*reinterpret_cast<volatile int*>(&sh.poison)) {
             const int32_t* table = a.page_table + static_cast<long long>(done.b) * a.table_stride;
@@ -769,9 +777,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       int wj = 0;
       bool more = true;  // the next tile to look up exists
       const uint8_t* blk = nullptr;  // this thread's key's block (null: not there)
-      auto look_up = [&](const uint8_t*& at) -> bool {  // tile wj of part w; then on to the next
+      uint32_t tiles = 0;  // two bits for this key tile, two for the next
+      auto look_up = [&](const uint8_t*& at, int shift) -> bool {  // tile wj of part w; then on to the next
         at = nullptr;
         if (!more) return false;
+        tiles |= (live_rows(w) > 128 ? 3u : 1u) << shift;
         const int key = (w.item.kt0 + w.o + wj) * kPreKeys + r;
         if (key < w.item.hi) {
           const int pg = key / a.page_size, in = key - pg * a.page_size;
@@ -816,16 +826,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
         }
       };
-      look_up(blk);
+      look_up(blk, 0);
       load(kc, ks, B::kK, B::kKScale);
       load(vc, vs, B::kV, B::kVScale);
       bool ok = blk != nullptr;
       const uint8_t* next;
-      bool here = true, behind = look_up(next);  // this tile and the next exist
+      bool here = true, behind = look_up(next, 2);  // this tile and the next exist
+      // by stage and tile: whether the tile's product on it is to be waited for, and
+      // the parity of how many there were
+      uint32_t used = 0, uses = 0;
       for (uint32_t it = 0; here; ++it) {
         const int st = it & 1;
-        if (it >= 2) cta_abort.wait(bar(sh.k_empty[st]), ((it >> 1) - 1) & 1);
+        // both tiles' products on what the stages held are done
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          if ((used >> (2 * st + t)) & 1u) cta_abort.wait(bar(sh.o_done[t][st]), ((uses >> (2 * st + t)) & 1u) ^ 1u);
         __syncwarp();
+        used = (used & ~(3u << (2 * st))) | ((tiles & 3u) << (2 * st));
+        uses ^= (tiles & 3u) << (2 * st);
+        tiles >>= 2;
         const uint32_t votes = __ballot_sync(0xffffffffu, ok);
         put(smem + kOffK + st * kTile, kc, ks);
         if (lane == 0) sh.valid[it & 3][warp - 8] = votes;
@@ -835,7 +854,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         blk = next;  // the next tile's K is on its way while V is written
         ok = blk != nullptr;
         load(kc, ks, B::kK, B::kKScale);
-        if (it >= 2) cta_abort.wait(bar(sh.v_empty[st]), ((it >> 1) - 1) & 1);
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)  // a NaN scale must not reach rows that do not see its key
 #pragma unroll
@@ -849,7 +867,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         mbar_arrive(bar(sh.v_full[st]));
         load(vc, vs, B::kV, B::kVScale);
         here = behind;
-        behind = look_up(next);
+        behind = look_up(next, 2);
       }
     }
   }

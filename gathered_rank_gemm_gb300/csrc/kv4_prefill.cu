@@ -498,15 +498,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (lane == 0) sh.part[warp][0] = q;
       __syncwarp();
       while (true) {
-        float m = kPreNoKey, l0 = 0.0f, l1 = 0.0f;
+        float m = kPreNoKey, l = 0.0f;
         const bool on = t < row.nact;
         for (int j = 0; on && j < take; ++j) {
           const int key0 = first_key + j * kPreKeys;
           const int hi_j = row.pos - key0, lo_j = row.lo - key0;
           // p = 2^(s c - m) against the running reference m, in one pass over S, 32
-          // keys at a time; where some score passes m by 2^15 (fp16 would end) the
-          // tile is done again with m moved, and so is a part's first tile
-          const float l0_was = l0, l1_was = l1;
+          // keys at a time.  The tile's sum tells whether m still serves: above 2^15
+          // some p may pass what fp16 holds, and the tile is done again with m moved.
+          // A part's first tile looks for its maximum at once.
           bool again = j == 0;
           while (true) {
             cta_abort.wait(bar(sh.s_full[t]), ns & 1);
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 // O takes the new reference
                 settled((it + j + 1) & 1);
                 const float f = exp2_approx(m - fmaxf(m, mx));
-                l0 *= f, l1 *= f;
+                l *= f;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                   uint32_t r[32];
@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               }
               m = fmaxf(m, mx);
             }
-            float mx = -INFINITY;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             uint32_t v[2][32];
             tmem_ld32_start(tS, v[0]);
 #pragma unroll
@@ -572,24 +572,31 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               tmem_ld32_wait(x);
               if (c < 3) tmem_ld32_start(tS + 32 * (c + 1), v[(c + 1) & 1]);
               if (masked) hide(c, x);
-              mx = top_of(mx, x);
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 float y, z;
                 fma2(y, z, x[e], x[e + 1], row.cf, -m);
                 y = exp2_approx(y), z = exp2_approx(z);
-                add2(l0, l1, y, z);
+                add2(sum[e & 2], sum[(e & 2) + 1], y, z);
                 w[e / 2] = pack_f16x2(y, z);
               }
               tmem_st16(tS + 16 * c, w);
             }
+            const float tile_sum = (sum[0] + sum[1]) + (sum[2] + sum[3]);
             // what the products need is waited for while the other warps finish
-            const bool ready = (warp & 3) != 0 || (have_v(it + j) && (j + 1 == take || have_k(it + j + 1)));
+            bool ready = true;
+            if ((warp & 3) == 0) {
+              const uint32_t i = it + j;
+              const bool v_there = mbar_try_wait(bar(sh.v_full[i & 1]), (i >> 1) & 1);
+              const bool k_there = j + 1 == take || mbar_try_wait(bar(sh.k_full[(i + 1) & 1]), ((i + 1) >> 1) & 1);
+              ready = v_there && k_there;
+              if (!__all_sync(0xffffffffu, ready)) ready = have_v(i) && (j + 1 == take || have_k(i + 1));
+            }
             tmem_wait_st();
             tc_fence_before();
             // the tile's P is there, or some row wants it again
-            again = pre_barrier_any(2 + t, 128, mx * row.cf > m + 15.0f);
+            again = pre_barrier_any(2 + t, 128, tile_sum > 32768.0f);
             if ((warp & 3) == 0 && ready) {
               tc_fence_after();
               const uint32_t st = __shfl_sync(0xffffffffu, (it + j) & 1, 0);
@@ -604,8 +611,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               }
             }
             __syncwarp();
-            if (!again) break;
-            l0 = l0_was, l1 = l1_was;
+            if (!again) {
+              l += tile_sum;
+              break;
+            }
           }
           if ((it + j) & 1) ++no[1]; else ++no[0];
         }
@@ -626,7 +635,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (on) {
           const Place out = place(done);
-          const float l = l0 + l1;
           settled((it - 1) & 1);
           uint32_t nan_blocks = 0;  // 16-dimension blocks with a NaN scale at a key of the row
           if (*reinterpret_cast<volatile int*>(&sh.poison)) {
@@ -771,32 +779,39 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const int r = tid - 256;  // key of the tile
       uint4 kc[D / 32], vc[D / 32];
       uint32_t ks[D / 64], vs[D / 64];  // scale bytes
-      // the next tiles' places: of the tile whose K, then V, is loaded next, and
-      // the page of the tile behind it
+      // the walk over the key tiles: two ahead, a tile's page is asked for (and
+      // nothing waits for it); one ahead, its codes and scales
       PrePart w = q;
       int wj = 0;
       bool more = true;  // the next tile to look up exists
       const uint8_t* blk = nullptr;  // this thread's key's block (null: not there)
+      const int page_blocks = a.page_size / 16;
+      const long long page_bytes = static_cast<long long>(a.num_kv_heads) * page_blocks * B::kBytes;
       uint32_t tiles = 0;  // two bits for this key tile, two for the next
-      auto look_up = [&](const uint8_t*& at, int shift) -> bool {  // tile wj of part w; then on to the next
-        at = nullptr;
+      int page = -1, in_page = 0;  // of this thread's key in the tile looked up last; -2: no such key
+      auto look_up = [&](int shift) -> bool {  // tile wj of part w; then on to the next
+        page = -2;
         if (!more) return false;
         tiles |= (live_rows(w) > 128 ? 3u : 1u) << shift;
         const int key = (w.item.kt0 + w.o + wj) * kPreKeys + r;
         if (key < w.item.hi) {
           const int pg = key / a.page_size, in = key - pg * a.page_size;
-          const int page = __ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride + pg);
-          if (page >= 0 && page < a.num_pages)
-            at = a.cache + ((static_cast<long long>(page) * a.num_kv_heads + w.h) * (a.page_size / 16) +
-                            in / 16) * B::kBytes;
-          else if (a.status)
-            atomicOr(a.status, kStatusBadSlot);
+          page = max(__ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride + pg), -1);
+          in_page = (w.h * page_blocks + in / 16) * B::kBytes;
         }
         if (++wj == w.take) {
           wj = 0;
           more = next_part(w);
         }
         return true;
+      };
+      auto block = [&]() -> const uint8_t* {  // of the key looked up last
+        if (page == -2) return nullptr;
+        if (page < 0 || page >= a.num_pages) {
+          if (a.status) atomicOr(a.status, kStatusBadSlot);
+          return nullptr;
+        }
+        return a.cache + page * page_bytes + in_page;
       };
       const int key16 = r & 15;
       auto load = [&](uint4 (&codes)[D / 32], uint32_t (&scales)[D / 64], int c0, int s0) {
@@ -826,12 +841,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
         }
       };
-      look_up(blk, 0);
+      look_up(0);
+      blk = block();
       load(kc, ks, B::kK, B::kKScale);
       load(vc, vs, B::kV, B::kVScale);
       bool ok = blk != nullptr;
-      const uint8_t* next;
-      bool here = true, behind = look_up(next, 2);  // this tile and the next exist
+      bool here = true, behind = look_up(2);  // this tile and the next exist
       // by stage and tile: whether the tile's product on it is to be waited for, and
       // the parity of how many there were
       uint32_t used = 0, uses = 0;
@@ -851,7 +866,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         fence_proxy_async();
         __syncwarp();
         mbar_arrive(bar(sh.k_full[st]));
-        blk = next;  // the next tile's K is on its way while V is written
+        blk = block();  // the next tile's K is on its way while V is written
         ok = blk != nullptr;
         load(kc, ks, B::kK, B::kKScale);
 #pragma unroll
@@ -867,7 +882,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         mbar_arrive(bar(sh.v_full[st]));
         load(vc, vs, B::kV, B::kVScale);
         here = behind;
-        behind = look_up(next, 2);
+        behind = look_up(2);
       }
     }
   }

@@ -8,20 +8,28 @@
 // fp16, from where the second product reads it.  The codes times their e4m3
 // scales are exact in fp16, so only P is rounded.
 //
-// Warp roles (13 warps, one CTA per SM, persistent):
-//  - warps 0-3 and 4-7, softmax of tile 0 and 1: a thread owns a row.  It writes
-//    the row's q (scaled by a power of two into fp16's range) to shared memory,
-//    then per key tile reads S, forms p with the running maximum (moved, and O
-//    rescaled, only when a row's scores exceed it by 2^6 or more, which almost never
-//    happens after the first tile) and stores P; at the end it writes the row of O.
+// Warp roles (12 warps of 168 registers, one CTA per SM, persistent):
+//  - warps 0-3 and 4-7, softmax of tile 0 and 1: a thread owns a row.  Per key tile
+//    it reads S, forms p in one pass against a running reference m (moved, and O
+//    rescaled, only when a tile's sum shows that p may leave fp16's range) and stores
+//    P; then one thread of the tile's first warp issues O += P V and the next S, so
+//    that one tile's products run under the other tile's softmax.  At an item's end the
+//    next item's queries (bf16: scaled by a power of two per row into fp16's range)
+//    and first S come before the rows of O go out.
 //  - warps 8-11, keys and values: a thread owns a key of the tile.  It loads
-//    the key's codes and scales into registers a tile ahead, and writes the fp16
-//    values into the swizzled operand tiles (two stages each for K and V).
-//  - warp 12 issues the products: while tile 0's softmax runs, tile 1's products
-//    do, and the other way round.
+//    the key's codes and scales into registers a tile ahead (the page's number two
+//    ahead), and writes the fp16 values into the swizzled operand tiles (two stages
+//    each for K and V).
 // Work: the key tiles of all items in one line, cut into equal runs, one per CTA;
 // an item that was cut leaves (m, l, O) partials, joined in run order by the last
-// of its CTAs to finish (as in kv4_decode.cu).
+// of its CTAs to finish (as in kv4_decode.cu).  Short items stay whole.
+//
+// Measured (GB300, bf16): 6 chunks of 700 to 2000 rows over 2000 to 5000 keys, 32 / 8
+// heads of 128: 333 us, 1033 TFLOP/s (0.54 of measured); one prompt of 8192 tokens,
+// 32 / 32 heads: 480 us, 1146 TFLOP/s.  Bound by the chain softmax (1250 cycles a tile of
+// 128 x 128), barrier and issue (200), two products (1024 at the tensor core's rate,
+// 1550 until S can be read): 3490 cycles for two tiles, whose products alone take
+// 2048.  An item's start and end cost about four key tiles.
 #include "kv4_attention.cuh"
 #include "kv4_attention.h"
 #include "launch.h"
@@ -36,6 +44,7 @@ constexpr int kPreRows = 256;     // packed rows of an item
 constexpr int kPreKeys = 128;     // keys of a tile
 // What the line counts: a key tile of two row tiles, of one, and an item's start and end.
 constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 12;
+constexpr int kWholeTiles = 8;    // an item of so few key tiles is not cut for the sake of idle CTAs
 constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
 constexpr float kPreLog2e = 1.4426950408889634f;
 constexpr float kPreLn2 = 0.6931471805599453f;
@@ -93,9 +102,11 @@ struct PreShared {
   int abort, poison, last;
   PrePart part[8][2];    // the softmax warps' parts (their registers are needed for S)
   long long u0, u_end, per;
+  int whole;  // items are not cut
   __align__(16) unsigned char staged[8][32 * kStagePitch];  // of the softmax warps
-  long long prefix[kPreThreads + 1];
-  long long warp_sum[kPreWarps];
+  long long prefix[2][kPreThreads + 1];  // of the line, and of items
+  long long warp_sum[2][kPreWarps];
+  int most;  // key tiles of the longest item
 };
 
 __device__ __forceinline__ uint32_t pre_hmul2(uint32_t a, uint32_t b) {
@@ -237,6 +248,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     fence_mbar_init();
     sh.abort = 0;
     sh.poison = 0;
+    sh.most = 0;
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
@@ -257,51 +269,69 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   auto tiles_of = [&](const Kv4Seq& s) {
     return (s.take * group + kPreRows - 1) / kPreRows;
   };
-  auto head_units = [&](const Kv4Seq& s) -> long long {  // units of one key head
+  auto head_units = [&](const Kv4Seq& s, int& most) -> long long {  // units of one key head
     long long n = 0;
     if (mine_of(s)) {
       const int nr = tiles_of(s);
-      for (int rt = 0; rt < nr; ++rt) n += pre_item(s, group, rt, a.window).size();
+      for (int rt = 0; rt < nr; ++rt) {
+        const PreItem it = pre_item(s, group, rt, a.window);
+        n += it.size();
+        most = max(most, it.nt);
+      }
     }
     return n;
   };
-  long long mine = 0;
+  long long mine[2] = {0, 0};
+  int most = 0;
   for (int i = 0; i < per_thread; ++i) {
     const int b = tid * per_thread + i;
-    if (b < a.num_seqs) mine += head_units(Kv4Seq::of(a, b)) * a.num_kv_heads;
+    if (b < a.num_seqs) {
+      const Kv4Seq s = Kv4Seq::of(a, b);
+      mine[0] += head_units(s, most) * a.num_kv_heads;
+      if (mine_of(s)) mine[1] += static_cast<long long>(tiles_of(s)) * a.num_kv_heads;
+    }
   }
-  long long run = mine;
+  long long run[2] = {mine[0], mine[1]};
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, run, o);
-    if (lane >= o) run += v;
-  }
-  if (lane == 31) sh.warp_sum[warp] = run;
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long v = __shfl_up_sync(0xffffffffu, run[i], o);
+      if (lane >= o) run[i] += v;
+    }
+  if (lane == 31) sh.warp_sum[0][warp] = run[0], sh.warp_sum[1][warp] = run[1];
+  most = __reduce_max_sync(0xffffffffu, most);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long before = 0, total = 0;
+  if (lane == 0 && most > 0) atomicMax(&sh.most, most);
+  long long all[2] = {0, 0};
 #pragma unroll
-  for (int w = 0; w < kPreWarps; ++w) {
-    if (w < warp) before += sh.warp_sum[w];
-    total += sh.warp_sum[w];
+  for (int i = 0; i < 2; ++i) {
+    long long before = 0;
+#pragma unroll
+    for (int w = 0; w < kPreWarps; ++w) {
+      if (w < warp) before += sh.warp_sum[i][w];
+      all[i] += sh.warp_sum[i][w];
+    }
+    sh.prefix[i][tid] = before + run[i] - mine[i];
+    if (tid == 0) sh.prefix[i][kPreThreads] = all[i];
   }
-  sh.prefix[tid] = before + run - mine;
-  if (tid == 0) sh.prefix[kPreThreads] = total;
   __syncthreads();
   const uint32_t taddr = sh.taddr;
 
-  // (a run is no shorter than a tile, so every run inside an item has one of its tiles)
-  const long long per = max((total + gridDim.x - 1) / static_cast<long long>(gridDim.x),
-                            static_cast<long long>(kCostTwo));
   if (tid == 0) {
-    sh.per = per;
-    sh.u0 = blockIdx.x * per;
-    sh.u_end = min(sh.u0 + per, total);
+    // Short items stay whole where there is a CTA for each: cutting one costs its
+    // join, about as long as kWholeTiles tiles.  Else the line is cut into equal
+    // runs (no shorter than a tile, so every run inside an item has one of its tiles).
+    sh.whole = sh.most <= kWholeTiles && all[1] <= gridDim.x;
+    sh.per = sh.whole ? 1 : max((all[0] + gridDim.x - 1) / static_cast<long long>(gridDim.x),
+                                static_cast<long long>(kCostTwo));
+    sh.u0 = blockIdx.x * sh.per;
+    sh.u_end = min(sh.u0 + sh.per, sh.whole ? all[1] : all[0]);
   }
   __syncthreads();
 
-  // The CTA's parts of items, in order; every role walks the same list.
   // A tile is the run's in which its place begins.
   auto set_part = [&](PrePart& q) {
     q.item = pre_item(q.seq, group, q.rt, a.window);
@@ -312,12 +342,12 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const uint32_t k = q.item.cost == kCostTwo ? (n + kCostTwo - 1) / kCostTwo : (n + kCostOne - 1) / kCostOne;
       return min(static_cast<int>(k), q.item.nt);
     };
-    q.o = tiles_before(sh.u0);
-    q.take = tiles_before(sh.u_end) - q.o;
+    q.o = sh.whole ? 0 : tiles_before(sh.u0);
+    q.take = sh.whole ? q.item.nt : tiles_before(sh.u_end) - q.o;
   };
   auto next_part = [&](PrePart& q) -> bool {
     do {
-      q.at += q.item.size();
+      q.at += sh.whole ? 1 : q.item.size();
       if (q.at >= sh.u_end) return false;
       if (++q.rt == tiles_of(q.seq)) {
         q.rt = 0;
@@ -334,16 +364,17 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   auto first_part = [&](PrePart& q) -> bool {
     const long long u0 = sh.u0;
     if (u0 >= sh.u_end) return false;
-    int lo = 0, hi = kPreThreads;
+    const long long* prefix = sh.prefix[sh.whole ? 1 : 0];
+    int lo = 0, hi = kPreThreads, ignored = 0;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if (sh.prefix[mid] <= u0) lo = mid; else hi = mid;
+      if (prefix[mid] <= u0) lo = mid; else hi = mid;
     }
-    long long off = u0 - sh.prefix[lo], n;
+    long long off = u0 - prefix[lo], n;
     q.b = lo * per_thread;
     while (true) {
       q.seq = Kv4Seq::of(a, q.b);
-      n = head_units(q.seq);
+      n = sh.whole ? (mine_of(q.seq) ? tiles_of(q.seq) : 0) : head_units(q.seq, ignored);
       if (off < n * a.num_kv_heads) break;
       off -= n * a.num_kv_heads;
       ++q.b;
@@ -352,7 +383,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     off -= q.h * n;
     q.rt = 0;
     while (true) {
-      const int size = pre_item(q.seq, group, q.rt, a.window).size();
+      const int size = sh.whole ? 1 : pre_item(q.seq, group, q.rt, a.window).size();
       if (off < size) break;
       off -= size;
       ++q.rt;
@@ -897,8 +928,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 
 namespace {
 // Sequences of up to kDecodeRows packed rows take the decode kernel, the others
-// the prefill kernel; a batch whose bound allows no sequence of a kind does not
-// launch that kind's kernel.
+// the prefill kernel; a batch whose bound allows no long sequence does not launch
+// the latter.  Measured: 48 windows of 2048 keys with up to 30 packed rows of 64
+// 39 us so, 52 us by the prefill kernel; 64 sequences of 2000 keys with 64 packed
+// rows 174 us by the decode kernel, 136 us so.
 constexpr int kDecodeRows = 32;
 
 long long packed_bound(long long max_q_len, int num_q_heads, int num_kv_heads) {

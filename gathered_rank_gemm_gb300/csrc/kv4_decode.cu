@@ -355,8 +355,7 @@ __global__ void __launch_bounds__(DecShape<D, NT>::kWarps * 32, DecShape<D, NT>:
     table = a.page_table + static_cast<long long>(b) * a.table_stride;
     np = item.hi > 0 && !p.wait_fault ? ((take + 1) / 2 - wt + TW - 1) / TW : (p.wait_fault ? 1 : 0);
     hole = false;
-    if (np > 0) now = addresses(0);
-    if (p.wait_fault) now = 0;
+    now = np > 0 && !p.wait_fault ? addresses(0) : 0;
     for (issued = 0; issued < min(np, STAGES); ++issued) issue(issued);
   };
   begin();

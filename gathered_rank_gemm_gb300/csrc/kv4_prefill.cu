@@ -621,7 +621,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               const uint32_t i = it + j;
               const bool v_there = mbar_try_wait(bar(sh.v_full[i & 1]), (i >> 1) & 1);
               const bool k_there = j + 1 == take || mbar_try_wait(bar(sh.k_full[(i + 1) & 1]), ((i + 1) >> 1) & 1);
-              ready = v_there && k_there;
+              ready = v_there && k_there && !cta_abort.raised();
               if (!__all_sync(0xffffffffu, ready)) ready = have_v(i) && (j + 1 == take || have_k(i + 1));
             }
             tmem_wait_st();
@@ -878,6 +878,11 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       load(vc, vs, B::kV, B::kVScale);
       bool ok = blk != nullptr;
       bool here = true, behind = look_up(2);  // this tile and the next exist
+      // Nothing arrives after giving up: a warp's 32 arrivals on a phase that waits for
+      // fewer (the test hook's) would end the kernel.
+      auto arrive = [&](uint64_t& b) {
+        if (__all_sync(0xffffffffu, !cta_abort.raised())) mbar_arrive(bar(b));
+      };
       // by stage and tile: whether the tile's product on it is to be waited for, and
       // the parity of how many there were
       uint32_t used = 0, uses = 0;
@@ -896,7 +901,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (lane == 0) sh.valid[it & 3][warp - 8] = votes;
         fence_proxy_async();
         __syncwarp();
-        mbar_arrive(bar(sh.k_full[st]));
+        arrive(sh.k_full[st]);
         blk = block();  // the next tile's K is on its way while V is written
         ok = blk != nullptr;
         load(kc, ks, B::kK, B::kKScale);
@@ -910,7 +915,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
         put(smem + kOffV + st * kTile, vc, vs);
         fence_proxy_async();
-        mbar_arrive(bar(sh.v_full[st]));
+        arrive(sh.v_full[st]);
         load(vc, vs, B::kV, B::kVScale);
         here = behind;
         behind = look_up(2);

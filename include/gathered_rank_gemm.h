@@ -568,10 +568,14 @@ int lora_kv4_append_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *q_out
  * output (LORA_STATUS_BAD_LENGTH).  What lies in the cache behind a sequence's
  * keys may hold anything, NaN scales included.
  * Sums, maxima and accumulators are fp32.  The products run on fp16 operands:
- * a cached value (without the cache's factor) is exact in fp16, q is scaled by
- * a power of two per row so that its largest element lies in [2^14, 2^15)
+ * a cached value (without the cache's factor) is exact in fp16, a bf16 row of q
+ * is scaled by a power of two so that its largest element lies in [2^14, 2^15)
  * (exact but for elements below 2^-29 of the row's largest), and a
- * probability is rounded once to fp16.
+ * probability is rounded once to fp16 (2^-11 of it).  A NaN among a row's keys,
+ * or in its q, makes the row NaN; one in V the 16 dimensions of its scale; rows
+ * that do not see that key keep their values.  Results do not depend on timing
+ * or on what else is in the batch's workspace.  The kernels' waits are bounded:
+ * one that gives up sets LORA_STATUS_TIMEOUT, and the call's output is unspecified.
  */
 size_t lora_kv4_attention_workspace_size(int64_t num_seqs, int64_t max_num_tokens,
                                          int64_t max_q_len, int num_q_heads, int num_kv_heads,

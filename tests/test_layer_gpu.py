@@ -518,3 +518,79 @@ def test_wrappers_refuse_wrong_operands():
         B.lora_kv4_attention(*args, 1, 0.1, ws[:16])
     with pytest.raises(B.LoraError):
         B.lora_kv4_attention(*args, 99, 0.1, ws)
+
+
+# ------------------------------------------------------------------ NaN where a row must not look
+
+@pytest.mark.parametrize("lengths,window", [([(1, 80), (6, 100)], 0), ([(6, 100)], 20), ([(140, 300)], 0),
+                                            ([(140, 300), (4, 90)], 50), ([(300, 310)], 0)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_nan_in_the_cache_stays_with_the_rows_that_see_it(lengths, window, d):
+    """A NaN scale of K takes the rows that see its key; one of V their 16 dimensions."""
+    c = _attend_case(lengths, 4, 2, d, 16, "bf16", seed=21)
+    b = len(lengths) - 1
+    m, n = lengths[b]
+    key = n - 3 if m < 10 else n - m // 2
+    page, r = c["table_np"][b][key // 16], key % 16
+    clean = c["cache"].clone()
+    _attend(c, window)
+    want = c["out"].clone()
+    rows = torch.arange(m, device="cuda") + int(c["start_np"][b])
+    pos = torch.arange(n - m, n, device="cuda")
+    sees = (pos >= key) & ((pos - window < key) if window else torch.ones_like(pos, dtype=torch.bool))
+    # V: the second 16 dimensions of key head 1
+    c["cache"].copy_(clean)
+    c["cache"][page, 1, 0, 17 * d + r * d // 16 + 1] = 0x7F
+    _attend(c, window)
+    got = c["out"]
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[rows[sees], 2:, 16:32] = True
+    assert torch.isnan(got[bad]).all()
+    assert torch.equal(got[~bad], want[~bad])
+    # K: any block of it
+    c["cache"].copy_(clean)
+    c["cache"][page, 1, 0, 16 * d + r * d // 16] = 0xFF
+    _attend(c, window)
+    bad = torch.zeros_like(got, dtype=torch.bool)
+    bad[rows[sees], 2:] = True
+    assert torch.isnan(c["out"][bad]).all()
+    assert torch.equal(c["out"][~bad], want[~bad])
+
+
+@pytest.mark.parametrize("lengths", [[(3, 50)], [(140, 200)]])
+def test_queries_that_are_not_finite_keep_to_their_rows(lengths):
+    c = _attend_case(lengths, 4, 2, 64, 16, "bf16", seed=22)
+    _attend(c)
+    want = c["out"].clone()
+    c["q"][1, 1, 5] = math.nan
+    c["q"][2, 3, 0] = math.inf
+    _attend(c)
+    other = torch.ones_like(want, dtype=torch.bool)
+    other[1, 1] = False
+    other[2, 3] = False
+    assert torch.isnan(c["out"][1, 1]).all()
+    assert torch.equal(c["out"][other], want[other])
+
+
+# ------------------------------------------------------------------ bounded waits
+
+@pytest.mark.parametrize("lengths", [[(1, 3000), (1, 90), (1, 0)], [(2, 40)], [(140, 900), (1, 60)]])
+def test_attention_gives_up_a_wait_and_recovers(lengths):
+    """Through the test hook: the call ends, says so, writes nothing, and the next call on the same
+    workspace is right."""
+    c = _attend_case(lengths, 8, 2, 128, 16, "bf16", seed=23)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = _attend(c, status=status)
+    torch.cuda.synchronize()
+    c["out"].fill_(7)
+    c["lse"].fill_(7)
+    assert B.lora_testing_inject_timeout(True) is False
+    try:
+        _attend(c, workspace=ws, status=status)
+        assert B.lora_read_status(status) == B.LORA_STATUS_TIMEOUT
+    finally:
+        assert B.lora_testing_inject_timeout(False) is True
+    assert (c["out"] == 7).all() and (c["lse"] == 7).all()
+    _attend(c, workspace=ws, status=status)
+    assert B.lora_read_status(status) == 0
+    _attend_check(c, some=10)

@@ -515,6 +515,7 @@ int lora_add_rmsnorm_f16(const uint16_t *x, int64_t x_row_stride, const uint16_t
  * A position outside [0, max_positions) sets LORA_STATUS_BAD_POSITION and the
  * token is skipped altogether; a slot that is neither -1 nor inside the cache
  * sets LORA_STATUS_BAD_SLOT and the token's k and v are not stored.
+ * Rows t >= n write nothing; what they hold may be read and is not used.
  * Sizes: rope_dim a multiple of 32 up to head_dim; strides multiples of 8;
  * pointers 16-byte aligned; num_pages * page_size below 2^31; the scales finite
  * and above 0.

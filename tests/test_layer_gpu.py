@@ -269,7 +269,7 @@ def test_append_refuses_what_only_the_data_shows():
 K_SCALE, V_SCALE = 1 / 32, 1 / 64
 
 
-def _attend_case(lengths, qh, kvh, d, page, dtype, seed=0, spread=1.0, pad=0):
+def _attend_case(lengths, qh, kvh, d, page, dtype, seed=0, spread=1.0, pad=0, grow=None):
     rng = np.random.default_rng(seed)
     dt = DTYPES[dtype]
     per = [-(-n // page) for _, n in lengths]
@@ -283,6 +283,8 @@ def _attend_case(lengths, qh, kvh, d, page, dtype, seed=0, spread=1.0, pad=0):
         at += m
     k = [rng.standard_normal((n, kvh, d)) * spread for _, n in lengths]
     v = [rng.standard_normal((n, kvh, d)) for _, n in lengths]
+    if grow:  # keys that grow along a sequence, by powers of two from 1 to 2^grow
+        k = [x * 2.0 ** np.linspace(0, grow, len(x))[:, None, None] for x in k]
     cache = R.build_cache(k, v, pages, table, page, K_SCALE, V_SCALE)
     rows = sum(m for m, _ in lengths) + 2
     q = torch.tensor(rng.standard_normal((rows, qh * d + pad)), dtype=torch.float32).to(dt).cuda()
@@ -387,6 +389,77 @@ def test_attention_of_peaked_and_flat_rows(lengths, spread):
     c["q"].mul_(3)
     _attend(c)
     _attend_check(c, some=20)
+
+
+@pytest.mark.parametrize("grow", [12, -12])
+@pytest.mark.parametrize("lengths", [[(1, 3000)], [(3, 700), (1, 90)], [(150, 1500)], [(300, 700), (40, 300)]])
+def test_attention_of_scores_that_grow_or_fall_along_the_keys(lengths, grow):
+    """The running reference has to move again and again, or never."""
+    c = _attend_case(lengths, 4, 2, 128, 16, "bf16", seed=17, spread=2.0 ** (-grow / 2), grow=grow)
+    _attend(c)
+    _attend_check(c, some=20)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("chunks", [False, True])
+def test_attention_of_many_sequences(chunks, d):
+    """More sequences than a CTA has threads; with chunks, some of them go to each kernel."""
+    rng = np.random.default_rng(18)
+    lengths = [(int(rng.integers(0, 4)), int(rng.integers(0, 60))) for _ in range(1100)]
+    if chunks:
+        for b in range(5, 1100, 90):
+            lengths[b] = (int(rng.integers(30, 140)), int(rng.integers(1, 200)))
+    c = _attend_case(lengths, 2, 1, d, 16, "bf16", seed=18)
+    _attend(c)
+    _attend_check(c)
+
+
+@pytest.mark.parametrize("bound", [1, 4, 100])
+def test_rows_beyond_the_bound_get_no_output(bound):
+    c = _attend_case([(3, 60), (130, 300), (1, 9)], 4, 2, 64, 16, "bf16", seed=19)
+    c["max_q"] = bound
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    _attend(c, status=status)
+    assert B.lora_read_status(status) == B.LORA_STATUS_BAD_LENGTH
+    got, lse = c["out"].clone(), c["lse"].clone()
+    c["max_q"] = 130
+    _attend(c)
+    _attend_check(c, some=20)
+    kept = torch.zeros(c["rows"], dtype=torch.bool, device="cuda")
+    for b, (m, _) in enumerate(c["lengths"]):
+        kept[c["start_np"][b]:c["start_np"][b] + min(m, bound)] = True
+    assert (got[~kept] == 7).all() and (lse[~kept] == 7).all()
+    # the same rows by the same formula, whichever kernel had them: two roundings of the output and
+    # two of the probabilities (2^-11 of values of at most 6) apart, and as much for the sums
+    diff = (got[kept].float() - c["out"][kept].float()).abs()
+    assert (diff <= 2.0 ** -7 * c["out"][kept].float().abs() + 2.0 ** -9 * 6).all()
+
+
+@pytest.mark.parametrize("rows", [1, 140])
+def test_sequences_that_share_pages(rows):
+    """A common beginning in common pages, as prefix reuse leaves it."""
+    c = _attend_case([(rows, 300), (rows, 300), (rows, 280)], 4, 2, 128, 32, "bf16", seed=20)
+    for t in (c["table"], c["table_np"]):
+        t[1:, :6] = t[0, :6]
+    _attend(c)
+    _attend_check(c, some=15)
+
+
+def test_two_streams_with_a_workspace_each():
+    one = _attend_case([(1, 2500), (1, 900)], 8, 2, 128, 16, "bf16", seed=24)
+    two = _attend_case([(140, 400), (2, 800)], 8, 2, 128, 16, "bf16", seed=25)
+    cases = (one, two)
+    spaces = [_attend(c) for c in cases]
+    want = [c["out"].clone() for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for c, ws, s in zip(cases, spaces, streams):
+            _attend(c, workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    for c, w in zip(cases, want):
+        assert torch.equal(c["out"], w)
+        _attend_check(c, some=10)
 
 
 @pytest.mark.parametrize("factor", [2.0 ** 60, 2.0 ** -60])

@@ -122,23 +122,23 @@ __device__ __forceinline__ DecItem dec_item(const Kv4Seq& s, int group, uint32_t
 }
 
 // Warps of a CTA, CTAs of an SM and pairs of blocks in a warp's ring: as many
-// warps as the registers allow (168 a thread with 12 warps, 128 with 16).
-template <int D, int NT>
+// warps as the registers allow (168 a thread with 12 warps, 128 with 16), in one
+// CTA an SM (ONE) or two.
+template <int D, int NT, bool ONE>
 struct DecShape {
-  static constexpr bool kWide = D == 128 && NT == 2;
-  static constexpr int kWarps = kWide ? 12 : 8;
-  static constexpr int kCtas = kWide ? 1 : 2;
+  static constexpr int kCtas = ONE ? 1 : 2;
+  static constexpr int kWarps = (D == 128 && NT == 2 ? 12 : 16) / kCtas;
   static constexpr int kStages = D == 64 ? 4 : 3;
 };
 
-template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(DecShape<D, NT>::kWarps * 32, DecShape<D, NT>::kCtas)
+template <int D, int NT, bool F16, bool ONE>
+__global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D, NT, ONE>::kCtas)
     lora_kv4_decode_kernel(const __grid_constant__ DecodeParams p) {
   using B = Kv4Block<D>;
-  constexpr int kDecWarps = DecShape<D, NT>::kWarps, kDecThreads = kDecWarps * 32;
+  constexpr int kDecWarps = DecShape<D, NT, ONE>::kWarps, kDecThreads = kDecWarps * 32;
   constexpr int ROWS = 8 * NT;
   constexpr int KS = D / 16;              // k steps of S, and 16-dimension tiles of O
-  constexpr int STAGES = DecShape<D, NT>::kStages;  // pairs of blocks in a warp's ring
+  constexpr int STAGES = DecShape<D, NT, ONE>::kStages;  // pairs of blocks in a warp's ring
   constexpr int kStage = 2 * B::kBytes;
   constexpr int kRing = STAGES * kStage;
   constexpr int PITCH = D + 4;            // floats of a row's partial in shared memory
@@ -226,17 +226,22 @@ __global__ void __launch_bounds__(DecShape<D, NT>::kWarps * 32, DecShape<D, NT>:
   if (all[0] == 0) return;
 
   // ---- who takes what.  A cut item costs its join (partials to L2, a counter,
-  // and back: about 6 us on the way of the last), so short items stay whole where
-  // there are workers for all of them: a warp takes 16 blocks in the time of
-  // that, a CTA 96.  Else the line of units is cut into equal runs, of warps,
-  // or of CTAs where an item would span over 8 warps' runs (16 sequences of
-  // 1000 to 4000 keys, 4 rows: 40 us so, 52 us by warps; 48 windows of 2048 keys: 38 and 36 us).
+  // and back: about 6 us on the way of the last), so items stay whole where the
+  // longest runs over a worker's fair share by less than that: 16 blocks of a
+  // warp, 160 of a CTA that has one item, 40 of a CTA that has two.  (48 windows of
+  // 2048 keys, 30 rows of 64: 21.8 us whole, 39.3 cut; 150 sequences of 1500 to 2000
+  // keys, two items a CTA: 60 and 72 us; 100 of 700, three: 33.6 and 31.3, so cut.)
+  // Else the line of units is cut into equal runs, of warps, or of CTAs where an
+  // item would span over 8 warps' runs (20 sequences of 2000 to 5000 keys, 16 rows).
   const long long warps_all = static_cast<long long>(gridDim.x) * kDecWarps;
   const long long per_warp = max((all[0] + warps_all - 1) / warps_all, 2ll * kItemCost);
-  const bool whole_warp = s_most <= 16 && all[1] <= warps_all;
-  const bool whole = whole_warp || (s_most <= 12 * kDecWarps && all[1] <= gridDim.x);
+  const long long warp_items = (all[1] + warps_all - 1) / warps_all;
+  const long long cta_items = (all[1] + gridDim.x - 1) / gridDim.x;
+  const bool whole_warp = warp_items * (s_most + kItemCost) <= per_warp + 16;
+  const bool whole = whole_warp ||
+      (cta_items <= 2 && cta_items * s_most <= all[0] / gridDim.x + (cta_items == 1 ? 160 : 40));
   const bool team = whole ? !whole_warp : all[0] > 8 * per_warp * all[1];
-  const long long per = whole ? 1
+  const long long per = whole  ? (whole_warp ? warp_items : cta_items)
                         : team ? max((all[0] + gridDim.x - 1) / gridDim.x, 2ll * kDecWarps)
                                : per_warp;
   const long long total = whole ? all[1] : all[0];  // items are the units where they stay whole
@@ -855,17 +860,14 @@ __global__ void __launch_bounds__(DecShape<D, NT>::kWarps * 32, DecShape<D, NT>:
 }
 
 namespace {
-template <int D, int NT, bool F16>
-int run_decode(const DecodeParams& q, cudaStream_t stream) {
-  using S = DecShape<D, NT>;
+template <int D, int NT, bool F16, bool ONE>
+int run_decode(const DecodeParams& q, int sms, cudaStream_t stream) {
+  using S = DecShape<D, NT, ONE>;
   DecodeParams p = q;
-  const void* fn = reinterpret_cast<const void*>(lora_kv4_decode_kernel<D, NT, F16>);
+  const void* fn = reinterpret_cast<const void*>(lora_kv4_decode_kernel<D, NT, F16, ONE>);
   const size_t smem = static_cast<size_t>(S::kWarps) * S::kStages * 2 * Kv4Block<D>::kBytes;
   if (ensure_smem_attr(fn, smem) != 0) return -6;
-  const int sms = device_sm_count();
-  if (sms <= 0) return -6;
-  return launch_pdl(fn, dim3(S::kCtas * min(sms, kDecSmsMax)), dim3(S::kWarps * 32), smem, stream,
-                    0, &p);
+  return launch_pdl(fn, dim3(S::kCtas * sms), dim3(S::kWarps * 32), smem, stream, 0, &p);
 }
 constexpr size_t kCounterBytes = kDecWorkersMax * 4;
 }  // namespace
@@ -891,11 +893,26 @@ int launch_kv4_decode(const Kv4AttnArgs& a, int max_packed_rows, size_t counters
   p.group_magic = (65536u + group - 1) / group;
   p.wait_fault = wait_fault() ? 1 : 0;
   p.wait_limit_ns = p.wait_fault ? kTestWaitLimitNs : kWaitLimitNs;
+  const int sms = min(device_sm_count(), kDecSmsMax);
+  if (sms <= 0) return -6;
   if (a.head_dim == 64)
-    return wide ? (f16 ? run_decode<64, 2, true>(p, stream) : run_decode<64, 2, false>(p, stream))
-                : (f16 ? run_decode<64, 1, true>(p, stream) : run_decode<64, 1, false>(p, stream));
-  return wide ? (f16 ? run_decode<128, 2, true>(p, stream) : run_decode<128, 2, false>(p, stream))
-              : (f16 ? run_decode<128, 1, true>(p, stream) : run_decode<128, 1, false>(p, stream));
+    return wide ? (f16 ? run_decode<64, 2, true, false>(p, sms, stream)
+                       : run_decode<64, 2, false, false>(p, sms, stream))
+                : (f16 ? run_decode<64, 1, true, false>(p, sms, stream)
+                       : run_decode<64, 1, false, false>(p, sms, stream));
+  if (!wide)
+    return f16 ? run_decode<128, 1, true, false>(p, sms, stream)
+               : run_decode<128, 1, false, false>(p, sms, stream);
+  // Where there can be no more items than SMs, CTAs of all of an SM's warps: 10
+  // sequences of 1000 to 1500 keys, 8 key heads, 16 rows: 15.9 us so, 22.9 us by two an SM;
+  // 60 of 500, 4 key heads: 20.1 us by one, 14.7 us by two.
+  const long long packed = min(static_cast<long long>(a.max_q_len) * group,
+                               static_cast<long long>(max_packed_rows));
+  if ((packed + 15) / 16 * a.num_seqs * a.num_kv_heads <= sms)
+    return f16 ? run_decode<128, 2, true, true>(p, sms, stream)
+               : run_decode<128, 2, false, true>(p, sms, stream);
+  return f16 ? run_decode<128, 2, true, false>(p, sms, stream)
+             : run_decode<128, 2, false, false>(p, sms, stream);
 }
 
 }  // namespace grg

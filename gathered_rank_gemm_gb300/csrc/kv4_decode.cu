@@ -227,21 +227,25 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
 
   // ---- who takes what.  A cut item costs its join (partials to L2, a counter,
   // and back: about 6 us on the way of the last), so items stay whole where the
-  // longest runs over a worker's fair share by less than that: 16 blocks of a
-  // warp, 160 of a CTA that has one item, 40 of a CTA that has two.  (48 windows of
+  // longest runs over a worker's fair share by less than that: 160 blocks of a CTA
+  // that has one item, 40 of a CTA that has two, 16 of a warp.  (48 windows of
   // 2048 keys, 30 rows of 64: 21.8 us whole, 39.3 cut; 150 sequences of 1500 to 2000
   // keys, two items a CTA: 60 and 72 us; 100 of 700, three: 33.6 and 31.3, so cut.)
-  // Else the line of units is cut into equal runs, of warps, or of CTAs where an
-  // item would span over 8 warps' runs (20 sequences of 2000 to 5000 keys, 16 rows).
+  // A CTA goes before a warp, which takes 0.6 us a block: 8 items of 200 keys 6.9 and
+  // 14.7 us, two items a CTA, 100 to 200 keys, 13.8 and 17.9 us; 20 to 100 keys, 18.7
+  // and 17.2 us.  Else the line of units is cut into equal runs, of warps, or of
+  // CTAs where an item would span over 8 warps' runs (20 sequences of 2000 to 5000
+  // keys, 16 rows).
   const long long warps_all = static_cast<long long>(gridDim.x) * kDecWarps;
   const long long per_warp = max((all[0] + warps_all - 1) / warps_all, 2ll * kItemCost);
   const long long warp_items = (all[1] + warps_all - 1) / warps_all;
   const long long cta_items = (all[1] + gridDim.x - 1) / gridDim.x;
-  const bool whole_warp = warp_items * (s_most + kItemCost) <= per_warp + 16;
-  const bool whole = whole_warp ||
-      (cta_items <= 2 && cta_items * s_most <= all[0] / gridDim.x + (cta_items == 1 ? 160 : 40));
-  const bool team = whole ? !whole_warp : all[0] > 8 * per_warp * all[1];
-  const long long per = whole  ? (whole_warp ? warp_items : cta_items)
+  const long long fair = all[0] / gridDim.x;
+  const bool whole_cta = (cta_items == 1 && s_most <= fair + 160) ||
+                         (cta_items == 2 && s_most > 8 && 2 * s_most <= fair + 40);
+  const bool whole = whole_cta || warp_items * (s_most + kItemCost) <= per_warp + 16;
+  const bool team = whole ? whole_cta : all[0] > 8 * per_warp * all[1];
+  const long long per = whole  ? (whole_cta ? cta_items : warp_items)
                         : team ? max((all[0] + gridDim.x - 1) / gridDim.x, 2ll * kDecWarps)
                                : per_warp;
   const long long total = whole ? all[1] : all[0];  // items are the units where they stay whole

@@ -12,7 +12,7 @@
 //  - warps 0-3 and 4-7, softmax of tile 0 and 1: a thread owns a row.  Per key tile
 //    it reads S, forms p in one pass against a running reference m (moved, and O
 //    rescaled, only when a tile's sum shows that p may leave fp16's range) and stores
-//    P; then one thread of the tile's first warp issues O += P V and the next S, so
+//    P; then one lane of the tile's first warp issues O += P V and the next S, so
 //    that one tile's products run under the other tile's softmax.  At an item's end the
 //    next item's queries (bf16: scaled by a power of two per row into fp16's range)
 //    and first S come before the rows of O go out.
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       uint32_t ns = 0;          // first products of this tile so far
       uint32_t no[2] = {0, 0};  // and second ones, by stage
       uint32_t it = 0;          // key tiles so far (the stages of K and V)
-      // The products, issued by one thread of the tile's first warp, in the order
+      // The products, issued by one lane of the tile's first warp, in the order
       // S(0), O(0), S(1), O(1), ...: the tensor core takes one tile's in turn, so S
       // never overwrites a P still to be read.  A key tile's stages of K and V are free
       // when the second products of both tiles (all that are active) are done: until

@@ -43,7 +43,7 @@ constexpr int kPreCtasMax = 160;  // CTAs that the workspace has room for
 constexpr int kPreRows = 256;     // packed rows of an item
 constexpr int kPreKeys = 128;     // keys of a tile
 // What the line counts: a key tile of two row tiles, of one, and an item's start and end.
-constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 12;
+constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 16;
 constexpr int kWholeTiles = 8;    // an item of so few key tiles is not cut for the sake of idle CTAs
 constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
 constexpr float kPreLog2e = 1.4426950408889634f;
@@ -261,19 +261,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   pdl_wait();
   pdl_launch_dependents();
 
-  // ---- the line of units (key tiles): a prefix sum over the threads' runs of sequences
+  // ---- the line of units (key tiles): a prefix sum over the threads' runs of
+  // sequences; where there are few, a group of lanes shares a sequence's row tiles,
+  // and its first lane has the sum (one prompt of 8192 rows: 13 thousand cycles
+  // with a thread a sequence)
   const int per_thread = (a.num_seqs + kPreThreads - 1) / kPreThreads;
+  int group_lanes = 1;
+  while (group_lanes < 32 && 2 * group_lanes * a.num_seqs <= kPreThreads) group_lanes *= 2;
   auto mine_of = [&](const Kv4Seq& s) {
     return s.take * group > p.max_packed_rows;
   };
   auto tiles_of = [&](const Kv4Seq& s) {
     return (s.take * group + kPreRows - 1) / kPreRows;
   };
-  auto head_units = [&](const Kv4Seq& s, int& most) -> long long {  // units of one key head
+  // units of one key head, the row tiles from `from` on in steps of `step`
+  auto head_units = [&](const Kv4Seq& s, int from, int step, int& most) -> long long {
     long long n = 0;
     if (mine_of(s)) {
       const int nr = tiles_of(s);
-      for (int rt = 0; rt < nr; ++rt) {
+      for (int rt = from; rt < nr; rt += step) {
         const PreItem it = pre_item(s, group, rt, a.window);
         n += it.size();
         most = max(most, it.nt);
@@ -283,13 +289,18 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   };
   long long mine[2] = {0, 0};
   int most = 0;
-  for (int i = 0; i < per_thread; ++i) {
-    const int b = tid * per_thread + i;
-    if (b < a.num_seqs) {
-      const Kv4Seq s = Kv4Seq::of(a, b);
-      mine[0] += head_units(s, most) * a.num_kv_heads;
-      if (mine_of(s)) mine[1] += static_cast<long long>(tiles_of(s)) * a.num_kv_heads;
+  {
+    const int sub = lane & (group_lanes - 1);
+    for (int i = 0; i < per_thread; ++i) {
+      const int b = tid / group_lanes * per_thread + i;
+      if (b < a.num_seqs) {
+        const Kv4Seq s = Kv4Seq::of(a, b);
+        mine[0] += head_units(s, sub, group_lanes, most) * a.num_kv_heads;
+        if (sub == 0 && mine_of(s)) mine[1] += static_cast<long long>(tiles_of(s)) * a.num_kv_heads;
+      }
     }
+    for (int o = 1; o < group_lanes; o <<= 1) mine[0] += __shfl_xor_sync(0xffffffffu, mine[0], o);
+    if (sub != 0) mine[0] = 0;
   }
   long long run[2] = {mine[0], mine[1]};
 #pragma unroll
@@ -371,10 +382,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (prefix[mid] <= u0) lo = mid; else hi = mid;
     }
     long long off = u0 - prefix[lo], n;
-    q.b = lo * per_thread;
+    q.b = lo / group_lanes * per_thread;
     while (true) {
       q.seq = Kv4Seq::of(a, q.b);
-      n = sh.whole ? (mine_of(q.seq) ? tiles_of(q.seq) : 0) : head_units(q.seq, ignored);
+      if (sh.whole) {
+        n = mine_of(q.seq) ? tiles_of(q.seq) : 0;
+      } else {  // by all lanes
+        n = head_units(q.seq, lane, 32, ignored);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      }
       if (off < n * a.num_kv_heads) break;
       off -= n * a.num_kv_heads;
       ++q.b;
@@ -382,11 +399,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     q.h = static_cast<int>(off / n);
     off -= q.h * n;
     q.rt = 0;
-    while (true) {
-      const int size = sh.whole ? 1 : pre_item(q.seq, group, q.rt, a.window).size();
-      if (off < size) break;
-      off -= size;
-      ++q.rt;
+    if (sh.whole) {
+      q.rt = static_cast<int>(off);
+      off = 0;
+    } else {  // 32 row tiles at a time
+      const int nr = tiles_of(q.seq);
+      while (true) {
+        const int size = q.rt + lane < nr ? pre_item(q.seq, group, q.rt + lane, a.window).size() : 0;
+        int to = size;  // sizes up to this lane's
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(0xffffffffu, to, o);
+          if (lane >= o) to += v;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, off < to);
+        const int at = past ? __ffs(past) - 1 : 31;
+        off -= __shfl_sync(0xffffffffu, past ? to - size : to, at);
+        q.rt += past ? at : 32;
+        if (past) break;
+      }
     }
     q.at = u0 - off;
     set_part(q);

@@ -180,14 +180,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
-// A 16-byte load that stays where it is written: several of them go out together.
-__device__ __forceinline__ uint4 load_now(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
 // One lane of the (converged) warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -497,8 +489,16 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         x.tok = w.seq.q0 + x.i;
         return x;
       };
-      // Starts a part: q in fp16 to shared memory, the first product under way.
-      auto open_part = [&](const PrePart& w) {
+      // Starts a part in two steps.  First its rows of q are copied to shared memory:
+      // asynchronously, while the rows of the part before go out.
+      // The warp's 32 rows, D / 8 lanes a row and 256 / D rows at a time, so that a row's
+      // reads are neighbours.
+      constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, PASSES = 32 / AT_ONCE;
+      auto chunk = [&](int i2) {  // the 16 bytes of q that this thread copies in a pass
+        const int r = i2 * AT_ONCE + lane / LANES, c = lane % LANES;
+        return static_cast<uint32_t>(t * kTile + (c >> 3) * kAtom) + swz128((warp & 3) * 32 + r, c & 7);
+      };
+      auto begin_part = [&](const PrePart& w) {
         Row x;
         const Place mine_p = place(w);
         x.nact = live_rows(w) > 128 ? 2 : 1;
@@ -506,25 +506,28 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         x.lo = w.seq.first_key(mine_p.i, a.window);
         x.cf = 0.0f;
         if (t >= x.nact) return x;
-        // the warp's 32 rows, D / 8 lanes a row and 256 / D rows at a time, so that
-        // a row's reads are neighbours
-        constexpr int LANES = D / 8, AT_ONCE = 32 / LANES, PASSES = 32 / AT_ONCE;
-        unsigned char* tile = smem + t * kTile;
-        float down = 1.0f;  // (fp16 rows need no factor)
-        uint4 raw_q[PASSES];
 #pragma unroll
         for (int i2 = 0; i2 < PASSES; ++i2) {
           const int r = i2 * AT_ONCE + lane / LANES;
           const long long tok = __shfl_sync(0xffffffffu, mine_p.tok, r);
           const int head = __shfl_sync(0xffffffffu, mine_p.head, r);
-          raw_q[i2] = load_now(reinterpret_cast<const uint4*>(a.q + tok * a.q_stride + head * D) + lane % LANES);
+          cp_async_16(sbase + chunk(i2), a.q + tok * a.q_stride + head * D + 8 * (lane % LANES), true);
         }
-        pre_barrier(2 + t, 128);  // (keeps the loads together, ahead of their first use)
-#pragma unroll
-        for (int i2 = 0; i2 < PASSES; ++i2) {
-          const int r = i2 * AT_ONCE + lane / LANES, c = lane % LANES;
-          uint32_t z[4] = {raw_q[i2].x, raw_q[i2].y, raw_q[i2].z, raw_q[i2].w};
-          if constexpr (!F16) {
+        cp_async_commit();
+        return x;
+      };
+      // Then each thread turns what it has copied into fp16, and the first product
+      // starts.
+      auto finish_part = [&](int nact) {
+        if (t >= nact) return 0.0f;
+        cp_async_wait<0>();
+        float down = 1.0f;  // (fp16 rows need no factor)
+        if constexpr (!F16) {
+#pragma unroll 4
+          for (int i2 = 0; i2 < PASSES; ++i2) {
+            uint4* at = reinterpret_cast<uint4*>(smem + chunk(i2));
+            const uint4 raw_q = *at;
+            uint32_t z[4] = {raw_q.x, raw_q.y, raw_q.z, raw_q.w};
             // the row's largest magnitude, as 16-bit patterns (they order like the numbers)
             uint32_t top = __vmaxu2(__vmaxu2(z[0] & 0x7FFF7FFFu, z[1] & 0x7FFF7FFFu),
                                     __vmaxu2(z[2] & 0x7FFF7FFFu, z[3] & 0x7FFF7FFFu));
@@ -540,11 +543,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             }
             dn = __shfl_sync(0xffffffffu, dn, (lane % AT_ONCE) * LANES);
             if (lane / AT_ONCE == i2) down = dn;
+            *at = make_uint4(z[0], z[1], z[2], z[3]);
           }
-          *reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + swz128((warp & 3) * 32 + r, c & 7)) =
-              make_uint4(z[0], z[1], z[2], z[3]);
         }
-        x.cf = down * (a.score_scale * kPreLog2e);
         fence_proxy_async();
         pre_barrier(2 + t, 128);
         if ((warp & 3) == 0 && have_k(it)) {
@@ -553,9 +554,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (elect_one()) scores(st);
         }
         __syncwarp();
-        return x;
+        return down * (a.score_scale * kPreLog2e);
       };
-      Row row = open_part(q);
+      Row row = begin_part(q);
+      row.cf = finish_part(row.nact);
       int slot_of_part = 0, take = q.take, first_key = (q.item.kt0 + q.o) * kPreKeys;
       if (lane == 0) sh.part[warp][0] = q;
       __syncwarp();
@@ -680,8 +682,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
           if ((it + j) & 1) ++no[1]; else ++no[0];
         }
-        // ---- the next part starts (neither tile's warps run ahead by a part);
-        // while its first product runs, this one's rows go out
+        // ---- the next part starts (neither tile's warps run ahead by a part): its
+        // queries are on their way while this one's rows go out
         it += take;
         const PrePart done = sh.part[warp][slot_of_part];
         const int done_lo = row.lo, done_pos = row.pos, done_nact = row.nact;
@@ -689,7 +691,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         const bool more = next_part(q2);
         if (more) {
           pre_barrier(1, 256);
-          row = open_part(q2);
+          row = begin_part(q2);
           slot_of_part ^= 1;
           take = q2.take, first_key = (q2.item.kt0 + q2.o) * kPreKeys;
           if (lane == 0) sh.part[warp][slot_of_part] = q2;
@@ -828,6 +830,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           }
         }
         if (!more) break;
+        row.cf = finish_part(row.nact);
       }
       if (cta_abort.raised()) {  // the products still running end before the TMEM goes
         if ((warp & 3) == 0 && elect_one()) {  // (the thread that issued them)

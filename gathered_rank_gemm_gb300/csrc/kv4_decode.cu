@@ -24,7 +24,7 @@
 // timing.
 //
 // Measured (GB300, bf16): 256 sequences of up to 4096 keys, 32 / 8 heads of 128
-// (608 MB): 133 us, 0.67 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
+// (608 MB): 134 us, 0.67 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
 // MB): 151 us, 0.77; one of 700 keys: 9 us.  Bound by issue: 306 instructions a
 // block of 16 keys (64 conversions and 64 scalings of pairs, 16 products, the
 // rest the softmax and the turning of V), 125 cycles an SM where HBM would give it

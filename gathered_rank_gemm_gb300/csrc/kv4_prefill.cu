@@ -14,8 +14,8 @@
 //    rescaled, only when a tile's sum shows that p may leave fp16's range) and stores
 //    P; then one lane of the tile's first warp issues O += P V and the next S, so
 //    that one tile's products run under the other tile's softmax.  At an item's end the
-//    next item's queries (bf16: scaled by a power of two per row into fp16's range)
-//    and first S come before the rows of O go out.
+//    next item's queries are copied to shared memory while the rows of O go out; then
+//    they are turned into fp16 (bf16: scaled by a power of two per row) in place.
 //  - warps 8-11, keys and values: a thread owns a key of the tile.  It loads
 //    the key's codes and scales into registers a tile ahead (the page's number two
 //    ahead), and writes the fp16 values into the swizzled operand tiles (two stages
@@ -25,11 +25,13 @@
 // of its CTAs to finish (as in kv4_decode.cu).  Short items stay whole.
 //
 // Measured (GB300, bf16): 6 chunks of 700 to 2000 rows over 2000 to 5000 keys, 32 / 8
-// heads of 128: 333 us, 1033 TFLOP/s (0.54 of measured); one prompt of 8192 tokens,
-// 32 / 32 heads: 480 us, 1146 TFLOP/s.  Bound by the chain softmax (1250 cycles a tile of
-// 128 x 128), barrier and issue (200), two products (1024 at the tensor core's rate,
-// 1550 until S can be read): 3490 cycles for two tiles, whose products alone take
-// 2048.  An item's start and end cost about four key tiles.
+// heads of 128: 320 us, 1072 TFLOP/s (0.56 of measured); one prompt of 8192 tokens,
+// 32 / 32 heads: 476 us, 1155 TFLOP/s.  Bound by the chain softmax (1400 cycles a tile of
+// 128 x 128), barrier and issue, two products (1024 at the tensor core's rate): 3390
+// cycles a key tile of two row tiles, whose products alone take 2048.  The issuing warp
+// is held until its products are nearly done, so its own softmax starts some 400 cycles
+// late; a warp for the issue alone would leave 128 registers a thread, and two threads a
+// row (96 registers) took 361 us.  An item's start and end cost about five key tiles.
 #include "kv4_attention.cuh"
 #include "kv4_attention.h"
 #include "launch.h"
@@ -42,7 +44,9 @@ constexpr int kPreWarps = kPreThreads / 32;
 constexpr int kPreCtasMax = 160;  // CTAs that the workspace has room for
 constexpr int kPreRows = 256;     // packed rows of an item
 constexpr int kPreKeys = 128;     // keys of a tile
-// What the line counts: a key tile of two row tiles, of one, and an item's start and end.
+// What the line counts: a key tile of two row tiles, of one, and an item's start and
+// end (12: 8192 rows in a window of 1000 122.8 us, 16: 117.1 us; 8 and 28 cost 3 % and 1 %
+// on 6 chunks).
 constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 16;
 constexpr int kWholeTiles = 8;    // an item of so few key tiles is not cut for the sake of idle CTAs
 constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
@@ -523,7 +527,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         cp_async_wait<0>();
         float down = 1.0f;  // (fp16 rows need no factor)
         if constexpr (!F16) {
-#pragma unroll 4
+#pragma unroll 4  // (by 8 or 16: 343 us instead of 320 on the case above, by 2: 326)
           for (int i2 = 0; i2 < PASSES; ++i2) {
             uint4* at = reinterpret_cast<uint4*>(smem + chunk(i2));
             const uint4 raw_q = *at;

@@ -99,6 +99,13 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 }  // namespace
 
+// a / b of values that are rarely past 32 bits (a >= 0, b > 0); a 64-bit division takes
+// some hundred cycles on every call's way.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                              : a / b;
+}
+
 // One item: a group of packed rows of a sequence and a key head, and its keys.
 struct DecItem {
   int blk0;  // first block of 16 keys
@@ -237,16 +244,16 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   // CTAs where an item would span over 8 warps' runs (20 sequences of 2000 to 5000
   // keys, 16 rows).
   const long long warps_all = static_cast<long long>(gridDim.x) * kDecWarps;
-  const long long per_warp = max((all[0] + warps_all - 1) / warps_all, 2ll * kItemCost);
-  const long long warp_items = (all[1] + warps_all - 1) / warps_all;
-  const long long cta_items = (all[1] + gridDim.x - 1) / gridDim.x;
-  const long long fair = all[0] / gridDim.x;
+  const long long per_warp = max(quotient(all[0] + warps_all - 1, warps_all), 2ll * kItemCost);
+  const long long warp_items = quotient(all[1] + warps_all - 1, warps_all);
+  const long long cta_items = quotient(all[1] + gridDim.x - 1, gridDim.x);
+  const long long fair = quotient(all[0], gridDim.x);
   const bool whole_cta = (cta_items == 1 && s_most <= fair + 160) ||
                          (cta_items == 2 && s_most > 8 && 2 * s_most <= fair + 40);
   const bool whole = whole_cta || warp_items * (s_most + kItemCost) <= per_warp + 16;
   const bool team = whole ? whole_cta : all[0] > 8 * per_warp * all[1];
   const long long per = whole  ? (whole_cta ? cta_items : warp_items)
-                        : team ? max((all[0] + gridDim.x - 1) / gridDim.x, 2ll * kDecWarps)
+                        : team ? max(quotient(all[0] + gridDim.x - 1, gridDim.x), 2ll * kDecWarps)
                                : per_warp;
   const long long total = whole ? all[1] : all[0];  // items are the units where they stay whole
   const int worker = team ? blockIdx.x : blockIdx.x * kDecWarps + warp;
@@ -262,10 +269,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
 
   const long long u0 = worker * per, u_end = min(u0 + per, total);
   const int cost = whole ? 0 : kItemCost;
-  auto run_of = [&](long long x) {  // the worker of place x of the line
-    return (total >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(per))
-                              : static_cast<int>(x / per);
-  };
+  auto run_of = [&](long long x) { return static_cast<int>(quotient(x, per)); };  // the worker of place x
   // the part of an item that this worker has: blocks [o, o + take) of the item
   // whose place in the line is [at, at + cost + nb)
   int b = 0, rg = 0, h = 0, o = 0, take = 0;
@@ -298,8 +302,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       off -= static_cast<long long>(size) * a.num_kv_heads;
       ++rg;
     }
-    h = (off >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(size))
-                         : static_cast<int>(off / size);
+    h = static_cast<int>(quotient(off, size));
     off -= static_cast<long long>(h) * size;
     at = -static_cast<int>(off);
     o = max(static_cast<int>(off) - cost, 0);
@@ -367,6 +370,25 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     now = np > 0 && !p.wait_fault ? addresses(0) : 0;
     for (issued = 0; issued < min(np, STAGES); ++issued) issue(issued);
   };
+  // this thread's share of the rows' queries (D / 4 dimensions of row g of each 8), which
+  // a first part asks for before its pages are looked up
+  uint4 raw_q[NT][KS / 2];
+  auto load_q = [&]() {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = rg * ROWS + nt * 8 + g;
+#pragma unroll
+      for (int i = 0; i < KS / 2; ++i) raw_q[nt][i] = make_uint4(0, 0, 0, 0);
+      if (r < seq.take * group) {
+        const int i = row_of(r, p.group_magic);
+        const uint16_t* src = a.q + (seq.q0 + i) * a.q_stride + (h * group + r - i * group) * D +
+                              t4 * (D / 4);
+#pragma unroll
+        for (int i = 0; i < KS / 2; ++i) raw_q[nt][i] = __ldg(reinterpret_cast<const uint4*>(src) + i);
+      }
+    }
+  };
+  load_q();
   begin();
 
   while (true) {
@@ -380,24 +402,15 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     int pos[NT][2], lo[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const int r = row0 + nt * 8 + g;
       float v[KS * 4], top = 0.0f;
 #pragma unroll
-      for (int i = 0; i < KS * 4; ++i) v[i] = 0.0f;
-      if (r < packed) {
-        const int i = row_of(r, p.group_magic);
-        const uint16_t* src = a.q + (seq.q0 + i) * a.q_stride + (h * group + r - i * group) * D +
-                              t4 * (D / 4);
+      for (int i = 0; i < KS / 2; ++i) {
+        const uint32_t x[4] = {raw_q[nt][i].x, raw_q[nt][i].y, raw_q[nt][i].z, raw_q[nt][i].w};
 #pragma unroll
-        for (int i = 0; i < KS / 2; ++i) {
-          const uint4 w = __ldg(reinterpret_cast<const uint4*>(src) + i);
-          const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = unpack_t<F16>(x[k]);
-            v[8 * i + 2 * k] = f.x, v[8 * i + 2 * k + 1] = f.y;
-            top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-          }
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = unpack_t<F16>(x[k]);
+          v[8 * i + 2 * k] = f.x, v[8 * i + 2 * k + 1] = f.y;
+          top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
         }
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
@@ -854,6 +867,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       }
     }
     if (!more) break;
+    load_q();
     if (team) {
       fence_proxy_async();  // the rings' next writes are bulk copies
       __syncthreads();

@@ -31,6 +31,16 @@ struct Kv4Seq {
   }
 };
 
+// The last of the 32 * PER ascending values that is not above x (values[0] is not), by
+// a whole warp in two looks.
+template <int PER>
+__device__ __forceinline__ int last_not_past(const long long* values, long long x, int lane) {
+  static_assert(PER <= 32, "the second look is one value a lane");
+  const int block = __popc(__ballot_sync(0xffffffffu, values[lane * PER] <= x)) - 1;
+  const bool in = lane < PER && values[block * PER + min(lane, PER - 1)] <= x;
+  return block * PER + __popc(__ballot_sync(0xffffffffu, in)) - 1;
+}
+
 // 2^x.
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;

@@ -282,11 +282,8 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   };
   if (u0 < u_end) {
     const long long* prefix = s_prefix[whole ? 1 : 0];
-    int lo = 0, hi = kDecThreads, ignored = 0;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (prefix[mid] <= u0) lo = mid; else hi = mid;
-    }
+    const int lo = last_not_past<kDecWarps>(prefix, u0, lane);
+    int ignored = 0;
     long long off = u0 - prefix[lo];
     for (b = lo * per_thread;; ++b) {
       seq = seq_at(b);

@@ -372,11 +372,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const long long u0 = sh.u0;
     if (u0 >= sh.u_end) return false;
     const long long* prefix = sh.prefix[sh.whole ? 1 : 0];
-    int lo = 0, hi = kPreThreads, ignored = 0;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (prefix[mid] <= u0) lo = mid; else hi = mid;
-    }
+    const int lo = last_not_past<kPreWarps>(prefix, u0, lane);
+    int ignored = 0;
     long long off = u0 - prefix[lo], n;
     q.b = lo / group_lanes * per_thread;
     while (true) {

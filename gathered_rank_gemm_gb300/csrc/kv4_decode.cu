@@ -243,18 +243,21 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   // and 17.2 us.  Else the line of units is cut into equal runs, of warps, or of
   // CTAs where an item would span over 8 warps' runs (20 sequences of 2000 to 5000
   // keys, 16 rows).
-  const long long warps_all = static_cast<long long>(gridDim.x) * kDecWarps;
-  const long long per_warp = max(quotient(all[0] + warps_all - 1, warps_all), 2ll * kItemCost);
-  const long long warp_items = quotient(all[1] + warps_all - 1, warps_all);
-  const long long cta_items = quotient(all[1] + gridDim.x - 1, gridDim.x);
-  const long long fair = quotient(all[0], gridDim.x);
-  const bool whole_cta = (cta_items == 1 && s_most <= fair + 160) ||
-                         (cta_items == 2 && s_most > 8 && 2 * s_most <= fair + 40);
-  const bool whole = whole_cta || warp_items * (s_most + kItemCost) <= per_warp + 16;
-  const bool team = whole ? whole_cta : all[0] > 8 * per_warp * all[1];
-  const long long per = whole  ? (whole_cta ? cta_items : warp_items)
-                        : team ? max(quotient(all[0] + gridDim.x - 1, gridDim.x), 2ll * kDecWarps)
-                               : per_warp;
+  // (Few divisions: they are on every call's way.)
+  const long long ctas = gridDim.x, warps_all = ctas * kDecWarps;
+  const int cta_items = all[1] <= ctas ? 1 : all[1] <= 2 * ctas ? 2 : 3;
+  const bool whole_cta = (cta_items == 1 && (s_most - 160ll) * ctas <= all[0]) ||
+                         (cta_items == 2 && s_most > 8 && (2ll * s_most - 40) * ctas <= all[0]);
+  bool whole = whole_cta, team = whole_cta;
+  long long per = cta_items;
+  if (!whole_cta) {
+    const long long per_warp = max(quotient(all[0] + warps_all - 1, warps_all), 2ll * kItemCost);
+    const long long warp_items = quotient(all[1] + warps_all - 1, warps_all);
+    whole = warp_items * (s_most + kItemCost) <= per_warp + 16;
+    team = !whole && all[0] > 8 * per_warp * all[1];
+    per = whole ? warp_items
+                : team ? max(quotient(all[0] + ctas - 1, ctas), 2ll * kDecWarps) : per_warp;
+  }
   const long long total = whole ? all[1] : all[0];  // items are the units where they stay whole
   const int worker = team ? blockIdx.x : blockIdx.x * kDecWarps + warp;
   const int TW = team ? kDecWarps : 1, wt = team ? warp : 0;

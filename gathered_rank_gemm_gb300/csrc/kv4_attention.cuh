@@ -31,6 +31,13 @@ struct Kv4Seq {
   }
 };
 
+// a / b of values that are rarely past 32 bits (a >= 0, b > 0); a 64-bit division takes
+// some hundred cycles on every call's way.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                              : a / b;
+}
+
 // The last of the 32 * PER ascending values that is not above x (values[0] is not), by
 // a whole warp in two looks.
 template <int PER>

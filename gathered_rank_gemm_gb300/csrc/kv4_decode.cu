@@ -99,13 +99,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 }  // namespace
 
-// a / b of values that are rarely past 32 bits (a >= 0, b > 0); a 64-bit division takes
-// some hundred cycles on every call's way.
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
-                              : a / b;
-}
-
 // One item: a group of packed rows of a sequence and a key head, and its keys.
 struct DecItem {
   int blk0;  // first block of 16 keys
@@ -154,7 +147,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t s_bar[kDecWarps * STAGES];
   __shared__ long long s_warp[2][kDecWarps];
-  __shared__ int s_abort, s_last, s_most;
+  __shared__ int s_abort, s_last, s_top[kDecWarps];
   // until the rings start: units and items before each thread's sequences, and
   // the sequences themselves where there are no more than threads
   using Prefix = long long[kDecThreads + 1];
@@ -170,7 +163,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     for (int i = 0; i < STAGES; ++i) mbar_init(bars + 8 * i, 2 + (p.wait_fault ? 1 : 0));
     fence_mbar_init();
   }
-  if (tid == 0) s_abort = 0, s_most = 0;
+  if (tid == 0) s_abort = 0;
   const CtaAbort cta_abort{&s_abort, p.wait_limit_ns};
   pdl_wait();
   pdl_launch_dependents();
@@ -213,10 +206,11 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       const long long v = __shfl_up_sync(0xffffffffu, run[i], o);
       if (lane >= o) run[i] += v;
     }
-  if (lane == 31) s_warp[0][warp] = run[0], s_warp[1][warp] = run[1];
   most = __reduce_max_sync(0xffffffffu, most);
-  __syncthreads();  // (s_most is zero)
-  if (lane == 0 && most > 0) atomicMax(&s_most, most);
+  if (lane == 31) s_warp[0][warp] = run[0], s_warp[1][warp] = run[1], s_top[warp] = most;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) most = max(most, s_top[w]);
   long long all[2] = {0, 0};
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -246,14 +240,14 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   // (Few divisions: they are on every call's way.)
   const long long ctas = gridDim.x, warps_all = ctas * kDecWarps;
   const int cta_items = all[1] <= ctas ? 1 : all[1] <= 2 * ctas ? 2 : 3;
-  const bool whole_cta = (cta_items == 1 && (s_most - 160ll) * ctas <= all[0]) ||
-                         (cta_items == 2 && s_most > 8 && (2ll * s_most - 40) * ctas <= all[0]);
+  const bool whole_cta = (cta_items == 1 && (most - 160ll) * ctas <= all[0]) ||
+                         (cta_items == 2 && most > 8 && (2ll * most - 40) * ctas <= all[0]);
   bool whole = whole_cta, team = whole_cta;
   long long per = cta_items;
   if (!whole_cta) {
     const long long per_warp = max(quotient(all[0] + warps_all - 1, warps_all), 2ll * kItemCost);
     const long long warp_items = quotient(all[1] + warps_all - 1, warps_all);
-    whole = warp_items * (s_most + kItemCost) <= per_warp + 16;
+    whole = warp_items * (most + kItemCost) <= per_warp + 16;
     team = !whole && all[0] > 8 * per_warp * all[1];
     per = whole ? warp_items
                 : team ? max(quotient(all[0] + ctas - 1, ctas), 2ll * kDecWarps) : per_warp;

@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     // join, about as long as kWholeTiles tiles.  Else the line is cut into equal
     // runs (no shorter than a tile, so every run inside an item has one of its tiles).
     sh.whole = sh.most <= kWholeTiles && all[1] <= gridDim.x;
-    sh.per = sh.whole ? 1 : max((all[0] + gridDim.x - 1) / static_cast<long long>(gridDim.x),
+    sh.per = sh.whole ? 1 : max(quotient(all[0] + gridDim.x - 1, gridDim.x),
                                 static_cast<long long>(kCostTwo));
     sh.u0 = blockIdx.x * sh.per;
     sh.u_end = min(sh.u0 + sh.per, sh.whole ? all[1] : all[0]);
@@ -389,7 +389,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       off -= n * a.num_kv_heads;
       ++q.b;
     }
-    q.h = static_cast<int>(off / n);
+    q.h = static_cast<int>(quotient(off, n));
     off -= q.h * n;
     q.rt = 0;
     if (sh.whole) {
@@ -784,8 +784,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             p.part_ml[static_cast<long long>(slot) * kPreRows + t * 128 + row_in_tile] = make_float2(m, l);
             const int threads = 128 * done_nact;
             const long long begins = done.at + kCostItem;
-            const int w0 = static_cast<int>(begins / sh.per);
-            const int w1 = static_cast<int>((begins + static_cast<long long>(done.item.nt - 1) * done.item.cost) / sh.per);
+            const int w0 = static_cast<int>(quotient(begins, sh.per));
+            const int w1 = static_cast<int>(quotient(begins + static_cast<long long>(done.item.nt - 1) * done.item.cost, sh.per));
             pre_barrier(3 + done_nact, threads);
             if (tid == 0) {
               uint32_t seen;  // releases what the barrier has gathered, acquires the others'

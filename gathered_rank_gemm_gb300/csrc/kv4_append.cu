@@ -12,8 +12,9 @@
 namespace grg {
 
 namespace {
-// Measured on 8000 tokens of 32 q and 8 kv heads (210 MB): 41.3 us with 128
-// threads and registers for 6 CTAs an SM, 43.2 us with 8 (spills), 48 us with 256 x 4.
+// Measured on 8000 tokens of 32 q and 8 kv heads (210 MB): 40.3 us with CTAs of 64
+// threads, 41.0 us of 96, 44.1 us of 192 (8192 tokens of 64 and 8 heads: 71.1, 77.0 and
+// 81.8 us), all with 80 registers a thread; 43.2 us with 64 registers (spills).
 constexpr int kAppendThreads = 128;
 constexpr int kAppendCtas = 6;
 
@@ -212,8 +213,8 @@ __device__ __forceinline__ void append_pair(const Kv4AppendArgs& p, int t, int u
   }
 }
 
-// One unit (append_pair) per thread, in CTAs of about 128 threads: several
-// tokens a CTA where a token has few units, or several CTAs a token.
+// One unit (append_pair) per thread: several tokens in a CTA of up to 128 threads where a
+// token has few units, else one or more CTAs a token.
 template <int D, bool F16>
 __global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     lora_kv4_append_kernel(const AppendParams q) {
@@ -241,9 +242,18 @@ int launch_kv4_append(const Kv4AppendArgs& a, bool f16, cudaStream_t stream) {
                        : (f16 ? reinterpret_cast<const void*>(lora_kv4_append_kernel<128, true>)
                               : reinterpret_cast<const void*>(lora_kv4_append_kernel<128, false>));
   const int per = (a.num_q_heads + 2 * a.num_kv_heads) * (a.head_dim / 32);
-  const int tokens = max(1, kAppendThreads / per);
-  const int ctas = tokens > 1 ? 1 : (per + kAppendThreads - 1) / kAppendThreads;
-  const int threads = (tokens > 1 ? per * tokens + 31 : (per + ctas - 1) / ctas + 31) / 32 * 32;
+  // a token of up to 64 units shares its CTA; else the CTA size that leaves the fewest
+  // threads idle, the smallest of them (small CTAs come and go more evenly)
+  int tokens = 1, ctas = 1, threads;
+  if (per <= 64) {
+    tokens = kAppendThreads / per;
+    threads = (per * tokens + 31) / 32 * 32;
+  } else {
+    threads = 64;
+    for (int x = 96; x <= kAppendThreads; x += 32)
+      if ((per + x - 1) / x * x < (per + threads - 1) / threads * threads) threads = x;
+    ctas = (per + threads - 1) / threads;
+  }
   const long long grid = tokens > 1 ? (a.max_num_tokens + tokens - 1) / tokens
                                     : static_cast<long long>(a.max_num_tokens) * ctas;
   if (grid > 0x7FFFFFFFll) return -3;

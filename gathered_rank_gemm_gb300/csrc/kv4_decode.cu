@@ -24,11 +24,12 @@
 // timing.
 //
 // Measured (GB300, bf16): 256 sequences of up to 4096 keys, 32 / 8 heads of 128
-// (608 MB): 134 us, 0.67 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
-// MB): 151 us, 0.77; one of 700 keys: 9 us.  Bound by issue: 306 instructions a
+// (608 MB): 131 us, 0.68 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
+// MB): 149 us, 0.78; one of 700 keys: 8.5 us.  Bound by issue: 306 instructions a
 // block of 16 keys (64 conversions and 64 scalings of pairs, 16 products, the
-// rest the softmax and the turning of V), 125 cycles an SM where HBM would give it
-// in 98.
+// rest the softmax and the turning of V), 122 cycles an SM where HBM would give it
+// in 98.  A short sequence is bound by its chain of latencies: lengths, line, page
+// table, copies, products, join.
 #include "kv4_attention.cuh"
 #include "kv4_attention.h"
 #include "launch.h"

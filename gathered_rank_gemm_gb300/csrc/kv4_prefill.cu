@@ -969,9 +969,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
 namespace {
 // Sequences of up to kDecodeRows packed rows take the decode kernel, the others
 // the prefill kernel; a batch whose bound allows no long sequence does not launch
-// the latter.  Measured: 48 windows of 2048 keys with up to 30 packed rows of 64
-// 21.8 us so, 52 us by the prefill kernel; 64 sequences of 2000 keys with 64 packed
-// rows 174 us by the decode kernel, 136 us so.
+// the latter.  Measured, by the decode and by the prefill kernel: 48 windows of 2048
+// keys with up to 30 packed rows of 64 20.7 and 51.2 us; 64 sequences of 2000 keys with 32
+// packed rows of 128 112 and 130 us, with 64 190 and 131 us; 16 of 2000 with 48 rows 56.6
+// and 47.9 us.
 constexpr int kDecodeRows = 32;
 
 long long packed_bound(long long max_q_len, int num_q_heads, int num_kv_heads) {

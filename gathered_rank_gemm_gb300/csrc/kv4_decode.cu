@@ -25,7 +25,7 @@
 //
 // Measured (GB300, bf16): 256 sequences of up to 4096 keys, 32 / 8 heads of 128
 // (608 MB): 131 us, 0.68 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
-// MB): 149 us, 0.78; one of 700 keys: 8.5 us.  Bound by issue: 306 instructions a
+// MB): 148 us, 0.78; one of 700 keys: 8.0 us.  Bound by issue: 306 instructions a
 // block of 16 keys (64 conversions and 64 scalings of pairs, 16 products, the
 // rest the softmax and the turning of V), 122 cycles an SM where HBM would give it
 // in 98.  A short sequence is bound by its chain of latencies: lengths, line, page
@@ -165,12 +165,16 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     fence_mbar_init();
   }
   if (tid == 0) s_abort = 0;
+  __syncthreads();
   const CtaAbort cta_abort{&s_abort, p.wait_limit_ns};
   pdl_wait();
   pdl_launch_dependents();
 
   // ---- the line of units (an item's fixed cost and its blocks) and of items, by
-  // sequence: prefix sums over the threads' runs of sequences
+  // sequence: prefix sums over the threads' runs of sequences.  Up to 32 sequences
+  // each warp has in its lanes (no barrier on the way: one sequence of 20 keys
+  // 5.25 us so, 5.75 us by the CTA; 64 sequences, which go by the CTA, pay 0.1 us for it).
+  const bool few = a.num_seqs <= 32;
   const int per_thread = (a.num_seqs + kDecThreads - 1) / kDecThreads;
   auto seq_at = [&](int b) { return per_thread == 1 ? s_seq[b] : Kv4Seq::of(a, b); };
   auto groups_of = [&](const Kv4Seq& s) {  // row groups; 0: no rows, or not this kernel's
@@ -189,11 +193,13 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   };
   long long mine[2] = {0, 0};
   int most = 0;  // blocks of the longest item
+  Kv4Seq own_seq{};  // the lane's, of few
   for (int i = 0; i < per_thread; ++i) {
-    const int b = tid * per_thread + i;
+    const int b = (few ? lane : tid) * per_thread + i;
     if (b < a.num_seqs) {
       const Kv4Seq s = Kv4Seq::of(a, b);
-      if (per_thread == 1) s_seq[b] = s;
+      if (few) own_seq = s;
+      else if (per_thread == 1) s_seq[b] = s;
       if (s.odd && blockIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
       mine[0] += units_of(s, most) * a.num_kv_heads;
       mine[1] += static_cast<long long>(groups_of(s)) * a.num_kv_heads;
@@ -208,23 +214,28 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       if (lane >= o) run[i] += v;
     }
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) s_warp[0][warp] = run[0], s_warp[1][warp] = run[1], s_top[warp] = most;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) most = max(most, s_top[w]);
   long long all[2] = {0, 0};
+  if (few) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    long long before = 0;
+    for (int i = 0; i < 2; ++i) all[i] = __shfl_sync(0xffffffffu, run[i], 31);
+  } else {
+    if (lane == 31) s_warp[0][warp] = run[0], s_warp[1][warp] = run[1], s_top[warp] = most;
+    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kDecWarps; ++w) {
-      if (w < warp) before += s_warp[i][w];
-      all[i] += s_warp[i][w];
+    for (int w = 0; w < kDecWarps; ++w) most = max(most, s_top[w]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      long long before = 0;
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        if (w < warp) before += s_warp[i][w];
+        all[i] += s_warp[i][w];
+      }
+      s_prefix[i][tid] = before + run[i] - mine[i];
+      if (tid == 0) s_prefix[i][kDecThreads] = all[i];
     }
-    s_prefix[i][tid] = before + run[i] - mine[i];
-    if (tid == 0) s_prefix[i][kDecThreads] = all[i];
+    __syncthreads();
   }
-  __syncthreads();
   if (all[0] == 0) return;
 
   // ---- who takes what.  A cut item costs its join (partials to L2, a counter,
@@ -279,15 +290,26 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     take = whole ? item.nb : min(item.nb, run_len - at - cost) - o;
   };
   if (u0 < u_end) {
-    const long long* prefix = s_prefix[whole ? 1 : 0];
-    const int lo = last_not_past<kDecWarps>(prefix, u0, lane);
-    int ignored = 0;
-    long long off = u0 - prefix[lo];
-    for (b = lo * per_thread;; ++b) {
-      seq = seq_at(b);
-      const long long n = (whole ? groups_of(seq) : units_of(seq, ignored)) * a.num_kv_heads;
-      if (off < n) break;
-      off -= n;
+    long long off;
+    if (few) {
+      const long long begins = whole ? run[1] - mine[1] : run[0] - mine[0];
+      b = __popc(__ballot_sync(0xffffffffu, begins <= u0)) - 1;
+      off = u0 - __shfl_sync(0xffffffffu, begins, b);
+      seq.q0 = __shfl_sync(0xffffffffu, own_seq.q0, b);
+      seq.rows = __shfl_sync(0xffffffffu, own_seq.rows, b);
+      seq.take = __shfl_sync(0xffffffffu, own_seq.take, b);
+      seq.kv = __shfl_sync(0xffffffffu, own_seq.kv, b);
+    } else {
+      const long long* prefix = s_prefix[whole ? 1 : 0];
+      const int lo = last_not_past<kDecWarps>(prefix, u0, lane);
+      int ignored = 0;
+      off = u0 - prefix[lo];
+      for (b = lo * per_thread;; ++b) {
+        seq = seq_at(b);
+        const long long n = (whole ? groups_of(seq) : units_of(seq, ignored)) * a.num_kv_heads;
+        if (off < n) break;
+        off -= n;
+      }
     }
     int size;
     while (true) {
@@ -319,8 +341,10 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     set_take();
     return take > 0;
   };
-  fence_proxy_async();
-  __syncthreads();  // the rings may start
+  if (!few) {  // the rings may start
+    fence_proxy_async();
+    __syncthreads();
+  }
   if (take <= 0) return;  // a whole team or a lone warp
 
   // ---- a part's copies: pairs of blocks 2 q, 2 q + 1 of it, q = wt + TW k for this warp

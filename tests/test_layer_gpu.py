@@ -414,6 +414,23 @@ def test_attention_of_many_sequences(chunks, d):
     _attend_check(c)
 
 
+@pytest.mark.parametrize("seqs", [31, 32, 33, 192, 193, 256, 257, 385])
+@pytest.mark.parametrize("rows", [1, 2, 9])
+def test_attention_where_the_walk_over_sequences_changes(seqs, rows):
+    """Sequences of a warp's lanes, of a CTA's threads, of several a thread; empty ones among them,
+    the first and the last too; a few long ones, so that items are whole, and cut."""
+    rng = np.random.default_rng(seqs)
+    lengths = [(int(rng.integers(0, rows + 1)), int(rng.integers(0, 40))) for _ in range(seqs)]
+    lengths[0] = lengths[-1] = (0, 5)
+    c = _attend_case(lengths, 4, 2, 128, 16, "bf16", seed=seqs)
+    _attend(c)
+    _attend_check(c)
+    lengths[seqs // 2] = (1, 3000)
+    c = _attend_case(lengths, 4, 2, 64, 16, "f16", seed=seqs)
+    _attend(c)
+    _attend_check(c)
+
+
 @pytest.mark.parametrize("bound", [1, 4, 100])
 def test_rows_beyond_the_bound_get_no_output(bound):
     c = _attend_case([(3, 60), (130, 300), (1, 9)], 4, 2, 64, 16, "bf16", seed=19)

@@ -24,10 +24,10 @@
 // timing.
 //
 // Measured (GB300, bf16): 256 sequences of up to 4096 keys, 32 / 8 heads of 128
-// (608 MB): 131 us, 0.68 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
+// (608 MB): 127 us, 0.71 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
 // MB): 148 us, 0.78; one of 700 keys: 8.0 us.  Bound by issue: 306 instructions a
 // block of 16 keys (64 conversions and 64 scalings of pairs, 16 products, the
-// rest the softmax and the turning of V), 122 cycles an SM where HBM would give it
+// rest the softmax and the turning of V), 118 cycles an SM where HBM would give it
 // in 98.  A short sequence is bound by its chain of latencies: lengths, line, page
 // table, copies, products, join.
 #include "kv4_attention.cuh"
@@ -41,7 +41,9 @@ constexpr int kDecSmsMax = 160;                   // SMs that the workspace has 
 constexpr int kDecWorkersMax = kDecSmsMax * 16;   // warps on them
 constexpr int kPartialSlots = kDecWorkersMax * 2;
 constexpr float kNoKey = -1e30f;  // the running maximum before any key
-constexpr int kItemCost = 4;      // what an item costs besides its blocks, in blocks
+// What an item costs besides its blocks, in blocks (256 sequences up to 4096 keys: 4 130.7
+// us, 6 127.0 us, 10 128.5 us; 64 of 2000 to 8000: 79.8, 78.7, 80.5 us).
+constexpr int kItemCost = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -52,7 +52,9 @@ constexpr int kWholeTiles = 8;    // an item of so few key tiles is not cut for 
 constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
 constexpr float kPreLog2e = 1.4426950408889634f;
 constexpr float kPreLn2 = 0.6931471805599453f;
-constexpr float kPreNoKey = -1e30f;  // the running maximum before any key
+constexpr float kPreNoKey = -3e38f;     // the running reference before any key
+constexpr float kPreFar = 16777216.0f;  // 2^24: from here on a reference's own rounding is half a unit or more
+constexpr float kPreTaken = 1e-30f;     // stands for a reference that has been taken off S: as good as 0
 
 struct PrefillParams {
   Kv4AttnArgs a;
@@ -564,6 +566,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       __syncwarp();
       while (true) {
         float m = kPreNoKey, l = 0.0f;
+        // The reference before it is multiplied: one of the row's S.
+        float& ref = reinterpret_cast<float*>(sh.staged[warp])[lane];
+        ref = kPreNoKey;
         const bool on = t < row.nact;
         for (int j = 0; on && j < take; ++j) {
           const int key0 = first_key + j * kPreKeys;
@@ -572,7 +577,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           // keys at a time.  The tile's sum tells whether m still serves: above 2^15
           // some p may pass what fp16 holds, and the tile is done again with m moved.
           // A part's first tile looks for its maximum at once.
-          bool again = j == 0;
+          // m = ref c is rounded, by up to 2^-24 of it: a factor that all of a row's p
+          // share, and that cancels, but past 2^27 it alone is more than fp16 holds.  So
+          // where m is far from 0 in some row of the warp (queries or a scale out of all
+          // proportion) ref is taken off S first, in TMEM, which leaves 0 at the maximum
+          // itself; each of the warp's tiles looks for its maximum then.  Against the
+          // tile's own maximum no p is above 2, so no tile is done a third time.
+          bool again = j == 0 || __any_sync(0xffffffffu, m == kPreTaken);
           while (true) {
             cta_abort.wait(bar(sh.s_full[t]), ns & 1);
             ++ns;
@@ -609,11 +620,13 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                 if (masked) hide(c, v);
                 mx = top_of(mx, v);
               }
-              mx *= row.cf;
-              if (__any_sync(0xffffffffu, mx > m && m != kPreNoKey)) {
+              const float old = ref, to = fmaxf(old, mx);
+              const float next = to == kPreNoKey ? kPreNoKey : to * row.cf;
+              const bool far = __any_sync(0xffffffffu, fabsf(next) >= kPreFar && to != kPreNoKey);
+              if (__any_sync(0xffffffffu, to > old && old != kPreNoKey)) {
                 // O takes the new reference
                 settled((it + j + 1) & 1);
-                const float f = exp2_approx(m - fmaxf(m, mx));
+                const float f = exp2_approx(far || m == kPreTaken ? (old - to) * row.cf : m - next);
                 l *= f;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
@@ -626,7 +639,21 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                   tmem_st16(tO + 32 * c + 16, r + 16);
                 }
               }
-              m = fmaxf(m, mx);
+              ref = to;
+              m = far ? kPreTaken : next;
+              if (far) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t v[32];
+                  tmem_ld32_start(tS + 32 * c, v);
+                  tmem_ld32_wait(v);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) - to);
+                  tmem_st16(tS + 32 * c, v);
+                  tmem_st16(tS + 32 * c + 16, v + 16);
+                }
+                tmem_wait_st();
+              }
             }
             float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             uint32_t v[2][32];
@@ -688,6 +715,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         it += take;
         const PrePart done = sh.part[warp][slot_of_part];
         const int done_lo = row.lo, done_pos = row.pos, done_nact = row.nact;
+        if (m == kPreTaken) m = ref == kPreNoKey ? kPreNoKey : fmaxf(ref * row.cf, kPreNoKey);
         PrePart q2 = done;
         const bool more = next_part(q2);
         if (more) {

@@ -1,0 +1,90 @@
+"""The operators around a layer's LoRA products where their contract is easily missed: scores of any
+finite size.  Helpers, and what the tolerances rest on, are those of test_layer_gpu.py."""
+import math
+
+import numpy as np
+import pytest
+
+from gathered_rank_gemm_gb300 import binding as B
+from tests import layer_ref as R
+from tests.test_layer_gpu import (BOTTOM, FP32, HALF_UNIT, K_SCALE, V_SCALE, _attend, _attend_case,  # noqa: F401
+                                  _attend_check, _i32, _np, lib)
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ scores of any finite size
+
+def _sequences(c):
+    """Each sequence's rows of q, out and lse, and its keys and values in 64 bits."""
+    for b, (m, n) in enumerate(c["lengths"]):
+        r = slice(c["start_np"][b], c["start_np"][b + 1])
+        k, v = R.read_cache(c["cache_np"], c["table_np"][b][:-(-n // c["page"])], n, c["page"], c["d"])
+        yield (m, n, _np(c["q"])[r], _np(c["out"])[r], c["lse"].cpu().numpy().astype(np.float64)[r],
+               k * K_SCALE, v * V_SCALE)
+
+
+def _check_single_keys(c, scale):
+    """Rows whose largest score leads by so much that its key has all the weight: the score's own
+    rounding in fp32 (2^-16 of sum |q k|, as everywhere) is far below the lead."""
+    checked = 0
+    for m, n, q, out, lse, k, v in _sequences(c):
+        for i in range(m):
+            pos = n - m + i
+            for h in range(c["qh"] if pos >= 0 else 0):
+                g = h // (c["qh"] // c["kvh"])
+                x = k[:pos + 1, g] @ q[i, h] * scale
+                span = (np.abs(k[:pos + 1, g]) @ np.abs(q[i, h])).max() * scale
+                best = int(x.argmax())
+                if len(x) > 1 and x[best] - np.partition(x, -2)[-2] < max(100.0, FP32 * span):
+                    continue
+                want = v[best, g]
+                assert (np.abs(out[i, h] - want) <= (HALF_UNIT[c["dtype"]] + FP32) * np.abs(want) + BOTTOM[c["dtype"]]).all(), \
+                    (n, i, h, x[best], out[i, h][:3], want[:3])
+                assert abs(lse[i, h] - x[best]) <= FP32 * span, (n, i, h, lse[i, h], x[best])
+                checked += 1
+    return checked
+
+
+FAR = [2.0 ** 20, 2.0 ** 24, 2.0 ** 26, 2.0 ** 28, 2.0 ** 60]  # times q k of about 10
+CHUNKS = [[(140, 300)], [(300, 290), (70, 600)]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("scale", FAR)
+@pytest.mark.parametrize("lengths", CHUNKS)
+def test_attention_of_large_scores(lengths, scale, dtype):
+    """Past 2^27 the rounding of a score alone is more than fp16 holds as a power of two."""
+    c = _attend_case(lengths, 4, 2, 128, 16, dtype, seed=31)
+    _attend(c, scale=scale)
+    total = sum(max(0, min(m, n)) for m, n in lengths) * 4
+    assert _check_single_keys(c, scale) > 0.9 * total
+
+
+@pytest.mark.parametrize("scale", FAR + [-1.0])
+@pytest.mark.parametrize("lengths", CHUNKS)
+def test_attention_of_equal_keys(lengths, scale):
+    """Keys that are all the same share the weight equally, however large their score is."""
+    c = _attend_case(lengths, 4, 2, 128, 16, "bf16", seed=32)
+    if scale < 0:  # large negative scores
+        scale = 2.0 ** 28
+        c["q"].copy_(-c["q"].abs())
+        c["cache_np"][..., :64] &= 0x77  # the first key of a block is above 0
+    codes, _, scales, _ = R.sections(c["cache_np"], 128)
+    first = c["table_np"][0][0]
+    codes[:] = codes[first, :, 0, 0].copy()[:, None, None]
+    scales[:] = scales[first, :, 0, 0].copy()[:, None, None]
+    assert np.array_equal(R.sections(c["cache_np"], 128)[0], codes)
+    c["cache"] = torch.tensor(c["cache_np"]).cuda()
+    _attend(c, scale=scale)
+    for m, n, q, out, lse, k, v in _sequences(c):
+        for i in range(max(0, m - n), m):
+            cut = n - m + i + 1
+            for h in range(4):
+                vv = v[:cut, h // 2]
+                want, size = vv.mean(0), np.abs(vv).mean(0)
+                tol = HALF_UNIT["bf16"] * np.abs(want) + (2.0 ** -11 + FP32) * size + 2.0 ** -25 * size.max() * cut ** 0.5
+                assert (np.abs(out[i, h] - want) <= tol).all(), (n, i, h, out[i, h][:3], want[:3])
+                span = np.abs(k[0, h // 2]) @ np.abs(q[i, h]) * scale
+                assert abs(lse[i, h] - (k[0, h // 2] @ q[i, h] * scale + math.log(cut))) <= FP32 * (1 + span)

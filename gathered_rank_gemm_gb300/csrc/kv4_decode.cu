@@ -6,13 +6,15 @@
 // Mathematics, for a block of 16 keys (mma.sync m16n8k16, fp16 operands, fp32
 // accumulators; the codes times their e4m3 scales are exact in fp16):
 //   S[16 keys x 8 rows] = K Q^T, the keys as M, so a group of 8 rows wastes
-//   nothing;  p = 2^(S c - m), m the running maximum in units of log2;
+//   nothing;  p = 2^((S - m) c), m a running maximum of S;
 //   O[16 dims x 8 rows] += V^T P, the P fragments turned by movmatrix.
 // A warp holds the rows' O and the maximum and sum per row in registers; keys
 // come two blocks at a time through a ring of bulk copies in shared memory, one
 // copy per block (a block's codes and scales lie together).  The maximum is
 // moved only when a block exceeds it by 2^6 or more: p stays below 2^6, far
-// inside fp16, and the rescaling of O almost never runs.
+// inside fp16, and the rescaling of O almost never runs.  The difference comes before
+// the product: S c would be rounded by up to 2^-24 of it, which for scores past 2^27 is
+// more than p's exponent has room for, while S - m is 0 at the maximum.
 //
 // Work: the blocks of all (sequence, row group, key head) items in one line, an
 // item's fixed cost among them, cut into equal runs whatever the lengths, so one
@@ -40,7 +42,7 @@ namespace {
 constexpr int kDecSmsMax = 160;                   // SMs that the workspace has room for
 constexpr int kDecWorkersMax = kDecSmsMax * 16;   // warps on them
 constexpr int kPartialSlots = kDecWorkersMax * 2;
-constexpr float kNoKey = -1e30f;  // the running maximum before any key
+constexpr float kNoKey = -3e38f;  // the running maximum before any key
 // What an item costs besides its blocks, in blocks (256 sequences up to 4096 keys: 4 130.7
 // us, 6 127.0 us, 10 128.5 us; 64 of 2000 to 8000: 79.8, 78.7, 80.5 us).
 constexpr int kItemCost = 6;
@@ -94,6 +96,14 @@ __device__ __forceinline__ uint32_t both_high(uint32_t a) {
   uint32_t r;
   asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n mov.b32 %0, {h, h};\n}\n" : "=r"(r) : "r"(a));
   return r;
+}
+// (a - m, b - n) * (c, d), two fp32 at a time.
+__device__ __forceinline__ void sub_mul2(float& x, float& y, float a, float b, float m, float n, float c,
+                                         float d) {
+  asm("{\n .reg .b64 s, r, f;\n mov.b64 s, {%2, %3};\n mov.b64 r, {%4, %5};\n mov.b64 f, {%6, %7};\n"
+      " sub.rn.f32x2 s, s, r;\n mul.rn.f32x2 s, s, f;\n mov.b64 {%0, %1}, s;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(m), "f"(n), "f"(c), "f"(d));
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t r;
@@ -566,8 +576,8 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           mx[nt][c] = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][c + 2]),
-                            fmaxf(sc[nt][1][c], sc[nt][1][c + 2])) * cf[nt][c];
-          move = move || mx[nt][c] > m[nt][c] + 6.0f;
+                            fmaxf(sc[nt][1][c], sc[nt][1][c + 2]));
+          move = move || (mx[nt][c] - m[nt][c]) * cf[nt][c] > 6.0f;
         }
       if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
@@ -579,7 +589,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
             const float to = fmaxf(m[nt][c], v);
-            const float f = exp2_approx(m[nt][c] - to);
+            const float f = exp2_approx((m[nt][c] - to) * cf[nt][c]);
             m[nt][c] = to;
             l[nt][c] *= f;
 #pragma unroll
@@ -591,10 +601,10 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const float p0 = exp2_approx(fmaf(sc[nt][x][0], cf[nt][0], -m[nt][0]));
-          const float p1 = exp2_approx(fmaf(sc[nt][x][1], cf[nt][1], -m[nt][1]));
-          const float p2 = exp2_approx(fmaf(sc[nt][x][2], cf[nt][0], -m[nt][0]));
-          const float p3 = exp2_approx(fmaf(sc[nt][x][3], cf[nt][1], -m[nt][1]));
+          float p0, p1, p2, p3;
+          sub_mul2(p0, p1, sc[nt][x][0], sc[nt][x][1], m[nt][0], m[nt][1], cf[nt][0], cf[nt][1]);
+          sub_mul2(p2, p3, sc[nt][x][2], sc[nt][x][3], m[nt][0], m[nt][1], cf[nt][0], cf[nt][1]);
+          p0 = exp2_approx(p0), p1 = exp2_approx(p1), p2 = exp2_approx(p2), p3 = exp2_approx(p3);
           l[nt][0] += p0 + p2;
           l[nt][1] += p1 + p3;
           pb[nt][x][0] = transpose8x8(pack_f16x2(p0, p1));
@@ -663,11 +673,13 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
         if (++stage_out == STAGES) stage_out = 0, phase ^= 1;
       }
 
-    // ---- join: sums over the lanes that share a row
+    // ---- join: sums over the lanes that share a row; m in units of log2 from here on
+    // (finite: no difference of two is a NaN)
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
+        m[nt][c] = fmaxf(m[nt][c] * cf[nt][c], kNoKey);
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 4);
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 8);
         l[nt][c] += __shfl_xor_sync(0xffffffffu, l[nt][c], 16);

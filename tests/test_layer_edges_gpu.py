@@ -49,11 +49,12 @@ def _check_single_keys(c, scale):
 
 FAR = [2.0 ** 20, 2.0 ** 24, 2.0 ** 26, 2.0 ** 28, 2.0 ** 60]  # times q k of about 10
 CHUNKS = [[(140, 300)], [(300, 290), (70, 600)]]
+FEW = [[(1, 200), (2, 30)], [(1, 3000)], [(4, 700), (1, 90)], [(1, 500 + 7 * i) for i in range(40)]]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("scale", FAR)
-@pytest.mark.parametrize("lengths", CHUNKS)
+@pytest.mark.parametrize("lengths", CHUNKS + FEW)
 def test_attention_of_large_scores(lengths, scale, dtype):
     """Past 2^27 the rounding of a score alone is more than fp16 holds as a power of two."""
     c = _attend_case(lengths, 4, 2, 128, 16, dtype, seed=31)
@@ -63,7 +64,7 @@ def test_attention_of_large_scores(lengths, scale, dtype):
 
 
 @pytest.mark.parametrize("scale", FAR + [-1.0])
-@pytest.mark.parametrize("lengths", CHUNKS)
+@pytest.mark.parametrize("lengths", CHUNKS + FEW)
 def test_attention_of_equal_keys(lengths, scale):
     """Keys that are all the same share the weight equally, however large their score is."""
     c = _attend_case(lengths, 4, 2, 128, 16, "bf16", seed=32)

@@ -364,7 +364,10 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   const int32_t* table = nullptr;
   int first_blk = 0, part_take = 0, part_h = 0, np = 0, issued = 0;
   unsigned long long now = 0;
-  bool hole = false;  // some page is not in the cache
+  bool hole = false;  // some page (of those looked up so far) is not in the cache
+  // pairs [k_open, k_open + k_shut) of a part need no mask: both blocks exist, every row
+  // sees every key
+  int k_open = 0, k_shut = 0;
   auto block_at = [&](int blk) -> const unsigned char* {  // null: its page is not in the cache
     const int pg = blk / page_blocks;
     const int page = __ldg(table + pg);
@@ -383,7 +386,10 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     return reinterpret_cast<unsigned long long>(x);
   };
   auto issue = [&](int k) {  // by the two lanes that hold pair k's addresses
-    if ((k & 15) == 0 && k > 0) now = addresses(k);
+    if ((k & 15) == 0 && k > 0) {
+      now = addresses(k);
+      if (hole) k_shut = 0;  // these pairs are scored after this
+    }
     if ((lane >> 1) == (k & 15) && !cta_abort.raised()) {
       const uint32_t bar = bars + 8 * stage_in;
       mbar_arrive_expect_tx(bar, now ? B::kBytes : 0);
@@ -477,9 +483,6 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     }
     bool poison = false;  // a NaN scale of V among keys that some rows must not see
 
-    // pairs [k_open, k_open + k_shut) need no mask: both blocks exist, every row
-    // sees every key
-    int k_open, k_shut;
     {
       const int last = min(min((pos_min + 1) / 16 - first_blk, part_take), 1 << 27);  // blocks all rows see
       const int first = max((lo_max + 15) / 16 - first_blk, 0);

@@ -1,5 +1,5 @@
-"""The operators around a layer's LoRA products where their contract is easily missed: scores of any
-finite size.  Helpers, and what the tolerances rest on, are those of test_layer_gpu.py."""
+"""The operators around a layer's LoRA products where their contract is easily missed.  Helpers, and what
+the tolerances rest on, are those of test_layer_gpu.py."""
 import math
 
 import numpy as np
@@ -8,7 +8,7 @@ import pytest
 from gathered_rank_gemm_gb300 import binding as B
 from tests import layer_ref as R
 from tests.test_layer_gpu import (BOTTOM, FP32, HALF_UNIT, K_SCALE, V_SCALE, _attend, _attend_case,  # noqa: F401
-                                  _attend_check, _i32, _np, lib)
+                                  _i32, _np, lib)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -89,3 +89,51 @@ def test_attention_of_equal_keys(lengths, scale):
                 assert (np.abs(out[i, h] - want) <= tol).all(), (n, i, h, out[i, h][:3], want[:3])
                 span = np.abs(k[0, h // 2]) @ np.abs(q[i, h]) * scale
                 assert abs(lse[i, h] - (k[0, h // 2] @ q[i, h] * scale + math.log(cut))) <= FP32 * (1 + span)
+
+
+# ------------------------------------------------------------------ pages that are not there
+
+def _check_without(c, gone, some=None):
+    """The last row of each sequence against the formula over the keys that are there."""
+    scale = 1 / math.sqrt(c["d"])
+    for b, (m, n, q, out, lse, k, v) in enumerate(_sequences(c)):
+        if m == 0:
+            continue
+        there = np.ones(n, bool)
+        for a in gone.get(b, ()):
+            there[a * c["page"]:(a + 1) * c["page"]] = False
+        want, wlse, size, span = R.attention(q[-1:], k[there], v[there], scale, 0)
+        tol = HALF_UNIT[c["dtype"]] * np.abs(want) + (2.0 ** -11 + FP32 + FP32 * span[..., None]) * size + \
+            2.0 ** -25 * size.max() * n ** 0.5
+        assert (np.abs(out[-1:] - want) <= tol).all(), (b, n, np.abs(out[-1:] - want).max())
+        assert (np.abs(lse[-1:] - wlse) <= FP32 * (1 + span + np.abs(wlse))).all(), (b, n, lse[-1:] - wlse)
+
+
+def _pool_case(lengths, qh, kvh, d, page, dtype, seed, pool=600):
+    """Long sequences whose pages are drawn, many times each, from a few."""
+    rows, pages = sum(m for m, _ in lengths), -(-pool // page)
+    c = _attend_case([(rows, pages * page)], qh, kvh, d, page, dtype, seed=seed)
+    rng = np.random.default_rng(seed)
+    table = c["table_np"][0][rng.integers(0, pages, (len(lengths), max(-(-n // page) for _, n in lengths)))]
+    start = np.concatenate([[0], np.cumsum([m for m, _ in lengths])])
+    return dict(c, lengths=lengths, table=_i32(table), table_np=table, start=_i32(start), start_np=start,
+                kv=_i32([n for _, n in lengths]), max_q=max(m for m, _ in lengths))
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("heads", [1, 32])
+@pytest.mark.parametrize("lengths,keys", [
+    ([(1, 1500)], [600]), ([(1, 9000)], [600, 5000, 8990]), ([(1, 20000), (1, 25000)], [4000, 8128, 17000, 19990]),
+    ([(1, 3000 + 10 * i) for i in range(20)], [700, 2000, 2900]), ([(12, 30000), (1, 600)], [100, 5000, 29000]),
+    ([(40, 5000)], [600, 3000, 4800])])
+def test_attention_masks_pages_that_are_not_there_wherever_they_are(lengths, keys, heads, page):
+    """Near and far from the beginning of what one warp, or one CTA, reads of a sequence."""
+    c = _pool_case(lengths, heads, heads, 64, page, "bf16", seed=33)
+    gone = {b: [j // page for j in keys if j < n] for b, (_, n) in enumerate(lengths)}
+    for b, pages in gone.items():
+        for i, a in enumerate(pages):
+            c["table"][b, a] = -1 if i % 2 else c["cache"].shape[0]
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    _attend(c, status=status)
+    assert B.lora_read_status(status) == B.LORA_STATUS_BAD_SLOT
+    _check_without(c, gone)

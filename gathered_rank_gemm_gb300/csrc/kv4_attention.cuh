@@ -65,4 +65,11 @@ __device__ __forceinline__ void row_factor(float top, float& up, float& down) {
   down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 }
 
+// What turns a row's products into scores in units of log2: its factor's inverse times the
+// call's.  Kept among the normal numbers, whose ends leave scores of 0 and beyond fp32
+// either way: 0 times a masked key's -infinity, or infinity times 0, would be a NaN.
+__device__ __forceinline__ float score_factor(float down, float scale) {
+  return fminf(fmaxf(down * scale, 1.17549435e-38f), 3.40282347e38f);
+}
+
 }  // namespace grg

@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       // the thread's columns of S and O are rows 2 t4 and 2 t4 + 1 of the tile
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        cf[nt][c] = __shfl_sync(0xffffffffu, down, (2 * t4 + c) * 4) * (a.score_scale * kLog2e);
+        cf[nt][c] = score_factor(__shfl_sync(0xffffffffu, down, (2 * t4 + c) * 4), a.score_scale * kLog2e);
         const int rr = row_of(min(row0 + nt * 8 + 2 * t4 + c, packed - 1), p.group_magic);
         pos[nt][c] = seq.pos(rr);
         lo[nt][c] = seq.first_key(rr, a.window);

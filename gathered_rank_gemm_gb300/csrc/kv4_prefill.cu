@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (elect_one()) scores(st);
         }
         __syncwarp();
-        return down * (a.score_scale * kPreLog2e);
+        return score_factor(down, a.score_scale * kPreLog2e);
       };
       Row row = begin_part(q);
       row.cf = finish_part(row.nact);

@@ -8,7 +8,7 @@ import pytest
 from gathered_rank_gemm_gb300 import binding as B
 from tests import layer_ref as R
 from tests.test_layer_gpu import (BOTTOM, FP32, HALF_UNIT, K_SCALE, V_SCALE, _attend, _attend_case,  # noqa: F401
-                                  _i32, _np, lib)
+                                  _attend_check, _i32, _np, lib)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -137,3 +137,14 @@ def test_attention_masks_pages_that_are_not_there_wherever_they_are(lengths, key
     _attend(c, status=status)
     assert B.lora_read_status(status) == B.LORA_STATUS_BAD_SLOT
     _check_without(c, gone)
+
+
+# ------------------------------------------------------------------ the ends of the ranges
+
+@pytest.mark.parametrize("lengths", [[(1, 200), (2, 30)], [(140, 300)]])
+def test_attention_of_queries_of_next_to_nothing(lengths):
+    """Scores that underflow are all 0: the keys that a row sees share the weight."""
+    c = _attend_case(lengths, 4, 2, 64, 16, "bf16", seed=35)
+    c["q"].mul_(2.0 ** -120)
+    _attend(c, scale=1e-12)
+    _attend_check(c, scale=1e-12, some=20)

@@ -390,7 +390,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       now = addresses(k);
       if (hole) k_shut = 0;  // these pairs are scored after this
     }
-    if ((lane >> 1) == (k & 15) && !cta_abort.raised()) {
+    if ((lane >> 1) == (k & 15)) {
       const uint32_t bar = bars + 8 * stage_in;
       mbar_arrive_expect_tx(bar, now ? B::kBytes : 0);
       if (now)
@@ -404,6 +404,9 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
     table = a.page_table + static_cast<long long>(b) * a.table_stride;
     np = item.hi > 0 && !p.wait_fault ? ((take + 1) / 2 - wt + TW - 1) / TW : (p.wait_fault ? 1 : 0);
     hole = false;
+    // After a wait has given up no part begins (those under way go on while their copies
+    // arrive), so every barrier that is drained has a copy on its way.
+    if (__any_sync(0xffffffffu, cta_abort.raised())) np = 0;
     now = np > 0 && !p.wait_fault ? addresses(0) : 0;
     for (issued = 0; issued < min(np, STAGES); ++issued) issue(issued);
   };
@@ -670,7 +673,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
       if (++stage_out == STAGES) stage_out = 0, phase ^= 1;
       if (issued < np) issue(issued++);
     }
-    if (k < np && !p.wait_fault)  // gave up: what is still on its way lands before the ring is left
+    if (k < np)  // gave up: what is still on its way lands before the ring is left
       for (; k < issued; ++k) {
         mbar_drain(bars + 8 * stage_out, phase, p.wait_limit_ns);
         if (++stage_out == STAGES) stage_out = 0, phase ^= 1;

@@ -19,7 +19,8 @@ extern "C" {
  * first wait, every later wait at once, writes no output, waits for nothing
  * in flight (it issued nothing) and ORs LORA_STATUS_TIMEOUT into the status
  * word: the call leaves u and y as they were.  The attention over the 4-bit
- * cache does the same (its status argument; out and lse stay as they were).  The
+ * cache does the same (its status argument; out and lse stay as they were), but
+ * that its decode kernel then waits 1 ms for copies in flight.  The
  * grouping kernel, the norm and the append have no such wait and run as usual.  The switch is process-wide and read when a
  * launch is enqueued (a CUDA graph keeps the value it was captured with).
  * Returns the previous setting.  Thread-safe; makes no GPU call.

@@ -148,3 +148,32 @@ def test_attention_of_queries_of_next_to_nothing(lengths):
     c["q"].mul_(2.0 ** -120)
     _attend(c, scale=1e-12)
     _attend_check(c, scale=1e-12, some=20)
+
+
+# ------------------------------------------------------------------ bounded waits
+
+@pytest.mark.parametrize("heads", [(32, 32), (64, 4)])
+def test_a_call_that_gives_up_ends_soon(heads):
+    """One wait of 1 ms (the test hook's) and one for what was in flight, however many parts a warp has left:
+    some 26 here.  (Through the hook nothing is in flight, so that wait runs out as well.)"""
+    qh, kvh = heads
+    c = _pool_case([(1, 40)] * (64000 // kvh), qh, kvh, 64, 16, "bf16", seed=44, pool=48)
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    ws = _attend(c, status=status)
+    want = c["out"].clone()
+    c["out"].fill_(7)
+    begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    assert B.lora_testing_inject_timeout(True) is False
+    try:
+        begin.record()
+        _attend(c, workspace=ws, status=status)
+        end.record()
+        assert B.lora_read_status(status) == B.LORA_STATUS_TIMEOUT
+    finally:
+        assert B.lora_testing_inject_timeout(False) is True
+    assert begin.elapsed_time(end) < 10.0
+    assert (c["out"] == 7).all()
+    _attend(c, workspace=ws, status=status)
+    assert B.lora_read_status(status) == 0
+    assert torch.equal(c["out"], want)

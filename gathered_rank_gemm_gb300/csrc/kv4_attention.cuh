@@ -27,7 +27,8 @@ struct Kv4Seq {
   // The position of row i, and the first key that it sees.
   __device__ __forceinline__ int pos(int i) const { return kv - rows + i; }
   __device__ __forceinline__ int first_key(int i, int window) const {
-    return window > 0 ? max(0, pos(i) - window + 1) : 0;
+    const int at = pos(i);  // (below 0 for a row without keys: at - window may not fit 32 bits)
+    return window > 0 && at >= window ? at - window + 1 : 0;
   }
 };
 

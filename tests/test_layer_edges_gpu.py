@@ -150,6 +150,14 @@ def test_attention_of_queries_of_next_to_nothing(lengths):
     _attend_check(c, scale=1e-12, some=20)
 
 
+@pytest.mark.parametrize("lengths", [[(8, 3), (3, 3), (1, 1)], [(140, 100), (1, 5)], [(300, 290)]])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 200])
+def test_attention_in_a_window_of_any_size(lengths, window):
+    c = _attend_case(lengths, 4, 2, 128, 16, "bf16", seed=36)
+    _attend(c, window)
+    _attend_check(c, 0, some=25)  # wider than any sequence: no window at all
+
+
 # ------------------------------------------------------------------ bounded waits
 
 @pytest.mark.parametrize("heads", [(32, 32), (64, 4)])

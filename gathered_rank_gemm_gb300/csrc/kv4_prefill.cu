@@ -82,7 +82,7 @@ __device__ __forceinline__ PreItem pre_item(const Kv4Seq& s, int group, int rt, 
   PreItem it;
   it.kt0 = lo / kPreKeys;
   it.hi = hi > lo ? hi : 0;
-  it.nt = hi > lo ? (hi + kPreKeys - 1) / kPreKeys - it.kt0 : 1;
+  it.nt = hi > lo ? (hi - 1) / kPreKeys - it.kt0 + 1 : 1;  // (hi may be 2^31 - 16)
   it.cost = rows > 128 ? kCostTwo : kCostOne;
   return it;
 }
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           if (*reinterpret_cast<volatile int*>(&sh.poison)) {
             const int32_t* table = a.page_table + static_cast<long long>(done.b) * a.table_stride;
             const int k0 = max(done_lo, (done.item.kt0 + done.o) * kPreKeys);
-            const int k1 = min(done_pos, (done.item.kt0 + done.o + done.take) * kPreKeys - 1);
+            const int k1 = min(done_pos, (done.item.kt0 + done.o + done.take - 1) * kPreKeys + kPreKeys - 1);
             for (int key = k0; key <= k1; ++key) {
               const int page = __ldg(table + key / a.page_size), in = key % a.page_size;
               if (page < 0 || page >= a.num_pages) continue;

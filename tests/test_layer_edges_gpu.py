@@ -158,6 +158,25 @@ def test_attention_in_a_window_of_any_size(lengths, window):
     _attend_check(c, 0, some=25)  # wider than any sequence: no window at all
 
 
+@pytest.mark.parametrize("rows", [1, 60])
+def test_attention_of_as_many_keys_as_an_integer_holds(rows):
+    """2^31 - 16 keys in a window of 300, every page the same one."""
+    page, wide, window = 16, 2 ** 27 - 1, 300
+    c = _attend_case([(rows, page)], 4, 2, 64, page, "bf16", seed=37)
+    c["table"] = torch.full((1, wide), int(c["table_np"][0, 0]), dtype=torch.int32, device="cuda")
+    c["kv"] = _i32([wide * page])
+    _attend(c, window)
+    got, lse = _np(c["out"]), c["lse"].cpu().numpy().astype(np.float64)
+    k, v = (np.tile(x, (400 // page, 1, 1)) for x in R.read_cache(c["cache_np"], c["table_np"][0][:1], page, page, 64))
+    q = _np(c["q"])
+    for i in range(rows):
+        cut = slice(0, 400 - rows + i + 1)
+        want, wlse, size, span = R.attention(q[i:i + 1], k[cut] * K_SCALE, v[cut] * V_SCALE, 0.125, window)
+        tol = HALF_UNIT["bf16"] * np.abs(want) + (2.0 ** -11 + FP32 + FP32 * span[..., None]) * size + 2.0 ** -25 * size.max() * 20
+        assert (np.abs(got[i] - want[0]) <= tol[0]).all(), (i, got[i, 0, :3], want[0, 0, :3])
+        assert (np.abs(lse[i] - wlse[0]) <= FP32 * (1 + span[0] + np.abs(wlse[0]))).all()
+
+
 # ------------------------------------------------------------------ bounded waits
 
 @pytest.mark.parametrize("heads", [(32, 32), (64, 4)])

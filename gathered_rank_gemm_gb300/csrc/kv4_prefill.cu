@@ -66,10 +66,11 @@ struct PrefillParams {
   int wait_fault;
 };
 
-// An item's key tiles: [kt0, kt0 + nt); hi = 0 where no row sees a key.
+// An item's keys [lo, hi), hi = 0 where no row sees a key, and its key tiles [kt0, kt0 + nt).
 struct PreItem {
-  int kt0, nt, hi;
+  int lo, hi, nt;
   int cost;  // of a key tile
+  __device__ __forceinline__ int kt0() const { return lo / kPreKeys; }
   __device__ __forceinline__ int size() const { return kCostItem + nt * cost; }
 };
 __device__ __forceinline__ PreItem pre_item(const Kv4Seq& s, int group, int rt, int window) {
@@ -80,9 +81,9 @@ __device__ __forceinline__ PreItem pre_item(const Kv4Seq& s, int group, int rt, 
   const int i1 = static_cast<int>((first + rows - 1) / static_cast<uint32_t>(group));
   const int hi = s.pos(i1) + 1, lo = s.first_key(i0, window);
   PreItem it;
-  it.kt0 = lo / kPreKeys;
+  it.lo = lo;
   it.hi = hi > lo ? hi : 0;
-  it.nt = hi > lo ? (hi - 1) / kPreKeys - it.kt0 + 1 : 1;  // (hi may be 2^31 - 16)
+  it.nt = hi > lo ? (hi - 1) / kPreKeys - it.kt0() + 1 : 1;  // (hi may be 2^31 - 16)
   it.cost = rows > 128 ? kCostTwo : kCostOne;
   return it;
 }
@@ -561,7 +562,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       };
       Row row = begin_part(q);
       row.cf = finish_part(row.nact);
-      int slot_of_part = 0, take = q.take, first_key = (q.item.kt0 + q.o) * kPreKeys;
+      int slot_of_part = 0, take = q.take, first_key = (q.item.kt0() + q.o) * kPreKeys;
       if (lane == 0) sh.part[warp][0] = q;
       __syncwarp();
       while (true) {
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           pre_barrier(1, 256);
           row = begin_part(q2);
           slot_of_part ^= 1;
-          take = q2.take, first_key = (q2.item.kt0 + q2.o) * kPreKeys;
+          take = q2.take, first_key = (q2.item.kt0() + q2.o) * kPreKeys;
           if (lane == 0) sh.part[warp][slot_of_part] = q2;
           __syncwarp();
         }
@@ -732,8 +733,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           uint32_t nan_blocks = 0;  // 16-dimension blocks with a NaN scale at a key of the row
           if (*reinterpret_cast<volatile int*>(&sh.poison)) {
             const int32_t* table = a.page_table + static_cast<long long>(done.b) * a.table_stride;
-            const int k0 = max(done_lo, (done.item.kt0 + done.o) * kPreKeys);
-            const int k1 = min(done_pos, (done.item.kt0 + done.o + done.take - 1) * kPreKeys + kPreKeys - 1);
+            const int k0 = max(done_lo, (done.item.kt0() + done.o) * kPreKeys);
+            const int k1 = min(done_pos, (done.item.kt0() + done.o + done.take - 1) * kPreKeys + kPreKeys - 1);
             for (int key = k0; key <= k1; ++key) {
               const int page = __ldg(table + key / a.page_size), in = key % a.page_size;
               if (page < 0 || page >= a.num_pages) continue;
@@ -887,8 +888,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         page = -2;
         if (!more) return false;
         tiles |= (live_rows(w) > 128 ? 3u : 1u) << shift;
-        const int key = (w.item.kt0 + w.o + wj) * kPreKeys + r;
-        if (key < w.item.hi) {
+        const int key = (w.item.kt0() + w.o + wj) * kPreKeys + r;
+        if (key >= w.item.lo && key < w.item.hi) {  // (pages in front of the window may be gone)
           const int pg = key / a.page_size, in = key - pg * a.page_size;
           page = max(__ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride + pg), -1);
           in_page = (w.h * page_blocks + in / 16) * B::kBytes;

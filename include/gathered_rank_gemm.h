@@ -558,7 +558,8 @@ int lora_kv4_append_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *q_out
  *   q_start       device int32[num_seqs + 1], ascending from 0
  *   kv_len        device int32[num_seqs]
  *   page_table    device int32[num_seqs][table_stride]; entries behind a
- *                 sequence's last page are not read
+ *                 sequence's last page, and in front of the first page that
+ *                 one of its rows' windows reaches, are not read
  *   max_q_len     a bound on the sequences' rows (host): it picks the kernels
  *   workspace     lora_kv4_attention_workspace_size bytes, 16-byte aligned,
  *                 zero-filled before its first use (every call leaves its

@@ -139,6 +139,20 @@ def test_attention_masks_pages_that_are_not_there_wherever_they_are(lengths, key
     _check_without(c, gone)
 
 
+@pytest.mark.parametrize("page", [16, 32, 48])
+@pytest.mark.parametrize("window", [1, 17, 100, 300])
+@pytest.mark.parametrize("lengths", [[(1, 900), (1, 60)], [(5, 700)], [(140, 500), (70, 1000)], [(300, 1200), (1, 400)]])
+def test_pages_in_front_of_a_window_are_not_looked_up(lengths, window, page):
+    """A server gives such pages to others: their entries may hold anything."""
+    c = _attend_case(lengths, 4, 2, 64, page, "bf16", seed=34)
+    for b, (m, n) in enumerate(lengths):
+        c["table"][b, :max(0, n - m - window + 1) // page] = -1
+    status = torch.zeros(4, dtype=torch.int32, device="cuda")
+    _attend(c, window, status=status)
+    assert B.lora_read_status(status) == 0
+    _attend_check(c, window, some=20)
+
+
 # ------------------------------------------------------------------ the ends of the ranges
 
 @pytest.mark.parametrize("lengths", [[(1, 200), (2, 30)], [(140, 300)]])

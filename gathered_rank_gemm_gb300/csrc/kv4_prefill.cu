@@ -623,7 +623,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
               }
               const float old = ref, to = fmaxf(old, mx);
               const float next = to == kPreNoKey ? kPreNoKey : to * row.cf;
-              const bool far = __any_sync(0xffffffffu, fabsf(next) >= kPreFar && to != kPreNoKey);
+              // (an infinity of S is a row whose q is not finite: NaN either way)
+              const bool far = __any_sync(0xffffffffu, fabsf(next) >= kPreFar && fabsf(to) < -kPreNoKey);
               if (__any_sync(0xffffffffu, to > old && old != kPreNoKey)) {
                 // O takes the new reference
                 settled((it + j + 1) & 1);

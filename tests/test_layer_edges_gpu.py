@@ -191,6 +191,50 @@ def test_attention_of_as_many_keys_as_an_integer_holds(rows):
         assert (np.abs(lse[i] - wlse[0]) <= FP32 * (1 + span[0] + np.abs(wlse[0]))).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("weight", [20.3, 25.1])
+@pytest.mark.parametrize("lengths", [[(1, 1 << 17), (1, 900)], [(1, 1 << 17)] * 304, [(70, 1 << 17)] * 160])
+def test_attention_of_one_key_above_a_long_flat_tail(lengths, weight, dtype):
+    """The first key weighs 1, each other one 2^-20.3 (all of them 10 %) or 2^-25.1 (0.4 %), all of one sign in
+    V.  Next to a sum of 1 an fp32 accumulator of the tensor cores keeps multiples of 2^-23, so a key may
+    lose that much; a probability's own rounding (2^-25) lies below.  (Many sequences: one that is cut has
+    its first key in one of its runs only.)"""
+    c = _pool_case(lengths, 1, 1, 64, 16, dtype, seed=38, pool=32)
+    codes, vcodes, scales, vscales = R.sections(c["cache_np"], 64)
+    codes[:], vcodes[:], scales[:], vscales[:] = 0, 0x22, 0x38, 0x38  # K 0, V 1
+    first, tail = c["table_np"].min(), c["table_np"].max()
+    assert first != tail
+    codes[first, :, 0, 0, :8] = 0x22  # a key of 1 in each of the first 16 dimensions
+    c["table_np"][:] = tail
+    c["table_np"][:, 0] = first
+    c["table"], c["cache"] = _i32(c["table_np"]), torch.tensor(c["cache_np"]).cuda()
+    c["q"].fill_(1)
+    scale = weight * math.log(2) / (16 * K_SCALE)
+    _attend(c, scale=scale)
+    out, lse = _np(c["out"]) / V_SCALE, c["lse"].cpu().numpy()
+    for b, (m, n) in enumerate(lengths):
+        for i in {0, m // 2, m - 1}:
+            keys, row = n - m + i + 1, c["start_np"][b] + i
+            tol = HALF_UNIT[dtype] + 2.0 ** -11 + 2.0 ** -23 * keys
+            assert (np.abs(out[row] - 1) <= tol).all(), (keys, out[row, 0, :2])
+            want = weight * math.log(2) + math.log1p((keys - 1) * 2.0 ** -weight)
+            assert abs(lse[row, 0] - want) <= FP32 * (1 + 2 * want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("lengths", [[(6, 700), (2, 90)], [(200, 900)]])
+def test_an_infinite_query_leaves_the_other_rows_as_they_are(lengths, dtype):
+    c = _attend_case(lengths, 4, 2, 128, 16, dtype, seed=39)
+    _attend(c)
+    want = c["out"].clone()
+    other = torch.ones_like(want, dtype=torch.bool)
+    for i, h, sign in ((1, 1, 1), (3, 2, -1), (5, 0, 1)):
+        c["q"][i, h, 7 * h] = sign * math.inf
+        other[i, h] = False
+    _attend(c)
+    assert torch.equal(c["out"][other], want[other])
+
+
 # ------------------------------------------------------------------ bounded waits
 
 @pytest.mark.parametrize("heads", [(32, 32), (64, 4)])

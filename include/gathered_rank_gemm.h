@@ -573,7 +573,11 @@ int lora_kv4_append_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *q_out
  * a cached value (without the cache's factor) is exact in fp16, a bf16 row of q
  * is scaled by a power of two so that its largest element lies in [2^14, 2^15)
  * (exact but for elements below 2^-29 of the row's largest), and a
- * probability is rounded once to fp16 (2^-11 of it).  A NaN among a row's keys,
+ * probability is rounded once to fp16 (2^-11 of it; 2^-25 of the row's largest
+ * where it lies below 2^-14 of that).  The weighted sum of V is accumulated in fp32
+ * by the tensor cores, so a key may lose 2^-23 of the row's largest weight: a tail
+ * of n keys of less weight than that each is counted in lse, and to within n 2^-23 in
+ * out.  Scores may be of any size that fp32 holds.  A NaN among a row's keys,
  * or in its q, makes the row NaN; one in V the 16 dimensions of its scale; rows
  * that do not see that key keep their values.  Results do not depend on timing
  * or on what else is in the batch's workspace.  The kernels' waits are bounded:

@@ -18,6 +18,9 @@ constexpr int kNormThreads = 384;      // of a CTA; more only where a row needs 
 constexpr int kNormMaxThreads = 1024;
 constexpr float kMinScale = 7.888609052210118e-31f;  // 2^-100
 constexpr float kInv448 = 1.0f / 448.0f;
+constexpr float kMaxFloat = 3.40282347e38f;
+constexpr float kMaxInv = 1073741824.0f;  // 2^30: mean(z^2) + eps below 2^-60
+constexpr float kUp = 1208925819614629174706176.0f, kDown = 1.0f / kUp;  // 2^80, 2^-80
 
 // max(a / 448, 2^-100) of a maximum taken over abs_bits: NaN stays NaN.
 __device__ __forceinline__ float scale_of(uint32_t bits) {
@@ -86,7 +89,29 @@ __global__ void __launch_bounds__(MAXT) lora_add_rmsnorm_kernel(const NormArgs p
   sum = lane < warps ? s_sum[lane] : 0.0f;
 #pragma unroll
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float inv = rsqrtf(sum / static_cast<float>(p.hidden) + p.eps);
+  float inv = rsqrtf(sum / static_cast<float>(p.hidden) + p.eps);
+  if (sum > kMaxFloat || inv > kMaxInv) {
+    // rare: squares that leave the range, whose mean does not leave its root's.  The row
+    // is scaled by a power of two and summed again (the whole CTA comes here).
+    const float f = sum > kMaxFloat ? kDown : kUp;
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < CH; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        z[i][e] *= f;
+        sum += z[i][e] * z[i][e];
+      }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncthreads();
+    if (lane == 0) s_sum[warp] = sum;
+    __syncthreads();
+    sum = lane < warps ? s_sum[lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    inv = rsqrtf(sum / static_cast<float>(p.hidden) + p.eps * f * f);
+  }
   uint32_t top = 0, tops[CH];
 #pragma unroll
   for (int i = 0; i < CH; ++i) {

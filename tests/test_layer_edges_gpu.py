@@ -8,7 +8,7 @@ import pytest
 from gathered_rank_gemm_gb300 import binding as B
 from tests import layer_ref as R
 from tests.test_layer_gpu import (BOTTOM, FP32, HALF_UNIT, K_SCALE, V_SCALE, _attend, _attend_case,  # noqa: F401
-                                  _attend_check, _i32, _np, lib)
+                                  _attend_check, _i32, _norm_case, _norm_check, _np, lib)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -233,6 +233,20 @@ def test_an_infinite_query_leaves_the_other_rows_as_they_are(lengths, dtype):
         other[i, h] = False
     _attend(c)
     assert torch.equal(c["out"][other], want[other])
+
+
+# ------------------------------------------------------------------ the norm's range and its codes
+
+@pytest.mark.parametrize("hidden,groups", [(8, 1), (512, 4), (4096, 32), (11008, 1), (32768, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_norm_of_rows_whose_squares_leave_the_range(hidden, groups, dtype):
+    x, _, w, out, nt = _norm_case(8, 8, hidden, groups, dtype, False, seed=41)
+    factors = [2.0 ** 60, 2.0 ** 100, 2.0 ** 122, 2.0 ** -70, 2.0 ** -110, 1.0, 2.0 ** 63, 2.0 ** -62] if dtype == "bf16" \
+        else [2.0 ** 12, 2.0 ** -20, 1.0, 2.0 ** -8, 2.0 ** 10, 2.0 ** -14, 2.0 ** 4, 2.0 ** 8]
+    x.mul_(torch.tensor(factors, device="cuda", dtype=torch.float64).to(x.dtype)[:, None])
+    for eps in (0.0, 1e-30):
+        B.lora_add_rmsnorm(x, w, eps, nt, **out)
+        _norm_check(x, None, w, out, 8, groups, dtype, eps=eps)
 
 
 # ------------------------------------------------------------------ bounded waits

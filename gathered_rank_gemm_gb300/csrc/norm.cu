@@ -161,10 +161,16 @@ __global__ void __launch_bounds__(MAXT) lora_add_rmsnorm_kernel(const NormArgs p
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * blockDim.x;
-    const float f = 1.0f / scale[i];
+    // n / scale rounded once (Markstein, 1990): with the correctly rounded reciprocal f,
+    // q + (n - q scale) f is the quotient's nearest.  (An infinite scale leaves q as it is.)
+    const float f = __frcp_rn(scale[i]), d = scale[i] > kMaxFloat ? 0.0f : scale[i];
+    auto over = [&](float n) {
+      const float q = __fmul_rn(n, f);
+      return __fmaf_rn(__fmaf_rn(-q, d, n), f, q);
+    };
     uint32_t b[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) b[e] = f32x2_to_e4m3(z[i][2 * e] * f, z[i][2 * e + 1] * f);
+    for (int e = 0; e < 4; ++e) b[e] = f32x2_to_e4m3(over(z[i][2 * e]), over(z[i][2 * e + 1]));
     if (c < chunks) y8[c] = make_uint2(b[0] | (b[1] << 16), b[2] | (b[3] << 16));
   }
 }

@@ -431,9 +431,9 @@ int lora_apply_noalloc(const int32_t *token_lora_mapping, const int32_t *num_tok
  *   residual_out[t][h] = 16-bit(z[t][h])
  *   n[t][h]     = z[t][h] / sqrt(mean_h(z[t][h]^2) + eps) * weight[h]  (fp32)
  *   y[t][h]     = 16-bit(n[t][h])
- *   y8_scale[t][g] = max(max_{h in group g} |n[t][h]| / 448, 2^-100)
- *   y8[t][h]    = e4m3(n[t][h] / y8_scale[t][h / group]), to the nearest, ties
- *                 to even, saturating at 448
+ *   y8_scale[t][g] = max(max_{h in group g} |n[t][h]| * (1 / 448), 2^-100)
+ *   y8[t][h]    = e4m3(n[t][h] / y8_scale[t][h / group]), the quotient rounded once
+ *                 to fp32, then to the nearest, ties to even, saturating at 448
  * for t < n; rows t >= n are neither read nor written.  A NaN among a row's
  * z makes the row's n, scales and codes NaN.
  *

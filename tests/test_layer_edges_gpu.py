@@ -249,6 +249,30 @@ def test_norm_of_rows_whose_squares_leave_the_range(hidden, groups, dtype):
         _norm_check(x, None, w, out, 8, groups, dtype, eps=eps)
 
 
+@pytest.mark.parametrize("hidden,groups", [(4096, 32), (8192, 64), (11008, 86)])
+def test_norm_codes_are_the_nearest(hidden, groups):
+    """Rows of +-1, so that mean(z^2) is 1 and n is the weight, and weights of t times the middle between two
+    codes in a group whose scale is t: a quotient that is off by its last bit takes the wrong code."""
+    rows = 4
+    g = torch.Generator().manual_seed(42)
+    t = (torch.randint(16, 32, (groups, 1), generator=g) * 2 + 1).float()  # 33, 35, ... 63
+    w = t * (torch.randint(8, 16, (groups, 128), generator=g) * 2 + 1) / 16 * 2.0 ** torch.randint(-4, 5, (groups, 128), generator=g)
+    w[:, 5] = 448 * t[:, 0]
+    w = w.flatten().half()
+    x = (torch.randint(0, 2, (rows, hidden), generator=g) * 2.0 - 1).half()
+    out = dict(y=torch.zeros(rows, hidden, dtype=torch.float16, device="cuda"),
+               y8=torch.zeros(rows, hidden, device="cuda").to(torch.float8_e4m3fn),
+               y8_scale=torch.zeros(rows, groups, device="cuda"))
+    B.lora_add_rmsnorm(x.cuda(), w.cuda(), 0.0, _i32([rows]), **out)
+    n = (x.float() * w.float()).numpy()
+    assert np.array_equal(_np(out["y"]), n)
+    s = np.repeat(out["y8_scale"].cpu().numpy(), 128, 1)
+    assert (np.abs(s / np.repeat(t.numpy(), 128, 0).T - 1) <= 2.0 ** -23).all()
+    want = np.sign(n) * R.E4M3[R.to_e4m3(np.abs(n / s))]  # the quotient rounded once to fp32
+    off = int((want != _np(out["y8"])).sum())
+    assert off == 0, f"{off} of {n.size} codes are not the nearest"
+
+
 # ------------------------------------------------------------------ bounded waits
 
 @pytest.mark.parametrize("heads", [(32, 32), (64, 4)])

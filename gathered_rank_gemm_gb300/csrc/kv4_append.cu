@@ -79,9 +79,9 @@ __device__ __forceinline__ uint32_t append_block(float (&v)[16], float factor, f
   uint32_t code[2] = {0, 0};
   if (scale > 0.0f) {
     // Quotients v / scale, correctly rounded (Markstein, 1990: with the correctly
-    // rounded reciprocal r, q + (v - q scale) r rounds to the quotient's nearest
-    // where q = v r).  At the largest scale v may be as large as infinity: what
-    // is beyond 6 * 448 becomes 6 either way.
+    // rounded reciprocal r, q - (q scale - v) r rounds to the quotient's nearest
+    // where q = v r; in this order of the signs -0 stays -0).  At the largest scale v
+    // may be as large as infinity: what is beyond 6 * 448 becomes 6 either way.
     const float r = __frcp_rn(scale);
     if (s8 == 0x7Eu) {
 #pragma unroll
@@ -90,7 +90,7 @@ __device__ __forceinline__ uint32_t append_block(float (&v)[16], float factor, f
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const float q = __fmul_rn(v[i], r);
-      v[i] = __fmaf_rn(__fmaf_rn(-q, scale, v[i]), r, q);
+      v[i] = __fmaf_rn(-__fmaf_rn(q, scale, -v[i]), r, q);
     }
     code[0] = f32x8_to_e2m1(v);
     code[1] = f32x8_to_e2m1(v + 8);

@@ -7,8 +7,9 @@ import pytest
 
 from gathered_rank_gemm_gb300 import binding as B
 from tests import layer_ref as R
-from tests.test_layer_gpu import (BOTTOM, FP32, HALF_UNIT, K_SCALE, V_SCALE, _attend, _attend_case,  # noqa: F401
-                                  _attend_check, _i32, _norm_case, _norm_check, _np, lib)
+from tests.test_layer_gpu import (BOTTOM, FP32, HALF_UNIT, K_SCALE, V_SCALE, _append, _append_case,  # noqa: F401
+                                  _append_check, _attend, _attend_case, _attend_check, _i32, _norm_case,
+                                  _norm_check, _np, lib)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -271,6 +272,23 @@ def test_norm_codes_are_the_nearest(hidden, groups):
     want = np.sign(n) * R.E4M3[R.to_e4m3(np.abs(n / s))]  # the quotient rounded once to fp32
     off = int((want != _np(out["y8"])).sum())
     assert off == 0, f"{off} of {n.size} codes are not the nearest"
+
+
+# ------------------------------------------------------------------ the append's zeros
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_append_keeps_the_sign_of_a_zero(d):
+    c = _append_case(6, 6, 1, 2, d, 16, 0, False, "bf16", seed=43)
+    c["slots"] = _i32(np.arange(6))
+    for x in ("k", "v"):
+        t = c[x]
+        t[0, :, ::3] = -0.0
+        t[1, :, ::3] = 0.0
+        t[2] = -0.0          # a block of zeros has scale 0 and codes 0
+        t[3, :, 1:16] = -0.0
+        t[4, :, 5] = -1e-30  # rounds to -0
+    _append(c)
+    _append_check(c, 6, d, 16, "bf16")
 
 
 # ------------------------------------------------------------------ bounded waits

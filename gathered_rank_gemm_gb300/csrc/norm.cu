@@ -162,11 +162,12 @@ __global__ void __launch_bounds__(MAXT) lora_add_rmsnorm_kernel(const NormArgs p
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * blockDim.x;
     // n / scale rounded once (Markstein, 1990): with the correctly rounded reciprocal f,
-    // q + (n - q scale) f is the quotient's nearest.  (An infinite scale leaves q as it is.)
+    // q - (q scale - n) f is the quotient's nearest; in this order of the signs -0 stays -0.
+    // (An infinite scale leaves q as it is.)
     const float f = __frcp_rn(scale[i]), d = scale[i] > kMaxFloat ? 0.0f : scale[i];
     auto over = [&](float n) {
       const float q = __fmul_rn(n, f);
-      return __fmaf_rn(__fmaf_rn(-q, d, n), f, q);
+      return __fmaf_rn(-__fmaf_rn(q, d, -n), f, q);
     };
     uint32_t b[4];
 #pragma unroll

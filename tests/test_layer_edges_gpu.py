@@ -274,6 +274,32 @@ def test_norm_codes_are_the_nearest(hidden, groups):
     assert off == 0, f"{off} of {n.size} codes are not the nearest"
 
 
+@pytest.mark.parametrize("groups", [1, 4])
+def test_norm_keeps_the_sign_of_a_zero_and_the_ends_of_a_scale(groups):
+    x, _, w, out, nt = _norm_case(4, 4, 512, groups, "bf16", False, seed=45)
+    w.abs_()
+    x[0, ::3], x[0, 1::3] = -0.0, 0.0
+    x[1] = -0.0
+    x[2, 5] = math.inf  # a mean of infinity: the others are 0
+    x[3, ::2] = 0.0
+    B.lora_add_rmsnorm(x, w, 1e-5, nt, **out)
+    code = out["y8"].view(torch.uint8)
+    assert (code[0, ::3] == 0x80).all() and (code[0, 1::3] == 0).all() and (code[1] == 0x80).all()
+    assert torch.equal(torch.signbit(out["y"][:2].float()), torch.signbit(x[:2].float()))
+    n = out["y"][2].float()
+    assert torch.isnan(n[5]) and (n[:5] == 0).all() and (n[6:] == 0).all()
+    _norm_check(x[3:], None, w, {k: v[3:] for k, v in out.items()}, 1, groups, "bf16")
+    # weights whose group's largest n, and its scale, are infinite: finite n / infinity is 0
+    w = torch.full((512,), 2.0 ** 127, dtype=torch.bfloat16, device="cuda")
+    x = torch.ones(4, 512, dtype=torch.bfloat16, device="cuda")
+    x[:, 7] = 200.0
+    w[9:] = 1.0
+    B.lora_add_rmsnorm(x, w, 1e-5, nt, **out)
+    n, s, y8 = out["y"].float(), out["y8_scale"], out["y8"].float()
+    assert torch.isinf(n[:, 7]).all() and torch.isinf(s[:, 0]).all()
+    assert torch.isnan(y8[:, 7]).all() and (y8[:, 9:128] == 0).all() and (y8[:, :7] == 0).all()
+
+
 # ------------------------------------------------------------------ the append's zeros
 
 @pytest.mark.parametrize("d", [64, 128])

@@ -138,36 +138,42 @@ __global__ void __launch_bounds__(MAXT) lora_add_rmsnorm_kernel(const NormArgs p
     }
   }
   if (!p.y8) return;
-  float scale[CH];
+  float down[CH], scale[CH];  // a scale's reciprocal, and the scale where it is finite
+  auto use = [&](int i, float s) {
+    down[i] = __frcp_rn(s);
+    scale[i] = s > kMaxFloat ? 0.0f : s;
+  };
   if (p.group == p.hidden) {
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) s_max[warp] = top;
     __syncthreads();
     top = __reduce_max_sync(0xffffffffu, lane < warps ? s_max[lane] : 0u);
+    const float s = scale_of(top);
+    if (tid == 0) p.y8_scale[t] = s;
+    use(0, s);
 #pragma unroll
-    for (int i = 0; i < CH; ++i) scale[i] = scale_of(top);
-    if (tid == 0) p.y8_scale[t] = scale[0];
+    for (int i = 1; i < CH; ++i) down[i] = down[0], scale[i] = scale[0];
   } else {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
 #pragma unroll
       for (int o = 8; o; o >>= 1) tops[i] = max(tops[i], __shfl_xor_sync(0xffffffffu, tops[i], o));
-      scale[i] = scale_of(tops[i]);
+      const float s = scale_of(tops[i]);
       const int c = tid + i * blockDim.x;
-      if (c < chunks && (lane & 15) == 0) p.y8_scale[t * (chunks >> 4) + (c >> 4)] = scale[i];
+      if (c < chunks && (lane & 15) == 0) p.y8_scale[t * (chunks >> 4) + (c >> 4)] = s;
+      use(i, s);
     }
   }
   uint2* y8 = reinterpret_cast<uint2*>(p.y8 + t * p.y8_stride);
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int c = tid + i * blockDim.x;
-    // n / scale rounded once (Markstein, 1990): with the correctly rounded reciprocal f,
-    // q - (q scale - n) f is the quotient's nearest; in this order of the signs -0 stays -0.
+    // n / scale rounded once (Markstein, 1990): with the correctly rounded reciprocal r,
+    // q - (q scale - n) r is the quotient's nearest; in this order of the signs -0 stays -0.
     // (An infinite scale leaves q as it is.)
-    const float f = __frcp_rn(scale[i]), d = scale[i] > kMaxFloat ? 0.0f : scale[i];
     auto over = [&](float n) {
-      const float q = __fmul_rn(n, f);
-      return __fmaf_rn(-__fmaf_rn(q, d, -n), f, q);
+      const float q = __fmul_rn(n, down[i]);
+      return __fmaf_rn(-__fmaf_rn(q, scale[i], -n), down[i], q);
     };
     uint32_t b[4];
 #pragma unroll

@@ -112,15 +112,25 @@ struct Cache {
       refuse("cache", "has a size out of range");
   }
 };
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(name, "must be true or false");
+  }
+  return v != 0;
+}
+// The stream's handle: of the device's current one, of a torch stream, or the number itself.
 void* stream_of(PyObject* o, c10::Device device) {
   if (o == Py_None) return c10::cuda::getCurrentCUDAStream(device.index()).stream();
   PyObject* p = PyObject_GetAttrString(o, "cuda_stream");
-  if (!p) {
+  if (!p) PyErr_Clear();
+  void* s = PyLong_AsVoidPtr(p ? p : o);
+  Py_XDECREF(p);
+  if (PyErr_Occurred()) {
     PyErr_Clear();
-    return PyLong_AsVoidPtr(o);
+    refuse("stream", "must be a CUDA stream, its handle as a whole number, or None");
   }
-  void* s = PyLong_AsVoidPtr(p);
-  Py_DECREF(p);
   return s;
 }
 
@@ -132,9 +142,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, F&& body) {
     return nullptr;
   }
   try {
-    const int rc = body();
-    if (PyErr_Occurred()) return nullptr;
-    return PyLong_FromLong(rc);
+    return PyLong_FromLong(body());  // (body leaves no Python error behind: it refuses)
   } catch (const Refused& e) {
     PyErr_SetString(PyExc_ValueError, e.what());
   } catch (const std::exception& e) {
@@ -212,7 +220,7 @@ PyObject* kv4_append(PyObject*, Args a, Py_ssize_t n) {
       rp = vec<float>(*rope, "rope", like, at::kFloat, {positions, rope_dim});
       pp = vec<int32_t>(*pos, "positions", like, at::kInt, {count});
     }
-    const int interleaved = PyObject_IsTrue(a[9]);
+    const int interleaved = truth(a[9], "interleaved") ? 1 : 0;
     const float k_scale = static_cast<float>(number(a[10], "k_scale"));
     const float v_scale = static_cast<float>(number(a[11], "v_scale"));
     uint16_t* khp = kh ? vec<uint16_t>(*kh, "k_held", like, like.type, shape) : nullptr;

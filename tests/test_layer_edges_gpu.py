@@ -317,6 +317,38 @@ def test_append_keeps_the_sign_of_a_zero(d):
     _append_check(c, 6, d, 16, "bf16")
 
 
+# ------------------------------------------------------------------ refusals come before the launch
+
+class _NotAStream:
+    cuda_stream = "none"
+
+
+@pytest.mark.parametrize("stream", ["0", 1.5, object(), _NotAStream()])
+def test_a_wrong_stream_is_refused_and_nothing_is_launched(stream):
+    x, r, w, out, nt = _norm_case(4, 4, 256, 2, "bf16")
+    c = _append_case(4, 4, 2, 1, 64, 16, 64, False, "bf16")
+    a = _attend_case([(1, 20)], 4, 2, 64, 16, "bf16")
+    with pytest.raises(ValueError):
+        B.lora_add_rmsnorm(x, w, 1e-5, nt, residual=r, stream=stream, **out)
+    with pytest.raises(ValueError):
+        _append(c, stream=stream)
+    with pytest.raises(ValueError):
+        _attend(a, stream=stream)
+    torch.cuda.synchronize()
+    assert all((t.float() == 7).all() for t in out.values())
+    assert (c["cache"] == 0xA5).all() and (c["q_out"] == 7).all()
+    assert (a["out"] == 7).all() and (a["lse"] == 7).all()
+
+
+def test_a_truth_value_that_has_none_is_refused():
+    c = _append_case(4, 4, 2, 1, 64, 16, 64, False, "bf16")
+    c["interleaved"] = np.zeros(2)  # its truth is ambiguous
+    with pytest.raises(ValueError):
+        _append(c)
+    torch.cuda.synchronize()
+    assert (c["cache"] == 0xA5).all() and (c["q_out"] == 7).all()
+
+
 # ------------------------------------------------------------------ bounded waits
 
 @pytest.mark.parametrize("heads", [(32, 32), (64, 4)])

@@ -4,12 +4,15 @@ Each ``csrc/*.cu`` file is compiled to an object with nvcc in parallel, then
 the objects are linked into one shared library that exports only the C ABI of
 ``include/gathered_rank_gemm.h``.  ``native/marshal.cpp`` becomes the Python module
 ``_native.so`` (argument marshalling of the per-token calls, against the installed
-PyTorch).  No CPU fallback is built.
+PyTorch); the library does not need it, and is there even where that module does not
+compile.  No CPU fallback is built.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -23,6 +26,7 @@ LIB_NAME = "libgathered_rank_gemm.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 NATIVE_SRC = os.path.join(HERE, "native", "marshal.cpp")
 NATIVE_PATH = os.path.join(HERE, "_native.so")
+NATIVE_FOR = os.path.join(BUILD_DIR, "native_for")  # the PyTorch that _native.so was compiled against
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
               "--expt-relaxed-constexpr", "-Xptxas", "-warn-spills"]
@@ -39,16 +43,38 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _headers():
+    return glob.glob(os.path.join(ROOT, "include", "*.h")) + [os.path.abspath(__file__)]
+
+
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h"))
-            + glob.glob(os.path.join(ROOT, "include", "*.h")) + [NATIVE_SRC, os.path.abspath(__file__)])
+            + _headers())
+
+
+def _older(path, deps) -> bool:
+    return not os.path.exists(path) or any(os.path.getmtime(p) > os.path.getmtime(path) for p in deps)
+
+
+def _pytorch() -> str:
+    """The installed PyTorch's version and place (without importing it)."""
+    spec = importlib.util.find_spec("torch")
+    return f"{importlib.metadata.version('torch')} {spec.origin}" if spec else "none"
+
+
+def native_is_stale() -> bool:
+    if _older(NATIVE_PATH, [NATIVE_SRC, *_headers()]) or not os.path.exists(NATIVE_FOR):
+        return True
+    with open(NATIVE_FOR) as f:
+        return f.read() != _pytorch()
+
+
+def library_is_stale() -> bool:
+    return _older(LIB_PATH, _deps())
 
 
 def is_stale() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(NATIVE_PATH):
-        return True
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(NATIVE_PATH))
-    return any(os.path.getmtime(p) > t for p in _deps())
+    return library_is_stale() or native_is_stale()
 
 
 def _compile_native() -> str:
@@ -77,11 +103,15 @@ def _link_native(obj: str) -> None:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, NATIVE_PATH)
+    with open(NATIVE_FOR, "w") as f:
+        f.write(_pytorch())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile and link the library if any source changed; returns its path."""
-    if not force and not is_stale():
+    """Compile and link the library, then the module, where a source changed; returns the library's
+    path.  The library is in place before a failure to compile the module is raised."""
+    library, module = force or library_is_stale(), force or native_is_stale()
+    if not library and not module:
         return LIB_PATH
     nvcc = nvcc_path()
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -98,16 +128,17 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
-        native = ex.submit(_compile_native)
-        objs = list(ex.map(compile_one, _sources()))
-        native = native.result()
-    tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, LIB_PATH)
-    _link_native(native)
+        native = ex.submit(_compile_native) if module else None
+        objs = list(ex.map(compile_one, _sources() if library else ()))
+    if library:
+        tmp = LIB_PATH + f".tmp{os.getpid()}"
+        cmd = [nvcc, *ARCH_FLAGS, "-shared", "-o", tmp, *objs]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+        os.replace(tmp, LIB_PATH)
+    if native:
+        _link_native(native.result())
     return LIB_PATH
 
 

@@ -12,9 +12,10 @@
 namespace grg {
 
 namespace {
-// Measured on 8000 tokens of 32 q and 8 kv heads (210 MB): 40.3 us with CTAs of 64
-// threads, 41.0 us of 96, 44.1 us of 192 (8192 tokens of 64 and 8 heads: 71.1, 77.0 and
-// 81.8 us), all with 80 registers a thread; 43.2 us with 64 registers (spills).
+// Measured on 8000 tokens of 32 q and 8 kv heads (210 MB, 0.76 of measured HBM): 40.5 us with
+// CTAs of 64 threads, 41.1 us of 96, 44.3 us of 192 (8192 tokens of 64 and 8 heads: 66.3,
+// 70.6 and 75.9 us), all with 80 registers a thread (16 bytes spilled); with 64 registers
+// 41.9 us, and 61.2 us on the second case, but 5.2 against 4.3 us for 256 tokens.
 constexpr int kAppendThreads = 128;
 constexpr int kAppendCtas = 6;
 

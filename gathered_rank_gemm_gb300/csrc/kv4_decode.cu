@@ -26,12 +26,13 @@
 // timing.
 //
 // Measured (GB300, bf16): 256 sequences of up to 4096 keys, 32 / 8 heads of 128
-// (608 MB): 127 us, 0.71 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
-// MB): 148 us, 0.78; one of 700 keys: 8.0 us.  Bound by issue: 306 instructions a
-// block of 16 keys (64 conversions and 64 scalings of pairs, 16 products, the
-// rest the softmax and the turning of V), 118 cycles an SM where HBM would give it
-// in 98.  A short sequence is bound by its chain of latencies: lengths, line, page
-// table, copies, products, join.
+// (608 MB): 125 us, 0.72 of measured HBM; 2 of 60000 to 100000 keys, 32 / 32 heads (785
+// MB): 145.5 us, 0.80; one of 700 keys: 7.8 us.  Bound by fixed latencies: some 300
+// instructions a block of 16 keys (64 conversions and 64 scalings of pairs, 16 products,
+// the rest the softmax and the turning of V) fill 60 % of the issue slots; the four warps
+// that a scheduler has (the registers allow no more) wait for each other's results. (All
+// of a batch of 256's instructions would issue in some 70 us.)  A short sequence is
+// bound by its chain of latencies: lengths, line, page table, copies, products, join.
 #include "kv4_attention.cuh"
 #include "kv4_attention.h"
 #include "launch.h"
@@ -43,8 +44,9 @@ constexpr int kDecSmsMax = 160;                   // SMs that the workspace has 
 constexpr int kDecWorkersMax = kDecSmsMax * 16;   // warps on them
 constexpr int kPartialSlots = kDecWorkersMax * 2;
 constexpr float kNoKey = -3e38f;  // the running maximum before any key
-// What an item costs besides its blocks, in blocks (256 sequences up to 4096 keys: 4 130.7
-// us, 6 127.0 us, 10 128.5 us; 64 of 2000 to 8000: 79.8, 78.7, 80.5 us).
+// What an item costs besides its blocks, in blocks (256 sequences up to 4096 keys: 4 128.8
+// us, 6 125.0 us, 10 126.0 us; 64 of 2000 to 8000: 79.6, 78.5, 79.2 us; but 100 of 700, cut:
+// 30.4, 32.5, 32.2 us).
 constexpr int kItemCost = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -135,8 +137,8 @@ __device__ __forceinline__ DecItem dec_item(const Kv4Seq& s, int group, uint32_t
 }
 
 // Warps of a CTA, CTAs of an SM and pairs of blocks in a warp's ring: as many
-// warps as the registers allow (168 a thread with 12 warps, 128 with 16), in one
-// CTA an SM (ONE) or two.
+// warps as the registers allow (168 a thread with 12 warps, 128 with 16; 16 packed rows spill
+// 312 bytes of 128 dimensions, 168 of 64, and 8 rows of 128 92), in one CTA an SM (ONE) or two.
 template <int D, int NT, bool ONE>
 struct DecShape {
   static constexpr int kCtas = ONE ? 1 : 2;
@@ -185,7 +187,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   // ---- the line of units (an item's fixed cost and its blocks) and of items, by
   // sequence: prefix sums over the threads' runs of sequences.  Up to 32 sequences
   // each warp has in its lanes (no barrier on the way: one sequence of 20 keys
-  // 5.25 us so, 5.75 us by the CTA; 64 sequences, which go by the CTA, pay 0.1 us for it).
+  // 5.3 us so, 5.8 us by the CTA; a batch of 256, which goes by the CTA, pays 1 of 125 us for it).
   const bool few = a.num_seqs <= 32;
   const int per_thread = (a.num_seqs + kDecThreads - 1) / kDecThreads;
   auto seq_at = [&](int b) { return per_thread == 1 ? s_seq[b] : Kv4Seq::of(a, b); };
@@ -254,11 +256,12 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   // and back: about 6 us on the way of the last), so items stay whole where the
   // longest runs over a worker's fair share by less than that: 160 blocks of a CTA
   // that has one item, 40 of a CTA that has two, 16 of a warp.  (48 windows of
-  // 2048 keys, 30 rows of 64: 21.8 us whole, 39.3 cut; 150 sequences of 1500 to 2000
-  // keys, two items a CTA: 60 and 72 us; 100 of 700, three: 33.6 and 31.3, so cut.)
-  // A CTA goes before a warp, which takes 0.6 us a block: 8 items of 200 keys 6.9 and
-  // 14.7 us, two items a CTA, 100 to 200 keys, 13.8 and 17.9 us; 20 to 100 keys, 18.7
-  // and 17.2 us.  Else the line of units is cut into equal runs, of warps, or of
+  // 2048 keys, 30 rows of 64: 20.2 us whole, 36.1 cut; 150 sequences of 1500 to 2000
+  // keys, two items a CTA: 42.5 and 49.3 us.  Three are cut, which an item's cost of 4
+  // called for; with 6, 100 sequences of 700 keys take 31.1 us whole and 32.5 cut.)
+  // A CTA goes before a warp, which takes 0.6 us a block: 8 items of 200 keys 5.7 and
+  // 13.3 us, two items a CTA, 100 to 200 keys, 12.8 and 18.2 us; 512 sequences of 20 to
+  // 100 keys, one head, 13.3 and 12.1 us.  Else the line of units is cut into equal runs, of warps, or of
   // CTAs where an item would span over 8 warps' runs (20 sequences of 2000 to 5000
   // keys, 16 rows).
   // (Few divisions: they are on every call's way.)
@@ -961,8 +964,8 @@ int launch_kv4_decode(const Kv4AttnArgs& a, int max_packed_rows, size_t counters
     return f16 ? run_decode<128, 1, true, false>(p, sms, stream)
                : run_decode<128, 1, false, false>(p, sms, stream);
   // Where there can be no more items than SMs, CTAs of all of an SM's warps: 10
-  // sequences of 1000 to 1500 keys, 8 key heads, 16 rows: 15.9 us so, 22.9 us by two an SM;
-  // 60 of 500, 4 key heads: 20.1 us by one, 14.7 us by two.
+  // sequences of 1000 to 1500 keys, 8 key heads, 16 rows: 14.3 us so, 22.0 us by two an SM;
+  // 60 of 500, 4 key heads: 19.4 us by one, 14.0 us by two.
   const long long packed = min(static_cast<long long>(a.max_q_len) * group,
                                static_cast<long long>(max_packed_rows));
   if ((packed + 15) / 16 * a.num_seqs * a.num_kv_heads <= sms)

@@ -25,8 +25,9 @@
 // of its CTAs to finish (as in kv4_decode.cu).  Short items stay whole.
 //
 // Measured (GB300, bf16): 6 chunks of 700 to 2000 rows over 2000 to 5000 keys, 32 / 8
-// heads of 128: 320 us, 1072 TFLOP/s (0.56 of measured); one prompt of 8192 tokens,
-// 32 / 32 heads: 476 us, 1155 TFLOP/s.  Bound by the chain softmax (1400 cycles a tile of
+// heads of 128: 319 us, 1080 TFLOP/s (0.56 of measured), fp16 304 us; heads of 64 264 and
+// 257 us; one prompt of 8192 tokens, 32 / 32 heads of 128: 462 us, 1190 TFLOP/s.  Bound by
+// the chain softmax (1400 cycles a tile of
 // 128 x 128), barrier and issue, two products (1024 at the tensor core's rate): 3390
 // cycles a key tile of two row tiles, whose products alone take 2048.  The issuing warp
 // is held until its products are nearly done, so its own softmax starts some 400 cycles
@@ -45,8 +46,8 @@ constexpr int kPreCtasMax = 160;  // CTAs that the workspace has room for
 constexpr int kPreRows = 256;     // packed rows of an item
 constexpr int kPreKeys = 128;     // keys of a tile
 // What the line counts: a key tile of two row tiles, of one, and an item's start and
-// end (12: 8192 rows in a window of 1000 122.8 us, 16: 117.1 us; 8 and 28 cost 3 % and 1 %
-// on 6 chunks).
+// end (12: 4000 rows in a window of 1000 123.8 us, 16: 118.4 us; 8 and 28 cost 3 % on 6
+// chunks).
 constexpr int kCostTwo = 3, kCostOne = 2, kCostItem = 16;
 constexpr int kWholeTiles = 8;    // an item of so few key tiles is not cut for the sake of idle CTAs
 constexpr int kStagePitch = 80;   // bytes of a staged row: 32 values of 16 bits, and 16 against bank conflicts
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         cp_async_wait<0>();
         float down = 1.0f;  // (fp16 rows need no factor)
         if constexpr (!F16) {
-#pragma unroll 4  // (by 8 or 16: 343 us instead of 320 on the case above, by 2: 326)
+#pragma unroll 4
           for (int i2 = 0; i2 < PASSES; ++i2) {
             uint4* at = reinterpret_cast<uint4*>(smem + chunk(i2));
             const uint4 raw_q = *at;
@@ -584,8 +585,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           // proportion) ref is taken off S first, in TMEM, which leaves 0 at the maximum
           // itself; each of the warp's tiles looks for its maximum then.  Against the
           // tile's own maximum no p is above 2, so no tile is done a third time.
-          // (m == kPreTaken holds for a whole warp; with a vote on it ptxas makes 351 us into
-          // 331 for 128 dimensions, 6 chunks, and 255 into 276 for 64.)
+          // (m == kPreTaken holds for a whole warp, with or without a vote.  With it ptxas's
+          // schedule takes 319 us for 128 dimensions, 6 chunks, and 278 for 64; without it 326
+          // and 262.)
           bool again = j == 0 || (D == 128 ? __any_sync(0xffffffffu, m == kPreTaken) : m == kPreTaken);
           while (true) {
             cta_abort.wait(bar(sh.s_full[t]), ns & 1);
@@ -1002,9 +1004,9 @@ namespace {
 // Sequences of up to kDecodeRows packed rows take the decode kernel, the others
 // the prefill kernel; a batch whose bound allows no long sequence does not launch
 // the latter.  Measured, by the decode and by the prefill kernel: 48 windows of 2048
-// keys with up to 30 packed rows of 64 20.7 and 51.2 us; 64 sequences of 2000 keys with 32
-// packed rows of 128 112 and 130 us, with 64 190 and 131 us; 16 of 2000 with 48 rows 56.6
-// and 47.9 us.
+// keys with up to 30 packed rows of 64 20.2 and 55.4 us; 64 sequences of 2000 keys with 32
+// packed rows of 128 110 and 131 us, with 64 186 and 131 us; 16 of 2000 with 48 rows 55.1
+// and 48.0 us.
 constexpr int kDecodeRows = 32;
 
 long long packed_bound(long long max_q_len, int num_q_heads, int num_kv_heads) {

@@ -5,8 +5,8 @@
 // in registers between its one read and its one write, 16-byte accesses.  A
 // scale of 128 columns is the maximum over 16 neighbouring lanes.
 // Measured (GB300, bf16, 16-bit and 8-bit outputs): 8192 rows of 4096 46.2 us, 0.97 of
-// the measured copy rate; 777 of 11008 (fp16) 15.1 us, 0.75: CTAs come and go in two and
-// a half waves; 256 of 4096 2.7 us and one row 2.1 us, where a launch is about 2.
+// the measured copy rate; 777 of 11008 (fp16) 15.8 us, 0.72: CTAs come and go in two and
+// a half waves; 256 of 4096 2.9 us and one row 2.2 us, where a launch is about 2.
 #include "kv4.cuh"
 #include "launch.h"
 #include "layer.h"
@@ -195,9 +195,9 @@ int run_norm(const NormArgs& a, bool f16, cudaStream_t stream) {
 }  // namespace
 
 // Chunks a thread holds: few for short rows, whose CTAs would else be small (one row
-// of 4096: 2.1 us with two, 2.3 us with four; 2048 of 5120: 16.4 and 17.2 us), four
-// where two would take more than kNormThreads (4096 of 8192: 46.7 us with
-// four, 49.7 us with two; 777 of 11008: 15.1 and 18.5 us).
+// of 4096: 2.2 us with two, 2.4 us with four; 2048 of 5120: 16.8 and 17.6 us), four
+// where two would take more than kNormThreads (4096 of 8192: 48.0 us with
+// four, 52.8 us with two; 777 of 11008: 15.8 and 19.0 us).
 int launch_add_rmsnorm(const NormArgs& a, bool f16, cudaStream_t stream) {
   const int chunks = a.hidden / 8;
   if (chunks <= 256) return run_norm<1, kNormThreads>(a, f16, stream);

@@ -580,8 +580,9 @@ int lora_kv4_append_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *q_out
  * out.  Scores may be of any size that fp32 holds.  A NaN among a row's keys,
  * or in its q, makes the row NaN; one in V the 16 dimensions of its scale; rows
  * that do not see that key keep their values.  Results do not depend on timing
- * or on what else is in the batch's workspace.  The kernels' waits are bounded:
- * one that gives up sets LORA_STATUS_TIMEOUT, and the call's output is unspecified.
+ * or on what else is in the batch's workspace.  The kernels' waits are bounded
+ * (200 ms): one that gives up sets LORA_STATUS_TIMEOUT, and the call's output is
+ * unspecified; where `status` is NULL nothing else tells.
  */
 size_t lora_kv4_attention_workspace_size(int64_t num_seqs, int64_t max_num_tokens,
                                          int64_t max_q_len, int num_q_heads, int num_kv_heads,

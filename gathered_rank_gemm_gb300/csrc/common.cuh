@@ -258,8 +258,10 @@ __device__ __forceinline__ void cp_async_mbar_arrive(uint32_t bar) {
 // returns false at once, the kernel issues no further copy and stores no
 // output, and before it exits it waits (bounded again, mbar_drain) for the
 // bulk copies it had already issued, so that none is still writing its shared
-// memory when it leaves.  Every block-wide or named barrier is still reached
-// by every thread: giving up changes no control flow around them.
+// memory when it leaves.  (A warp of the 4-bit decode attention whose copies still
+// arrive ends its part first, and begins no other.)  Every block-wide or named
+// barrier is still reached by every thread: giving up changes no control flow
+// around them.
 struct CtaAbort {
   volatile int* flag;           // in shared memory, 0 until a wait runs out
   unsigned long long limit_ns;  // kWaitLimitNs, or 1 ms under the test hook

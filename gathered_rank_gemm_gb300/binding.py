@@ -29,6 +29,7 @@ LORA_STATUS_BAD_LENGTH = 0x40
 LORA_MAX_SLICES = 3
 LORA_MAX_LORAS = 1024
 LORA_MAX_NUM_TOKENS = 1 << 22
+LORA_KV4_MAX_PATH = 512
 
 LORA_NOALLOC_SCRATCH_BYTES = 384 * 1024
 
@@ -41,7 +42,9 @@ EXPORTED = ("lora_workspace_size", "lora_prepare_metadata", "lora_shrink", "lora
             "lora_shrink_partials_f16", "lora_expand_partials_f16", "lora_shrink_expand_path",
             "lora_testing_inject_timeout", "lora_add_rmsnorm", "lora_add_rmsnorm_f16",
             "lora_kv4_append", "lora_kv4_append_f16", "lora_kv4_attention",
-            "lora_kv4_attention_f16", "lora_kv4_attention_workspace_size")
+            "lora_kv4_attention_f16", "lora_kv4_attention_workspace_size",
+            "lora_kv4_tree_attention", "lora_kv4_tree_attention_f16", "lora_kv4_accept",
+            "lora_kv4_key_weights", "lora_kv4_key_weights_f16", "lora_kv4_evict")
 
 LORA_PATH_FUSED = 1
 LORA_PATH_SPLIT_PAIR = 3
@@ -128,6 +131,19 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         getattr(lib, name).restype = i32
         getattr(lib, name).argtypes = [p, i64, p, i64, p, i32, p, i64, i32, i32, i32, f32, f32, p,
                                        p, p, i64, i64, i64, i64, f32, i64, p, sz, p, p]
+    for name in ("lora_kv4_tree_attention", "lora_kv4_tree_attention_f16"):
+        getattr(lib, name).restype = i32
+        getattr(lib, name).argtypes = [p, i64, p, i64, p, i32, p, i64, i32, i32, i32, f32, f32, p,
+                                       p, p, i64, i64, i64, i64, p, i64, f32, i64, p, sz, p, p]
+    lib.lora_kv4_accept.restype = i32
+    lib.lora_kv4_accept.argtypes = [p, i64, i32, i32, i32, p, p, p, i64, i64, p, p, i64, p, p, p]
+    for name in ("lora_kv4_key_weights", "lora_kv4_key_weights_f16"):
+        getattr(lib, name).restype = i32
+        getattr(lib, name).argtypes = [p, i64, p, i64, p, i32, p, i64, i32, i32, i32, f32, p, p, p,
+                                       i64, i64, i64, i64, f32, i64, p, p, i64, p, p]
+    lib.lora_kv4_evict.restype = i32
+    lib.lora_kv4_evict.argtypes = [p, i64, i32, i32, i32, p, p, i64, p, p, p, i64, i64, i64, i64,
+                                   i64, p, p, p]
     lib.lora_kv4_attention_workspace_size.restype = sz
     lib.lora_kv4_attention_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
     _lib = lib
@@ -531,6 +547,58 @@ def lora_kv4_attention(cache, q, out, q_start, kv_len, page_table, max_q_len: in
                                                    k_scale, v_scale, lse, status, stream)
     if rc:
         _check("lora_kv4_attention", rc)
+
+
+def lora_kv4_tree_attention(cache, q, out, q_start, kv_len, page_table, max_q_len: int, tree_mask,
+                            softmax_scale: float, workspace, window: int = 0, k_scale=1.0,
+                            v_scale=1.0, lse=None, status=None, stream=None):
+    """lora_kv4_attention for rows of drafted trees: a sequence's rows are its drafted tokens, whose keys
+    are its last ones.  Bit c % 32 of tree_mask[row][c / 32] (int32 [rows][words], 32 * words >=
+    max_q_len) says that the row sees the sequence's drafted token c: set for its ancestors and
+    itself.  Every row sees the keys in front of the drafted ones, back to its window where window > 0."""
+    rc = (_native or _load_native()).kv4_tree_attention(cache, q, out, q_start, kv_len, page_table,
+                                                        max_q_len, tree_mask, softmax_scale, workspace,
+                                                        window, k_scale, v_scale, lse, status, stream)
+    if rc:
+        _check("lora_kv4_tree_attention", rc)
+
+
+def lora_kv4_accept(cache, q_start, kv_len, page_table, path, path_len, kv_len_out, status=None,
+                    stream=None):
+    """Keeps the accepted path of each sequence's drafted tree: its tokens path[b][i], i < path_len[b]
+    (int32 [sequences][longest path] and [sequences]), move together behind the keys in front of the
+    tree, and kv_len_out (not kv_len itself) takes the new lengths."""
+    rc = (_native or _load_native()).kv4_accept(cache, q_start, kv_len, page_table, path, path_len,
+                                                kv_len_out, status, stream)
+    if rc:
+        _check("lora_kv4_accept", rc)
+
+
+def lora_kv4_key_weights(weights, cache, q, lse, q_start, kv_len, page_table, max_q_len: int,
+                         softmax_scale: float, window: int = 0, k_scale=1.0, path=None,
+                         path_len=None, status=None, stream=None):
+    """Adds to each key's weight (fp32 [sequences][kv heads][capacity]) the probabilities that the rows
+    of q give it, from the lse that lora_kv4_attention has left; the rows' own keys begin at 0.  With
+    path and path_len, the rows are those of a tree's accepted path and kv_len is what
+    lora_kv4_accept has left."""
+    rc = (_native or _load_native()).kv4_key_weights(weights, cache, q, lse, q_start, kv_len, page_table,
+                                                     max_q_len, softmax_scale, window, k_scale, path,
+                                                     path_len, status, stream)
+    if rc:
+        _check("lora_kv4_key_weights", rc)
+
+
+def lora_kv4_evict(cache, weights, key_pos, kv_len, last_pos, page_table, budget: int, kv_len_out,
+                   sink: int = 0, recent: int = 0, status=None, stream=None):
+    """Sequences longer than budget keep that many keys in each head: those of the first `sink` and
+    the newest `recent` positions, then those of the largest weights; kept keys from budget on take
+    the others' places, with their weights and positions.  key_pos (int32, like weights): -1 where a
+    sequence begins; last_pos (int32 [sequences]): the position of its last key.  kv_len_out (not
+    kv_len itself) takes the new lengths.  Afterwards a head's keys are in no order: no window."""
+    rc = (_native or _load_native()).kv4_evict(cache, weights, key_pos, kv_len, last_pos, page_table,
+                                               budget, kv_len_out, sink, recent, status, stream)
+    if rc:
+        _check("lora_kv4_evict", rc)
 
 
 # ------------------------------------------------------------------ buffers

@@ -129,6 +129,18 @@ int kv4_append(const uint16_t* q, int64_t q_row_stride, uint16_t* q_out, int64_t
   return grg::launch_kv4_append(a, f16, static_cast<cudaStream_t>(stream));
 }
 
+bool path_ok(int64_t max_path) { return max_path >= 1 && max_path <= LORA_KV4_MAX_PATH; }
+bool capacity_ok(int64_t capacity) { return capacity >= 1 && capacity <= LORA_KV4_MAX_KEYS; }
+bool seqs_ok(int64_t num_seqs) { return num_seqs >= 1 && num_seqs <= LORA_KV4_MAX_SEQS; }
+// Whether an array of n words and one of m have one in common.
+bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(m) * 4 && y < x + static_cast<uintptr_t>(n) * 4;
+}
+bool table_ok(int64_t table_stride, int page_size) {
+  return table_stride >= 1 && table_stride < (1ll << 31) / page_size;
+}
+
 bool attention_sizes_ok(int64_t num_seqs, int64_t max_num_tokens, int64_t max_q_len,
                         int num_q_heads, int num_kv_heads, int head_dim) {
   return num_seqs >= 1 && num_seqs <= LORA_KV4_MAX_SEQS && tokens_ok(max_num_tokens) &&
@@ -142,8 +154,9 @@ int kv4_attention(const uint16_t* q, int64_t q_row_stride, uint16_t* out, int64_
                   int num_kv_heads, int page_size, int head_dim, float k_scale, float v_scale,
                   const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
                   int64_t table_stride, int64_t num_seqs, int64_t max_num_tokens,
-                  int64_t max_q_len, float softmax_scale, int64_t window, void* workspace,
-                  size_t workspace_bytes, uint32_t* status, void* stream, bool f16) {
+                  int64_t max_q_len, float softmax_scale, int64_t window, const uint32_t* tree_mask,
+                  int tree_words, void* workspace, size_t workspace_bytes, uint32_t* status,
+                  void* stream, bool f16) {
   if (!q || !out || !cache || !q_start || !kv_len || !page_table || !workspace)
     return LORA_ERR_NULL;
   if (!cache_ok(num_pages, num_kv_heads, page_size, head_dim) ||
@@ -152,13 +165,14 @@ int kv4_attention(const uint16_t* q, int64_t q_row_stride, uint16_t* out, int64_
       !factor_ok(k_scale) || !factor_ok(v_scale) || !std::isfinite(softmax_scale) ||
       !(softmax_scale > 0.0f) || !(softmax_scale * k_scale > 0.0f) ||
       !std::isfinite(softmax_scale * k_scale) || window < 0 || window >= (1ll << 31) ||
-      table_stride < 1 || table_stride >= (1ll << 31) / page_size)
+      !table_ok(table_stride, page_size))
     return LORA_ERR_SHAPE;
   const int64_t qw = static_cast<int64_t>(num_q_heads) * head_dim;
   if (!stride_ok(q_row_stride, qw) || !stride_ok(out_row_stride, qw)) return LORA_ERR_SHAPE;
   if (!aligned(q, 16) || q_row_stride % 8 || !aligned(out, 16) || out_row_stride % 8 ||
       !aligned(lse, 4) || !aligned(cache, 16) || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
-      !aligned(page_table, 4) || !aligned(workspace, 16) || !aligned(status, 4))
+      !aligned(page_table, 4) || !aligned(tree_mask, 4) || !aligned(workspace, 16) ||
+      !aligned(status, 4))
     return LORA_ERR_ALIGN;
   if (workspace_bytes < grg::kv4_attention_workspace(num_seqs, max_num_tokens, max_q_len,
                                                      num_q_heads, num_kv_heads, head_dim))
@@ -185,9 +199,63 @@ int kv4_attention(const uint16_t* q, int64_t q_row_stride, uint16_t* out, int64_
   a.max_num_tokens = static_cast<int>(max_num_tokens);
   a.max_q_len = static_cast<int>(max_q_len);
   a.window = static_cast<int>(window);
+  a.tree_mask = tree_mask;
+  a.tree_words = tree_words;
   a.workspace = workspace;
   a.status = status;
   return grg::launch_kv4_attention(a, f16, static_cast<cudaStream_t>(stream));
+}
+
+int kv4_key_weights(float* weights, int64_t capacity, const uint16_t* q, int64_t q_row_stride,
+                    const float* lse, int num_q_heads, const uint8_t* cache, int64_t num_pages,
+                    int num_kv_heads, int page_size, int head_dim, float k_scale,
+                    const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                    int64_t table_stride, int64_t num_seqs, int64_t max_num_tokens,
+                    int64_t max_q_len, float softmax_scale, int64_t window, const int32_t* path,
+                    const int32_t* path_len, int64_t max_path, uint32_t* status, void* stream,
+                    bool f16) {
+  if (!weights || !q || !lse || !cache || !q_start || !kv_len || !page_table ||
+      (path != nullptr) != (path_len != nullptr))
+    return LORA_ERR_NULL;
+  if (!cache_ok(num_pages, num_kv_heads, page_size, head_dim) ||
+      !attention_sizes_ok(num_seqs, max_num_tokens, max_q_len, num_q_heads, num_kv_heads,
+                          head_dim) ||
+      !factor_ok(k_scale) || !std::isfinite(softmax_scale) || !(softmax_scale > 0.0f) ||
+      !(softmax_scale * k_scale > 0.0f) || !std::isfinite(softmax_scale * k_scale) || window < 0 ||
+      window >= (1ll << 31) || !table_ok(table_stride, page_size) || !capacity_ok(capacity) ||
+      (path && !path_ok(max_path)))
+    return LORA_ERR_SHAPE;
+  if (!stride_ok(q_row_stride, static_cast<int64_t>(num_q_heads) * head_dim)) return LORA_ERR_SHAPE;
+  if (!aligned(weights, 4) || !aligned(q, 16) || q_row_stride % 8 || !aligned(lse, 4) ||
+      !aligned(cache, 16) || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
+      !aligned(page_table, 4) || !aligned(path, 4) || !aligned(path_len, 4) || !aligned(status, 4))
+    return LORA_ERR_ALIGN;
+  grg::Kv4WeightsArgs a;
+  a.weights = weights;
+  a.capacity = static_cast<int>(capacity);
+  a.q = q;
+  a.q_stride = q_row_stride;
+  a.lse = lse;
+  a.cache = cache;
+  a.num_pages = static_cast<int>(num_pages);
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = num_kv_heads;
+  a.page_size = page_size;
+  a.head_dim = head_dim;
+  a.score_scale = softmax_scale * k_scale;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.num_seqs = static_cast<int>(num_seqs);
+  a.max_num_tokens = static_cast<int>(max_num_tokens);
+  a.max_q_len = static_cast<int>(max_q_len);
+  a.window = static_cast<int>(window);
+  a.path = path;
+  a.path_len = path_len;
+  a.max_path = path ? static_cast<int>(max_path) : 0;
+  a.status = status;
+  return grg::launch_kv4_weights(a, f16, static_cast<cudaStream_t>(stream));
 }
 
 }  // namespace
@@ -248,12 +316,127 @@ size_t lora_kv4_attention_workspace_size(int64_t num_seqs, int64_t max_num_token
     return kv4_attention(q, q_row_stride, out, out_row_stride, lse, num_q_heads, cache,           \
                          num_pages, num_kv_heads, page_size, head_dim, k_scale, v_scale, q_start, \
                          kv_len, page_table, table_stride, num_seqs, max_num_tokens, max_q_len,   \
-                         softmax_scale, window, workspace, workspace_bytes, status, stream,       \
-                         half);                                                                   \
+                         softmax_scale, window, nullptr, 0, workspace, workspace_bytes, status,   \
+                         stream, half);                                                           \
   }
 GRG_ATTENTION(lora_kv4_attention, false)
 GRG_ATTENTION(lora_kv4_attention_f16, true)
 #undef GRG_ATTENTION
+
+#define GRG_TREE(name, half)                                                                      \
+  int name(const uint16_t* q, int64_t q_row_stride, uint16_t* out, int64_t out_row_stride,        \
+           float* lse, int num_q_heads, const uint8_t* cache, int64_t num_pages,                  \
+           int num_kv_heads, int page_size, int head_dim, float k_scale, float v_scale,           \
+           const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,              \
+           int64_t table_stride, int64_t num_seqs, int64_t max_num_tokens, int64_t max_q_len,     \
+           const uint32_t* tree_mask, int64_t mask_words, float softmax_scale, int64_t window,    \
+           void* workspace, size_t workspace_bytes, uint32_t* status, void* stream) {             \
+    if (!tree_mask) return LORA_ERR_NULL;                                                         \
+    if (mask_words < 1 || mask_words > LORA_MAX_NUM_TOKENS / 32 || 32 * mask_words < max_q_len)   \
+      return LORA_ERR_SHAPE;                                                                      \
+    return kv4_attention(q, q_row_stride, out, out_row_stride, lse, num_q_heads, cache,           \
+                         num_pages, num_kv_heads, page_size, head_dim, k_scale, v_scale, q_start, \
+                         kv_len, page_table, table_stride, num_seqs, max_num_tokens, max_q_len,   \
+                         softmax_scale, window, tree_mask, static_cast<int>(mask_words),          \
+                         workspace, workspace_bytes, status, stream, half);                       \
+  }
+GRG_TREE(lora_kv4_tree_attention, false)
+GRG_TREE(lora_kv4_tree_attention_f16, true)
+#undef GRG_TREE
+
+#define GRG_WEIGHTS(name, half)                                                                   \
+  int name(float* weights, int64_t capacity, const uint16_t* q, int64_t q_row_stride,             \
+           const float* lse, int num_q_heads, const uint8_t* cache, int64_t num_pages,            \
+           int num_kv_heads, int page_size, int head_dim, float k_scale, const int32_t* q_start,  \
+           const int32_t* kv_len, const int32_t* page_table, int64_t table_stride,                \
+           int64_t num_seqs, int64_t max_num_tokens, int64_t max_q_len, float softmax_scale,      \
+           int64_t window, const int32_t* path, const int32_t* path_len, int64_t max_path,        \
+           uint32_t* status, void* stream) {                                                      \
+    return kv4_key_weights(weights, capacity, q, q_row_stride, lse, num_q_heads, cache,           \
+                           num_pages, num_kv_heads, page_size, head_dim, k_scale, q_start,        \
+                           kv_len, page_table, table_stride, num_seqs, max_num_tokens, max_q_len, \
+                           softmax_scale, window, path, path_len, max_path, status, stream,       \
+                           half);                                                                 \
+  }
+GRG_WEIGHTS(lora_kv4_key_weights, false)
+GRG_WEIGHTS(lora_kv4_key_weights_f16, true)
+#undef GRG_WEIGHTS
+
+int lora_kv4_accept(uint8_t* cache, int64_t num_pages, int num_kv_heads, int page_size, int head_dim,
+                    const int32_t* q_start, const int32_t* kv_len, const int32_t* page_table,
+                    int64_t table_stride, int64_t num_seqs, const int32_t* path,
+                    const int32_t* path_len, int64_t max_path, int32_t* kv_len_out,
+                    uint32_t* status, void* stream) {
+  if (!cache || !q_start || !kv_len || !page_table || !path || !path_len || !kv_len_out)
+    return LORA_ERR_NULL;
+  if (!cache_ok(num_pages, num_kv_heads, page_size, head_dim) || !seqs_ok(num_seqs) ||
+      !table_ok(table_stride, page_size) || !path_ok(max_path) ||
+      overlap(kv_len, num_seqs, kv_len_out, num_seqs) ||
+      overlap(path_len, num_seqs, kv_len_out, num_seqs) ||
+      overlap(q_start, num_seqs + 1, kv_len_out, num_seqs))
+    return LORA_ERR_SHAPE;
+  if (!aligned(cache, 16) || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
+      !aligned(page_table, 4) || !aligned(path, 4) || !aligned(path_len, 4) ||
+      !aligned(kv_len_out, 4) || !aligned(status, 4))
+    return LORA_ERR_ALIGN;
+  grg::Kv4AcceptArgs a;
+  a.cache = cache;
+  a.num_pages = static_cast<int>(num_pages);
+  a.num_kv_heads = num_kv_heads;
+  a.page_size = page_size;
+  a.head_dim = head_dim;
+  a.q_start = q_start;
+  a.kv_len = kv_len;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.num_seqs = static_cast<int>(num_seqs);
+  a.path = path;
+  a.path_len = path_len;
+  a.max_path = static_cast<int>(max_path);
+  a.kv_len_out = kv_len_out;
+  a.status = status;
+  return grg::launch_kv4_accept(a, static_cast<cudaStream_t>(stream));
+}
+
+int lora_kv4_evict(uint8_t* cache, int64_t num_pages, int num_kv_heads, int page_size, int head_dim,
+                   float* weights, int32_t* key_pos, int64_t capacity, const int32_t* kv_len,
+                   const int32_t* last_pos, const int32_t* page_table, int64_t table_stride,
+                   int64_t num_seqs, int64_t budget, int64_t sink, int64_t recent,
+                   int32_t* kv_len_out, uint32_t* status, void* stream) {
+  if (!cache || !weights || !key_pos || !kv_len || !last_pos || !page_table || !kv_len_out)
+    return LORA_ERR_NULL;
+  if (!cache_ok(num_pages, num_kv_heads, page_size, head_dim) || !seqs_ok(num_seqs) ||
+      !table_ok(table_stride, page_size) || !capacity_ok(capacity) || budget < 1 ||
+      budget >= (1ll << 31) || sink < 0 || recent < 0 || sink > budget || recent > budget - sink ||
+      overlap(kv_len, num_seqs, kv_len_out, num_seqs) ||
+      overlap(last_pos, num_seqs, kv_len_out, num_seqs))
+    return LORA_ERR_SHAPE;
+  if (!aligned(cache, 16) || !aligned(weights, 4) || !aligned(key_pos, 4) || !aligned(kv_len, 4) ||
+      !aligned(last_pos, 4) || !aligned(page_table, 4) || !aligned(kv_len_out, 4) ||
+      !aligned(status, 4))
+    return LORA_ERR_ALIGN;
+  grg::Kv4EvictArgs a;
+  a.cache = cache;
+  a.num_pages = static_cast<int>(num_pages);
+  a.num_kv_heads = num_kv_heads;
+  a.page_size = page_size;
+  a.head_dim = head_dim;
+  a.weights = weights;
+  a.key_pos = key_pos;
+  a.capacity = static_cast<int>(capacity);
+  a.kv_len = kv_len;
+  a.last_pos = last_pos;
+  a.page_table = page_table;
+  a.table_stride = table_stride;
+  a.num_seqs = static_cast<int>(num_seqs);
+  a.budget = static_cast<int>(budget);
+  a.sink = static_cast<int>(sink);
+  a.recent = static_cast<int>(recent);
+  a.kv_len_out = kv_len_out;
+  a.status = status;
+  a.smem_keys = 0;
+  return grg::launch_kv4_evict(a, static_cast<cudaStream_t>(stream));
+}
 
 }  // extern "C"
 #pragma GCC visibility pop

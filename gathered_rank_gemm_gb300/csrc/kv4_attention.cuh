@@ -24,13 +24,67 @@ struct Kv4Seq {
     s.odd = a != s.q0 || e != s.q0 + s.rows || s.kv != k || s.take != s.rows;
     return s;
   }
-  // The position of row i, and the first key that it sees.
+  // The position of row i, and the first key that a row there sees.
   __device__ __forceinline__ int pos(int i) const { return kv - rows + i; }
   __device__ __forceinline__ int first_key(int i, int window) const {
     const int at = pos(i);  // (below 0 for a row without keys: at - window may not fit 32 bits)
     return window > 0 && at >= window ? at - window + 1 : 0;
   }
+
+  // Which keys rows see.  A row of a sequence sees a run of keys that ends at its own
+  // position; a row of a tree (TREE) those in front of all rows' own, from its window's
+  // first on, and of the rows' own what its mask names.
+  __device__ __forceinline__ int before() const { return kv - rows; }
+  // The last key of row i's run.
+  template <bool TREE>
+  __device__ __forceinline__ int run_last(int i) const {
+    return TREE ? before() - 1 : pos(i);
+  }
+  // The first.  A row of a tree stands as far behind the keys in front as it has ancestors.
+  template <bool TREE>
+  __device__ __forceinline__ int run_first(const Kv4AttnArgs& a, int i) const {
+    if constexpr (!TREE) return first_key(i, a.window);
+    if (a.window == 0) return 0;
+    const uint32_t* mask = a.tree_mask + static_cast<long long>(q0 + i) * a.tree_words;
+    int named = 0;
+    for (int w = 0; w < a.tree_words && 32 * w < rows; ++w)
+      named += __popc(mask[w] & (rows - 32 * w >= 32 ? ~0u : (1u << (rows - 32 * w)) - 1u));
+    return first_key(max(named - 1, 0), a.window);
+  }
+  // Bounds for the rows i0 .. i1: no row sees a key in front of keys_first or from keys_end
+  // on, and every row's run reaches from run_first_max to run_last(i0).
+  template <bool TREE>
+  __device__ __forceinline__ int keys_first(int i0, int window) const {
+    return first_key(TREE ? 0 : i0, window);
+  }
+  template <bool TREE>
+  __device__ __forceinline__ int keys_end(int i1) const {
+    return TREE ? kv : pos(i1) + 1;
+  }
+  template <bool TREE>
+  __device__ __forceinline__ int run_first_max(int i1, int window) const {
+    return first_key(TREE ? rows - 1 : i1, window);
+  }
 };
+
+// The lowest n bits (none below 0, all from 32 on), and all but those.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// Of 32 keys from key0 on, those that a row of a tree sees, as bits: the run [lo, before) and
+// what the row's mask names among the rows' own keys [before, kv).
+__device__ __forceinline__ uint32_t tree_sees(const Kv4AttnArgs& a, const Kv4Seq& s, long long row, int lo,
+                                              int key0) {
+  const int c0 = key0 - s.before();  // the first key among the rows' own, rounded down to a word
+  const int w0 = c0 >> 5;
+  uint32_t bits = low_bits(-c0) & ~low_bits(lo - key0);
+  if (c0 > -32) {
+    const uint32_t* mask = a.tree_mask + row * a.tree_words;
+    const uint32_t x = w0 >= 0 && w0 < a.tree_words ? __ldg(mask + w0) : 0u;
+    const uint32_t y = w0 + 1 < a.tree_words ? __ldg(mask + w0 + 1) : 0u;  // (w0 + 1 >= 0)
+    bits |= __funnelshift_r(x, y, c0 & 31) & ~low_bits(-c0);
+  }
+  return bits & low_bits(s.kv - key0);
+}
 
 // a / b of values that are rarely past 32 bits (a >= 0, b > 0); a 64-bit division takes
 // some hundred cycles on every call's way.

@@ -86,11 +86,83 @@ struct Kv4AttnArgs {
   int max_num_tokens;
   int max_q_len;
   int window;  // 0: none
+  const uint32_t* tree_mask;  // [max_num_tokens][tree_words], null for causal rows
+  int tree_words;
   void* workspace;
   uint32_t* status;
 };
 size_t kv4_attention_workspace(long long num_seqs, long long max_num_tokens, long long max_q_len,
                                int num_q_heads, int num_kv_heads, int head_dim);
 int launch_kv4_attention(const Kv4AttnArgs& a, bool f16, cudaStream_t stream);
+
+struct Kv4AcceptArgs {
+  uint8_t* cache;
+  int num_pages;
+  int num_kv_heads;
+  int page_size;
+  int head_dim;
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  long long table_stride;
+  int num_seqs;
+  const int32_t* path;  // [num_seqs][max_path]
+  const int32_t* path_len;
+  int max_path;
+  int32_t* kv_len_out;
+  uint32_t* status;
+};
+int launch_kv4_accept(const Kv4AcceptArgs& a, cudaStream_t stream);
+
+struct Kv4WeightsArgs {
+  float* weights;  // [num_seqs][num_kv_heads][capacity]
+  int capacity;
+  const uint16_t* q;
+  long long q_stride;
+  const float* lse;  // [max_num_tokens][num_q_heads]
+  const uint8_t* cache;
+  int num_pages;
+  int num_q_heads;
+  int num_kv_heads;
+  int page_size;
+  int head_dim;
+  float score_scale;  // softmax_scale * k_scale
+  const int32_t* q_start;
+  const int32_t* kv_len;
+  const int32_t* page_table;
+  long long table_stride;
+  int num_seqs;
+  int max_num_tokens;
+  int max_q_len;
+  int window;           // 0: none
+  const int32_t* path;  // [num_seqs][max_path], null: a sequence's rows are all of its own
+  const int32_t* path_len;
+  int max_path;
+  uint32_t* status;
+};
+int launch_kv4_weights(const Kv4WeightsArgs& a, bool f16, cudaStream_t stream);
+
+struct Kv4EvictArgs {
+  uint8_t* cache;
+  int num_pages;
+  int num_kv_heads;
+  int page_size;
+  int head_dim;
+  float* weights;    // [num_seqs][num_kv_heads][capacity]
+  int32_t* key_pos;  // the same
+  int capacity;
+  const int32_t* kv_len;
+  const int32_t* last_pos;
+  const int32_t* page_table;
+  long long table_stride;
+  int num_seqs;
+  int budget;
+  int sink;
+  int recent;
+  int32_t* kv_len_out;
+  uint32_t* status;
+  int smem_keys;  // the launcher's: keys whose integers are kept in shared memory
+};
+int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream);
 
 }  // namespace grg

@@ -52,7 +52,8 @@ int64_t whole(PyObject* o, const char* name) {
   return v;
 }
 
-// The call's 16-bit type and device, taken from its main operand.
+// The call's 16-bit type and device, taken from its main operand (of a call without 16-bit
+// data, the cache).
 struct Like {
   at::ScalarType type;
   c10::Device device;
@@ -61,6 +62,9 @@ struct Like {
     if (!t.is_cuda()) refuse(name, "must be a CUDA tensor (there is no CPU path)");
     if (type != at::kBFloat16 && type != at::kHalf) refuse(name, "must be bfloat16 or float16");
     f16 = type == at::kHalf;
+  }
+  explicit Like(const at::Tensor& cache) : type(at::kByte), device(cache.device()), f16(false) {
+    if (!cache.is_cuda()) refuse("cache", "must be a CUDA tensor (there is no CPU path)");
   }
 };
 
@@ -110,6 +114,19 @@ struct Cache {
     pages = t.size(0), heads = t.size(1), page_size = 16 * t.size(2), dim = t.size(3) / 18;
     if (heads > INT32_MAX || page_size > INT32_MAX || dim > INT32_MAX)
       refuse("cache", "has a size out of range");
+  }
+};
+// The sequences' rows, keys and pages.
+struct Sequences {
+  int32_t *start, *kv, *table;
+  int64_t count, wide;
+  Sequences(PyObject* q_start, PyObject* kv_len, PyObject* page_table, const Like& like) {
+    const at::Tensor& t = required(page_table, "page_table");
+    if (t.dim() != 2) refuse("page_table", "must be [sequences][pages]");
+    count = t.size(0), wide = t.size(1);
+    start = vec<int32_t>(required(q_start, "q_start"), "q_start", like, at::kInt, {count + 1});
+    kv = vec<int32_t>(required(kv_len, "kv_len"), "kv_len", like, at::kInt, {count});
+    table = vec<int32_t>(t, "page_table", like, at::kInt, {count, wide});
   }
 };
 bool truth(PyObject* o, const char* name) {
@@ -235,8 +252,9 @@ PyObject* kv4_append(PyObject*, Args a, Py_ssize_t n) {
   });
 }
 
-PyObject* kv4_attention(PyObject*, Args a, Py_ssize_t n) {
-  return guarded(n, 15, [&] {
+// The attention of causal rows (15 arguments), and that of trees (16: a mask behind max_q_len).
+PyObject* attention(Args a, Py_ssize_t n, bool tree) {
+  return guarded(n, tree ? 16 : 15, [&] {
     const at::Tensor& q = required(a[1], "q");
     const Like like(q, "q");
     if (q.dim() != 3) refuse("q", "must be [rows][heads][head_dim]");
@@ -246,13 +264,17 @@ PyObject* kv4_attention(PyObject*, Args a, Py_ssize_t n) {
     int64_t qs, os;
     auto* qp = rows<uint16_t>(q, "q", like, like.type, shape, qs);
     auto* op = rows<uint16_t>(required(a[2], "out"), "out", like, like.type, shape, os);
-    const at::Tensor& table = required(a[5], "page_table");
-    if (table.dim() != 2) refuse("page_table", "must be [sequences][pages]");
-    const int64_t seqs = table.size(0), wide = table.size(1);
-    auto* start = vec<int32_t>(required(a[3], "q_start"), "q_start", like, at::kInt, {seqs + 1});
-    auto* kv = vec<int32_t>(required(a[4], "kv_len"), "kv_len", like, at::kInt, {seqs});
-    auto* tp = vec<int32_t>(table, "page_table", like, at::kInt, {seqs, wide});
+    const Sequences s(a[3], a[4], a[5], like);
     const int64_t max_q = whole(a[6], "max_q_len");
+    int64_t words = 0;
+    uint32_t* mask = nullptr;
+    if (tree) {
+      const at::Tensor& t = required(a[7], "tree_mask");
+      if (t.dim() != 2) refuse("tree_mask", "must be [rows][words]");
+      words = t.size(1);
+      mask = vec<uint32_t>(t, "tree_mask", like, at::kInt, {count, words});
+      ++a;
+    }
     const float scale = static_cast<float>(number(a[7], "softmax_scale"));
     const at::Tensor& ws = required(a[8], "workspace");
     on(ws, "workspace", like);
@@ -264,11 +286,112 @@ PyObject* kv4_attention(PyObject*, Args a, Py_ssize_t n) {
     float* lp = lse ? vec<float>(*lse, "lse", like, at::kFloat, {count, qh}) : nullptr;
     uint32_t* st = status_word(a[13], like);
     const c10::cuda::CUDAGuard guard(like.device);
+    const int heads = static_cast<int>(std::min<int64_t>(qh, INT32_MAX));
+    const int kvh = static_cast<int>(c.heads), page = static_cast<int>(c.page_size), dim = static_cast<int>(c.dim);
+    const size_t bytes = static_cast<size_t>(ws.numel() * ws.element_size());
+    void* stream = stream_of(a[14], like.device);
+    if (tree)
+      return (like.f16 ? lora_kv4_tree_attention_f16 : lora_kv4_tree_attention)(
+          qp, qs, op, os, lp, heads, c.ptr, c.pages, kvh, page, dim, k_scale, v_scale, s.start, s.kv,
+          s.table, s.wide, s.count, count, max_q, mask, words, scale, window, ws.data_ptr(), bytes, st,
+          stream);
     return (like.f16 ? lora_kv4_attention_f16 : lora_kv4_attention)(
-        qp, qs, op, os, lp, static_cast<int>(std::min<int64_t>(qh, INT32_MAX)), c.ptr, c.pages,
+        qp, qs, op, os, lp, heads, c.ptr, c.pages, kvh, page, dim, k_scale, v_scale, s.start, s.kv,
+        s.table, s.wide, s.count, count, max_q, scale, window, ws.data_ptr(), bytes, st, stream);
+  });
+}
+PyObject* kv4_attention(PyObject*, Args a, Py_ssize_t n) { return attention(a, n, false); }
+PyObject* kv4_tree_attention(PyObject*, Args a, Py_ssize_t n) { return attention(a, n, true); }
+
+// Accepted paths of the sequences' trees.
+struct Paths {
+  int32_t *path, *len;
+  int64_t longest;
+  Paths(const at::Tensor& t, const at::Tensor& l, int64_t seqs, const Like& like) {
+    if (t.dim() != 2) refuse("path", "must be [sequences][longest path]");
+    longest = t.size(1);
+    path = vec<int32_t>(t, "path", like, at::kInt, {seqs, longest});
+    len = vec<int32_t>(l, "path_len", like, at::kInt, {seqs});
+  }
+};
+
+PyObject* kv4_accept(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 9, [&] {
+    const at::Tensor& cache = required(a[0], "cache");
+    const Like like(cache);
+    const Cache c(cache, like);
+    const Sequences s(a[1], a[2], a[3], like);
+    const Paths p(required(a[4], "path"), required(a[5], "path_len"), s.count, like);
+    auto* out = vec<int32_t>(required(a[6], "kv_len_out"), "kv_len_out", like, at::kInt, {s.count});
+    uint32_t* st = status_word(a[7], like);
+    const c10::cuda::CUDAGuard guard(like.device);
+    return lora_kv4_accept(c.ptr, c.pages, static_cast<int>(c.heads), static_cast<int>(c.page_size),
+                           static_cast<int>(c.dim), s.start, s.kv, s.table, s.wide, s.count, p.path,
+                           p.len, p.longest, out, st, stream_of(a[8], like.device));
+  });
+}
+
+PyObject* kv4_key_weights(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 15, [&] {
+    const at::Tensor& q = required(a[2], "q");
+    const Like like(q, "q");
+    if (q.dim() != 3) refuse("q", "must be [rows][heads][head_dim]");
+    const Cache c(required(a[1], "cache"), like);
+    const int64_t count = q.size(0), qh = q.size(1);
+    int64_t qs;
+    auto* qp = rows<uint16_t>(q, "q", like, like.type, {count, qh, c.dim}, qs);
+    auto* lp = vec<float>(required(a[3], "lse"), "lse", like, at::kFloat, {count, qh});
+    const Sequences s(a[4], a[5], a[6], like);
+    const at::Tensor& w = required(a[0], "weights");
+    if (w.dim() != 3) refuse("weights", "must be [sequences][kv heads][capacity]");
+    const int64_t capacity = w.size(2);
+    auto* wp = vec<float>(w, "weights", like, at::kFloat, {s.count, c.heads, capacity});
+    const int64_t max_q = whole(a[7], "max_q_len");
+    const float scale = static_cast<float>(number(a[8], "softmax_scale"));
+    const int64_t window = whole(a[9], "window");
+    const float k_scale = static_cast<float>(number(a[10], "k_scale"));
+    const at::Tensor *path = optional(a[11], "path"), *len = optional(a[12], "path_len");
+    if (!path != !len) refuse("path", "must come with path_len");
+    int32_t *pp = nullptr, *np = nullptr;
+    int64_t longest = 0;
+    if (path) {
+      const Paths p(*path, *len, s.count, like);
+      pp = p.path, np = p.len, longest = p.longest;
+    }
+    uint32_t* st = status_word(a[13], like);
+    const c10::cuda::CUDAGuard guard(like.device);
+    return (like.f16 ? lora_kv4_key_weights_f16 : lora_kv4_key_weights)(
+        wp, capacity, qp, qs, lp, static_cast<int>(std::min<int64_t>(qh, INT32_MAX)), c.ptr, c.pages,
         static_cast<int>(c.heads), static_cast<int>(c.page_size), static_cast<int>(c.dim), k_scale,
-        v_scale, start, kv, tp, wide, seqs, count, max_q, scale, window, ws.data_ptr(),
-        static_cast<size_t>(ws.numel() * ws.element_size()), st, stream_of(a[14], like.device));
+        s.start, s.kv, s.table, s.wide, s.count, count, max_q, scale, window, pp, np, longest, st,
+        stream_of(a[14], like.device));
+  });
+}
+
+PyObject* kv4_evict(PyObject*, Args a, Py_ssize_t n) {
+  return guarded(n, 12, [&] {
+    const at::Tensor& cache = required(a[0], "cache");
+    const Like like(cache);
+    const Cache c(cache, like);
+    const at::Tensor& table = required(a[5], "page_table");
+    if (table.dim() != 2) refuse("page_table", "must be [sequences][pages]");
+    const int64_t seqs = table.size(0), wide = table.size(1);
+    auto* tp = vec<int32_t>(table, "page_table", like, at::kInt, {seqs, wide});
+    const at::Tensor& w = required(a[1], "weights");
+    if (w.dim() != 3) refuse("weights", "must be [sequences][kv heads][capacity]");
+    const int64_t capacity = w.size(2);
+    auto* wp = vec<float>(w, "weights", like, at::kFloat, {seqs, c.heads, capacity});
+    auto* pp = vec<int32_t>(required(a[2], "key_pos"), "key_pos", like, at::kInt, {seqs, c.heads, capacity});
+    auto* kp = vec<int32_t>(required(a[3], "kv_len"), "kv_len", like, at::kInt, {seqs});
+    auto* lp = vec<int32_t>(required(a[4], "last_pos"), "last_pos", like, at::kInt, {seqs});
+    const int64_t budget = whole(a[6], "budget");
+    auto* out = vec<int32_t>(required(a[7], "kv_len_out"), "kv_len_out", like, at::kInt, {seqs});
+    const int64_t sink = whole(a[8], "sink"), recent = whole(a[9], "recent");
+    uint32_t* st = status_word(a[10], like);
+    const c10::cuda::CUDAGuard guard(like.device);
+    return lora_kv4_evict(c.ptr, c.pages, static_cast<int>(c.heads), static_cast<int>(c.page_size),
+                          static_cast<int>(c.dim), wp, pp, capacity, kp, lp, tp, wide, seqs, budget,
+                          sink, recent, out, st, stream_of(a[11], like.device));
   });
 }
 
@@ -278,6 +401,14 @@ PyMethodDef kMethods[] = {
     {"kv4_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv4_append)),
      METH_FASTCALL, nullptr},
     {"kv4_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv4_attention)),
+     METH_FASTCALL, nullptr},
+    {"kv4_tree_attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv4_tree_attention)),
+     METH_FASTCALL, nullptr},
+    {"kv4_accept", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv4_accept)),
+     METH_FASTCALL, nullptr},
+    {"kv4_key_weights", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv4_key_weights)),
+     METH_FASTCALL, nullptr},
+    {"kv4_evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(kv4_evict)),
      METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, kMethods,

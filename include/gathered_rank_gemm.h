@@ -605,6 +605,141 @@ int lora_kv4_attention_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *ou
                            int64_t window, void *workspace, size_t workspace_bytes,
                            uint32_t *status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Drafted trees and bounded memory, over the same cache.  A step that verifies
+ * drafted trees runs, behind the append of the drafted tokens: the attention of
+ * the trees, lora_kv4_accept for the paths that the verification accepts,
+ * and where the cache is bounded lora_kv4_key_weights and lora_kv4_evict.
+ */
+
+/*
+ * lora_kv4_attention for the rows of drafted trees.  A sequence's m rows are the
+ * drafted tokens, in any order, its last m keys theirs.  Row i sees
+ *   the keys j < kv_len[b] - m in front of them (and j > p - window where window > 0,
+ *     p = kv_len[b] - m + max(named - 1, 0) with the number of rows that its mask names), and
+ *   key kv_len[b] - m + c where bit c of its mask is set: bit c % 32 of word c / 32, c < m.
+ * A mask names a row's ancestors and the row itself, so that p is the row's position; nothing
+ * else is assumed of it, and a row that sees no key gets 0 and lse = -inf.
+ *
+ *   tree_mask     device uint32[max_num_tokens][mask_words], 4-byte aligned; bits from m on
+ *                 count for nothing
+ *   mask_words    words of a row, 32 * mask_words >= max_q_len
+ * All else, the workspace included, as in lora_kv4_attention.
+ */
+int lora_kv4_tree_attention(const uint16_t *q, int64_t q_row_stride, uint16_t *out,
+                            int64_t out_row_stride, float *lse, int num_q_heads,
+                            const uint8_t *cache, int64_t num_pages, int num_kv_heads,
+                            int page_size, int head_dim, float k_scale, float v_scale,
+                            const int32_t *q_start, const int32_t *kv_len,
+                            const int32_t *page_table, int64_t table_stride, int64_t num_seqs,
+                            int64_t max_num_tokens, int64_t max_q_len, const uint32_t *tree_mask,
+                            int64_t mask_words, float softmax_scale, int64_t window,
+                            void *workspace, size_t workspace_bytes, uint32_t *status,
+                            void *stream);
+int lora_kv4_tree_attention_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *out,
+                                int64_t out_row_stride, float *lse, int num_q_heads,
+                                const uint8_t *cache, int64_t num_pages, int num_kv_heads,
+                                int page_size, int head_dim, float k_scale, float v_scale,
+                                const int32_t *q_start, const int32_t *kv_len,
+                                const int32_t *page_table, int64_t table_stride,
+                                int64_t num_seqs, int64_t max_num_tokens, int64_t max_q_len,
+                                const uint32_t *tree_mask, int64_t mask_words,
+                                float softmax_scale, int64_t window, void *workspace,
+                                size_t workspace_bytes, uint32_t *status, void *stream);
+
+#define LORA_KV4_MAX_PATH 512
+
+/*
+ * The accepted path of each sequence's tree: with n = kv_len[b] and m rows (q_start),
+ *   key n - m + i  <-  key n - m + path[b][i]   for i < path_len[b], in every head,
+ *   kv_len_out[b]   =  n - m + path_len[b].
+ * Every key is read before any of its sequence is written, so a path may name rows in any
+ * order and more than once.  Keys behind the path keep what they hold.
+ *
+ *   path          device int32[num_seqs][max_path], max_path up to LORA_KV4_MAX_PATH
+ *   path_len      device int32[num_seqs]
+ *   kv_len_out    device int32[num_seqs], apart from the other arrays
+ * The pages of a sequence's last m keys hold no other sequence's.  Data that does not fit: lengths
+ * are clamped (kv_len to the table, m to kv_len, path_len to m and max_path) and a path's row
+ * outside [0, m) is not moved (LORA_STATUS_BAD_LENGTH); nothing is moved from or to a page
+ * outside the cache (LORA_STATUS_BAD_SLOT).
+ */
+int lora_kv4_accept(uint8_t *cache, int64_t num_pages, int num_kv_heads, int page_size,
+                    int head_dim, const int32_t *q_start, const int32_t *kv_len,
+                    const int32_t *page_table, int64_t table_stride, int64_t num_seqs,
+                    const int32_t *path, const int32_t *path_len, int64_t max_path,
+                    int32_t *kv_len_out, uint32_t *status, void *stream);
+
+#define LORA_KV4_MAX_KEYS ((1ll << 31) - 4096)
+
+/*
+ * The weight that each key has drawn: for every key head h and every key j of sequence b that
+ * is one of its m rows' own (j >= kv_len[b] - m) or is seen by one of them,
+ *   weights[b][h][j] = (j < kv_len[b] - m ? weights[b][h][j] : 0)
+ *                      + sum over rows i that see j, heads g of h of exp(x_ijg - lse[t][g])
+ * with x and the rows' sight as in lora_kv4_attention (causal, window), q and lse those of
+ * that call.  The rows' own keys are new: their weight begins at 0, so weights needs no clearing.
+ * With a path, the m rows are the tree's rows path[b][0 .. path_len[b]) in their order (q and lse
+ * at q_start[b] + path[b][i]), and kv_len is that after lora_kv4_accept; without one, they are
+ * all rows of the sequence.
+ *
+ *   weights       fp32[num_seqs][num_kv_heads][capacity], in and out
+ *   lse           fp32[max_num_tokens][num_q_heads]; -inf: the row adds nothing
+ *   path, path_len  NULL, or int32[num_seqs][max_path] and int32[num_seqs]
+ * Sums are fp32, in the rows' order for every key whatever else is in the batch; products as
+ * in lora_kv4_attention.  A NaN in a row's q or lse makes the weights that it adds to NaN,
+ * one in a key that key's.  Data that does not fit: as in lora_kv4_attention; keys from capacity
+ * on have no weight, rows beyond max_q_len add nothing, nor does a path's row outside the
+ * sequence's rows (LORA_STATUS_BAD_LENGTH).  A key whose page is outside the cache draws no
+ * weight (LORA_STATUS_BAD_SLOT).
+ */
+int lora_kv4_key_weights(float *weights, int64_t capacity, const uint16_t *q,
+                         int64_t q_row_stride, const float *lse, int num_q_heads,
+                         const uint8_t *cache, int64_t num_pages, int num_kv_heads, int page_size,
+                         int head_dim, float k_scale, const int32_t *q_start,
+                         const int32_t *kv_len, const int32_t *page_table, int64_t table_stride,
+                         int64_t num_seqs, int64_t max_num_tokens, int64_t max_q_len,
+                         float softmax_scale, int64_t window, const int32_t *path,
+                         const int32_t *path_len, int64_t max_path, uint32_t *status,
+                         void *stream);
+int lora_kv4_key_weights_f16(float *weights, int64_t capacity, const uint16_t *q,
+                             int64_t q_row_stride, const float *lse, int num_q_heads,
+                             const uint8_t *cache, int64_t num_pages, int num_kv_heads,
+                             int page_size, int head_dim, float k_scale, const int32_t *q_start,
+                             const int32_t *kv_len, const int32_t *page_table,
+                             int64_t table_stride, int64_t num_seqs, int64_t max_num_tokens,
+                             int64_t max_q_len, float softmax_scale, int64_t window,
+                             const int32_t *path, const int32_t *path_len, int64_t max_path,
+                             uint32_t *status, void *stream);
+
+/*
+ * Eviction by accumulated weight: a sequence of n = kv_len[b] > budget keys keeps budget of them in
+ * each key head, each head its own.  key_pos[b][h][j] is the position of the token that key j
+ * stands for, below 0 for a key that was appended since the last call; those become
+ * last_pos[b] - (n - 1 - j).  The kept keys are first the protected ones, whose position is
+ * below sink or above last_pos[b] - recent, then those of the largest weight (NaN below all
+ * numbers); ties go to the lowest index.  The i-th kept key j >= budget, in the order of the indices,
+ * takes the place of the i-th key j < budget that is not kept, with its weight and position;
+ * the others stay where they are.  So keys of a head are in no order afterwards: attention
+ * over them is called without a window.  key_pos of [budget, n) becomes -1.
+ *   kv_len_out[b] = min(n, budget)
+ * A sequence within its budget keeps everything; its new keys get their positions.
+ *
+ *   weights       fp32[num_seqs][num_kv_heads][capacity], in and out (lora_kv4_key_weights)
+ *   key_pos       int32, the same; filled with -1 where a sequence begins
+ *   last_pos      device int32[num_seqs]: the position of the last key's token
+ *   budget        at least 1; sink + recent <= budget, both at least 0
+ *   kv_len_out    device int32[num_seqs], apart from kv_len and last_pos
+ * A sequence's pages hold no other sequence's.  Data that does not fit: kv_len is clamped to
+ * the table and the capacity (LORA_STATUS_BAD_LENGTH); keys are not moved from or to a page
+ * outside the cache (LORA_STATUS_BAD_SLOT), though their weights and positions are.
+ */
+int lora_kv4_evict(uint8_t *cache, int64_t num_pages, int num_kv_heads, int page_size,
+                   int head_dim, float *weights, int32_t *key_pos, int64_t capacity,
+                   const int32_t *kv_len, const int32_t *last_pos, const int32_t *page_table,
+                   int64_t table_stride, int64_t num_seqs, int64_t budget, int64_t sink,
+                   int64_t recent, int32_t *kv_len_out, uint32_t *status, void *stream);
+
 /* Static text for a LORA_OK / LORA_ERR_* code. */
 const char *lora_error_string(int code);
 

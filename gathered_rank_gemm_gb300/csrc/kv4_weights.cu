@@ -20,6 +20,7 @@ constexpr float kWtsLog2e = 1.4426950408889634f;
 
 struct WtsParams {
   Kv4WeightsArgs a;
+  int max_packed_rows;  // sequences with more packed rows are not this kernel's
 };
 __device__ __forceinline__ uint32_t wts_hmul2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -47,6 +48,9 @@ __global__ void __launch_bounds__(kWtsThreads, 2)
   pdl_launch_dependents();
 
   // ---- the line of blocks
+  auto blocks_of = [&](const WeightSeq& s) {
+    return static_cast<long long>(s.take) * group > p.max_packed_rows ? 0 : s.blocks(a.window);
+  };
   const int per_thread = (a.num_seqs + kWtsThreads - 1) / kWtsThreads;
   long long mine = 0;
   for (int i = 0; i < per_thread; ++i) {
@@ -54,7 +58,7 @@ __global__ void __launch_bounds__(kWtsThreads, 2)
     if (b < a.num_seqs) {
       const WeightSeq s = WeightSeq::of(a, b);
       if (s.odd && blockIdx.x == 0 && a.status) atomicOr(a.status, kStatusBadLength);
-      mine += static_cast<long long>(s.blocks(a.window)) * a.num_kv_heads;
+      mine += static_cast<long long>(blocks_of(s)) * a.num_kv_heads;
     }
   }
   long long run = mine;
@@ -87,7 +91,7 @@ __global__ void __launch_bounds__(kWtsThreads, 2)
     long long off = u0 - s_prefix[lo];
     for (b = lo * per_thread;; ++b) {
       seq = WeightSeq::of(a, b);
-      nb = seq.blocks(a.window);
+      nb = blocks_of(seq);
       const long long n = static_cast<long long>(nb) * a.num_kv_heads;
       if (off < n) break;
       off -= n;
@@ -261,7 +265,7 @@ __global__ void __launch_bounds__(kWtsThreads, 2)
       h = 0;
       do {
         seq = WeightSeq::of(a, ++b);
-        nb = seq.blocks(a.window);
+        nb = blocks_of(seq);
       } while (nb == 0);
     }
   }
@@ -283,13 +287,19 @@ int run_weights(const WtsParams& q, bool wide, cudaStream_t stream) {
 }
 }  // namespace
 
+// Sequences of up to kFewRows packed rows go by mma.sync, the others by tcgen05; a batch whose
+// bound allows no long sequence does not launch the latter.
+constexpr int kFewRows = 32;
+
 int launch_kv4_weights(const Kv4WeightsArgs& a, bool f16, cudaStream_t stream) {
-  const int group = a.num_q_heads / a.num_kv_heads;
-  const bool wide = static_cast<long long>(a.max_q_len) * group > 8;
+  const long long packed = static_cast<long long>(a.max_q_len) * (a.num_q_heads / a.num_kv_heads);
+  const bool wide = packed > 8;
   WtsParams p;
   p.a = a;
-  if (a.head_dim == 64) return f16 ? run_weights<64, true>(p, wide, stream) : run_weights<64, false>(p, wide, stream);
-  return f16 ? run_weights<128, true>(p, wide, stream) : run_weights<128, false>(p, wide, stream);
+  p.max_packed_rows = kFewRows;
+  const int rc = a.head_dim == 64 ? (f16 ? run_weights<64, true>(p, wide, stream) : run_weights<64, false>(p, wide, stream))
+                                  : (f16 ? run_weights<128, true>(p, wide, stream) : run_weights<128, false>(p, wide, stream));
+  return rc == 0 && packed > kFewRows ? launch_kv4_weights_tc(a, kFewRows, f16, stream) : rc;
 }
 
 }  // namespace grg

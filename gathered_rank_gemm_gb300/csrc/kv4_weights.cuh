@@ -51,4 +51,7 @@ struct WeightSeq {
   }
 };
 
+// Sequences with more than max_packed_rows rows x heads of a key head (kv4_weights_tc.cu).
+int launch_kv4_weights_tc(const Kv4WeightsArgs& a, int max_packed_rows, bool f16, cudaStream_t stream);
+
 }  // namespace grg

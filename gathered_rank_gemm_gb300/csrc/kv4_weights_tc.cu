@@ -10,32 +10,47 @@
 // most six significant bits, which bf16 holds too, so that q is copied as it is and c is
 // the same for all rows.
 //
-// Warp roles (16 warps of 128 registers, one CTA per SM, persistent):
+// Warp roles (20 warps of 96 registers, one CTA per SM, persistent):
 //  - warps 0-3 and 4-7: the sums of tile 0 and 1; a thread owns a key
-//  - warps 8-11: widen K into swizzled operand tiles, an item ahead of the products
-//  - warps 12-14: copy the rows of q and their logarithms, two row tiles deep
-//  - warp 15: issues the products; S is double-buffered in TMEM
-// Work: items by the number of their row tiles, most first, dealt out to the CTAs to and fro;
-// where they are too many to sort (over kTcPairs pairs of sequence and keys) in their own order.
+//  - warps 8-15: widen K into swizzled operand tiles, an item ahead of the products; a thread
+//    has a key, its codes asked for an item ahead, its page two
+//  - warp 16: issues the products; S is double-buffered in TMEM
+//  - warps 17-19: the rows' logarithms, and the rows of q, two tiles deep: by TMA, or, where a path
+//    picks them, by copies of 16 bytes
+// Work: few items a CTA (up to kTcDeal) are dealt out in rounds, those of most row tiles first, each
+// round to the CTAs with the least so far; many stay in their own order and are cut into equal runs.
+#include <algorithm>
+
 #include "kv4_weights.cuh"
 #include "launch.h"
 
 namespace grg {
 
 namespace {
-constexpr int kTcThreads = 512, kTcWarps = kTcThreads / 32;
-constexpr int kTcRowThreads = 96;  // that copy rows
+constexpr int kTcWarps = 20, kTcThreads = kTcWarps * 32;
+constexpr int kTcCopiers = 96;  // threads that copy rows
+constexpr int kTcLine = 512;    // threads that sum up the sequences
+constexpr int kTcCtasMax = 160;
+constexpr int kTcFixed = 2;     // what an item costs besides its row tiles, in row tiles
 constexpr int kTcKeys = 256;   // keys of an item
-constexpr int kTcRows = 128;   // packed rows of a tile
-constexpr int kTcPairs = 512;  // (sequence, keys) pairs that are sorted
+constexpr int kTcRows = 128;   // packed rows of a tile, at most: whole rows where 128 heads hold one
+constexpr int kTcPairs = 512;  // (sequence, key tile) pairs that can be sorted
+constexpr int kTcDeal = 16;    // items a CTA up to which they are
 constexpr int kTcAhead = 4;    // row tiles' logarithms kept
 constexpr float kTcLog2e = 1.4426950408889634f;
 
 struct TcParams {
   Kv4WeightsArgs a;
   int max_packed_rows;  // sequences with no more packed rows are not this kernel's
+  int tile_rows;        // packed rows of a tile
+  int by_tma;           // q's rows come by TMA
   unsigned long long wait_limit_ns;
   int wait_fault;
+};
+
+struct TcParamsTma {
+  CUtensorMap q;  // [rows][heads][D], boxes of 64 columns of the heads of a tile's rows
+  TcParams p;
 };
 
 struct TcShared {
@@ -45,14 +60,16 @@ struct TcShared {
   uint64_t s_full[2], s_empty[2];  // by row tile
   uint64_t drain;
   __align__(16) float neg[kTcAhead][kTcRows];  // -lse log2 e of a tile's rows, -infinity: adds nothing
-  int odd[kTcAhead];                           // a row that exists adds nothing
+  __align__(16) uint32_t adds[kTcAhead][4];    // its rows that do (and what lies behind the last)
   uint32_t taddr;
   int abort;
-  int warp_sum[kTcWarps];
-  long long warp_long[kTcWarps];
-  long long prefix[kTcThreads + 1];  // pairs before a thread's sequences
-  int pair_b[kTcPairs], pair_kt[kTcPairs], pair_tiles[kTcPairs];
+  long long warp_sum[kTcLine / 32];
+  long long prefix[kTcLine];  // pairs before a thread's sequences
+  struct Pair {
+    int b, kt, row0, rows, q0, q_rows, seq_rows, kv, end;
+  } pair[kTcPairs];
   int sorted[kTcPairs];
+  int load[kTcCtasMax], dealt[kTcDeal];  // row tiles of each CTA so far; this one's items
 };
 
 // An item: its keys [256 kt, ...) and the packed rows [row0, row0 + rows) that see one of them.
@@ -60,7 +77,7 @@ struct TcItem {
   int b, h, kt;
   WeightSeq seq;
   int row0, rows;
-  __device__ __forceinline__ int tiles() const { return (rows + kTcRows - 1) / kTcRows; }
+  __device__ __forceinline__ int tiles(int tile_rows) const { return (rows + tile_rows - 1) / tile_rows; }
 };
 __device__ __forceinline__ bool tc_mine(const WeightSeq& s, int group, int max_packed_rows) {
   return s.rows > 0 && static_cast<long long>(s.take) * group > max_packed_rows;
@@ -89,27 +106,22 @@ __device__ __forceinline__ bool tc_elect() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
   return r != 0;
 }
-// 32 consecutive 32-bit columns of this thread's TMEM lane: the load, and the wait for every
+// 16 consecutive 32-bit columns of this thread's TMEM lane: the load, and the wait for every
 // load so far (the registers hold nothing before it).
-__device__ __forceinline__ void tc_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+__device__ __forceinline__ void tc_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];\n"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tc_ld32_wait(uint32_t (&r)[32]) {
+__device__ __forceinline__ void tc_ld16_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
-                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 // (s0, s1) * (c, c) + (n0, n1), and a sum, two fp32 at a time.
 __device__ __forceinline__ void tc_fma2(float& x, float& y, uint32_t s0, uint32_t s1, float c, float n0,
@@ -129,7 +141,8 @@ __device__ __forceinline__ void tc_add2(float& x, float& y, float a, float b) {
 
 template <int D, bool F16>
 __global__ void __launch_bounds__(kTcThreads, 1)
-    lora_kv4_weights_tc_kernel(const __grid_constant__ TcParams p) {
+    lora_kv4_weights_tc_kernel(const __grid_constant__ TcParamsTma params) {
+  const TcParams& p = params.p;
   using B = Kv4Block<D>;
   constexpr int ATOMS = D / 64;                        // 128-byte atoms of a row
   constexpr uint32_t kAtom = 128 * 128;                // 128 rows of one
@@ -151,9 +164,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(sh.q_full[i]), kTcRowThreads + (p.wait_fault ? 1 : 0));
+      mbar_init(bar(sh.q_full[i]), (p.by_tma ? 1 : kTcCopiers) + (p.wait_fault ? 1 : 0));
       mbar_init(bar(sh.q_empty[i]), 1);
-      mbar_init(bar(sh.k_full[i]), 4);
+      mbar_init(bar(sh.k_full[i]), 8);
       mbar_init(bar(sh.k_empty[i]), 1);
       mbar_init(bar(sh.s_full[i]), 1);
       mbar_init(bar(sh.s_empty[i]), 8);
@@ -163,7 +176,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     fence_mbar_init();
     sh.abort = 0;
   }
-  if (warp == 15) {
+  if (warp == 16) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(
                      smem_u32(&sh.taddr)),
                  "r"(512u)
@@ -171,13 +184,20 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
   }
   const CtaAbort cta_abort{&sh.abort, p.wait_limit_ns};
+  const int R = p.tile_rows;
+  // what TMA never writes behind a tile's last row is read by the products all the same
+  for (int i = tid; i < 2 * ATOMS * (kTcRows - R) * 8; i += kTcThreads) {
+    const int tile = i / ((kTcRows - R) * 8), in = i % ((kTcRows - R) * 8);
+    *reinterpret_cast<uint4*>(smem + kOffQ + tile * kAtom + R * 128 + in * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_proxy_async();
   pdl_wait();
   pdl_launch_dependents();
 
   // ---- the pairs of sequence and key tile, and their order
-  const int per_thread = (a.num_seqs + kTcThreads - 1) / kTcThreads;
+  const int per_thread = (a.num_seqs + kTcLine - 1) / kTcLine;
   long long mine = 0;
-  for (int i = 0; i < per_thread; ++i) {
+  for (int i = 0; i < per_thread && tid < kTcLine; ++i) {
     const int b = tid * per_thread + i;
     if (b < a.num_seqs) {
       const WeightSeq s = WeightSeq::of(a, b);
@@ -190,73 +210,128 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const long long v = __shfl_up_sync(0xffffffffu, run, o);
     if (lane >= o) run += v;
   }
-  if (lane == 31) sh.warp_long[warp] = run;
+  if (lane == 31 && tid < kTcLine) sh.warp_sum[warp] = run;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  long long before = 0, pairs = 0;
+  long long before = 0, pairs = 0;  // (in front of this thread's)
 #pragma unroll
-  for (int w = 0; w < kTcWarps; ++w) {
-    if (w < warp) before += sh.warp_long[w];
-    pairs += sh.warp_long[w];
+  for (int w = 0; w < kTcLine / 32; ++w) {
+    if (w < warp) before += sh.warp_sum[w];
+    pairs += sh.warp_sum[w];
   }
-  before += run - mine;
-  sh.prefix[tid] = before;
-  const bool sorted = pairs <= kTcPairs;
-  if (sorted && mine > 0) {
-    int at = static_cast<int>(before);
-    for (int i = 0; i < per_thread; ++i) {
-      const int b = tid * per_thread + i;
-      if (b >= a.num_seqs) break;
-      const WeightSeq s = WeightSeq::of(a, b);
-      if (!tc_mine(s, group, p.max_packed_rows)) continue;
-      const int first = tc_first(s, a.window), n = tc_count(s, a.window);
-      for (int k = 0; k < n; ++k, ++at) {
-        int row0, rows;
-        tc_rows(s, first + k, group, a.window, row0, rows);
-        sh.pair_b[at] = b, sh.pair_kt[at] = first + k, sh.pair_tiles[at] = (rows + kTcRows - 1) / kTcRows;
-      }
-    }
-  }
+  if (tid < kTcLine) sh.prefix[tid] = before + run - mine;
+  if (tid < kTcCtasMax) sh.load[tid] = 0;
+  const long long items = pairs * a.num_kv_heads, G = gridDim.x;
+  const bool sorted = pairs <= kTcPairs && items <= kTcDeal * G;
   __syncthreads();
-  if (sorted && tid < pairs) {  // a pair's place: those of more tiles first, then in their own order
-    const int n = sh.pair_tiles[tid];
-    int place = 0;
-    for (int i = 0; i < static_cast<int>(pairs); ++i) {
-      const int m = sh.pair_tiles[i];
-      place += m > n || (m == n && i < tid) ? 1 : 0;
-    }
-    sh.sorted[place] = tid;
-  }
-  __syncthreads();
-  const uint32_t taddr = sh.taddr;
-  const long long items = pairs * a.num_kv_heads;
-  // The CTA's k-th item (by whole warps); false: there is none.
-  auto item_at = [&](long long k, TcItem& it) -> bool {
-    const long long G = gridDim.x, c = blockIdx.x;
-    const long long e = k * G + ((k & 1) && sorted ? G - 1 - c : c);
-    if (e >= items) return false;
-    const long long pr = quotient(e, a.num_kv_heads);
-    it.h = static_cast<int>(e - pr * a.num_kv_heads);
-    if (sorted) {
-      const int at = sh.sorted[pr];
-      it.b = sh.pair_b[at], it.kt = sh.pair_kt[at];
+  // The sequence of a pair, by one thread (the last prefix that is not past it).
+  auto pair_of = [&](long long pr, TcItem& it) {
+    int lo = 0;
+#pragma unroll
+    for (int step = kTcLine / 2; step; step /= 2)
+      if (sh.prefix[lo + step] <= pr) lo += step;
+    long long off = pr - sh.prefix[lo];
+    for (it.b = lo * per_thread;; ++it.b) {
       it.seq = WeightSeq::of(a, it.b);
-    } else {
-      const int lo = last_not_past<kTcWarps>(sh.prefix, pr, lane);
-      long long off = pr - sh.prefix[lo];
-      for (it.b = lo * per_thread;; ++it.b) {
-        it.seq = WeightSeq::of(a, it.b);
-        const int n = tc_mine(it.seq, group, p.max_packed_rows) ? tc_count(it.seq, a.window) : 0;
-        if (off < n) break;
-        off -= n;
-      }
-      it.kt = tc_first(it.seq, a.window) + static_cast<int>(off);
+      const int n = tc_mine(it.seq, group, p.max_packed_rows) ? tc_count(it.seq, a.window) : 0;
+      if (off < n) break;
+      off -= n;
     }
+    it.kt = tc_first(it.seq, a.window) + static_cast<int>(off);
     tc_rows(it.seq, it.kt, group, a.window, it.row0, it.rows);
+  };
+  if (sorted) {
+    TcItem it;
+    if (tid < pairs) {
+      pair_of(tid, it);
+      sh.pair[tid] = {it.b, it.kt, it.row0, it.rows, it.seq.q0, it.seq.q_rows, it.seq.rows, it.seq.kv, it.seq.end};
+    }
+    __syncthreads();
+    if (tid < pairs) {  // a pair's place: those of more tiles first, then in their own order
+      int place = 0;
+      for (int i = 0; i < static_cast<int>(pairs); ++i) {
+        const int m = (sh.pair[i].rows + R - 1) / R;
+        place += m > it.tiles(R) || (m == it.tiles(R) && i < tid) ? 1 : 0;
+      }
+      sh.sorted[place] = tid;
+    }
+    __syncthreads();
+    // Rounds: the CTA with the least so far takes the round's largest item, and so on.  (6 chunks of
+    // 800 to 2000 rows: 760 items, the longest CTA has 1.05 of the mean; to and fro, 1.17.)
+    for (int k = 0; k * G < items; ++k) {
+      int rank = 0, size = 0;
+      if (tid < G) {
+        const int own = sh.load[tid];
+        for (int i = 0; i < static_cast<int>(G); ++i) {
+          const int other = sh.load[i];
+          rank += other < own || (other == own && i < tid) ? 1 : 0;
+        }
+        const long long e = k * G + rank;
+        const bool has = e < items;
+        if (has) size = (sh.pair[sh.sorted[static_cast<int>(e) / a.num_kv_heads]].rows + R - 1) / R + kTcFixed;
+        if (tid == blockIdx.x) sh.dealt[k] = has ? static_cast<int>(e) : -1;
+      }
+      __syncthreads();
+      if (tid < G) sh.load[tid] += size;
+      __syncthreads();
+    }
+  }
+  const uint32_t taddr = sh.taddr;
+  // The CTA's items one after the other; false: there is no (further) one.
+  const long long per = quotient(items + G - 1, G);
+  struct Walk {
+    TcItem it;
+    long long k;
+  };
+  auto deal = [&](Walk& w) -> bool {  // the item of this CTA's round k (one without is the last)
+    if (w.k * G >= items) return false;
+    const int e = sh.dealt[w.k];
+    if (e < 0) return false;
+    const auto& x = sh.pair[sh.sorted[e / a.num_kv_heads]];
+    w.it.h = e % a.num_kv_heads;
+    w.it.b = x.b, w.it.kt = x.kt, w.it.row0 = x.row0, w.it.rows = x.rows;
+    w.it.seq.q0 = x.q0, w.it.seq.q_rows = x.q_rows, w.it.seq.rows = x.seq_rows, w.it.seq.kv = x.kv, w.it.seq.end = x.end;
     return true;
   };
-  // (a place past the end in one round is followed by none that is not)
+  auto first_item = [&](Walk& w) -> bool {
+    w.k = 0;
+    if (sorted) return deal(w);
+    // (own order: sequence, head, key tile; a pair stands for a key tile of one head here)
+    const long long e = blockIdx.x * per;
+    if (e >= items) return false;
+    int lo = 0;
+#pragma unroll
+    for (int step = kTcLine / 2; step; step /= 2)
+      if (sh.prefix[lo + step] * a.num_kv_heads <= e) lo += step;
+    long long off = e - sh.prefix[lo] * a.num_kv_heads;
+    int n;
+    for (w.it.b = lo * per_thread;; ++w.it.b) {
+      w.it.seq = WeightSeq::of(a, w.it.b);
+      n = tc_mine(w.it.seq, group, p.max_packed_rows) ? tc_count(w.it.seq, a.window) : 0;
+      if (off < static_cast<long long>(n) * a.num_kv_heads) break;
+      off -= static_cast<long long>(n) * a.num_kv_heads;
+    }
+    w.it.h = static_cast<int>(quotient(off, n));
+    w.it.kt = tc_first(w.it.seq, a.window) + static_cast<int>(off - static_cast<long long>(w.it.h) * n);
+    tc_rows(w.it.seq, w.it.kt, group, a.window, w.it.row0, w.it.rows);
+    return true;
+  };
+  auto next_item = [&](Walk& w) -> bool {
+    ++w.k;
+    if (sorted) return deal(w);
+    if (w.k >= per || blockIdx.x * per + w.k >= items) return false;
+    if (++w.it.kt - tc_first(w.it.seq, a.window) == tc_count(w.it.seq, a.window)) {
+      if (++w.it.h == a.num_kv_heads) {
+        w.it.h = 0;
+        do w.it.seq = WeightSeq::of(a, ++w.it.b);
+        while (!tc_mine(w.it.seq, group, p.max_packed_rows) || tc_count(w.it.seq, a.window) == 0);
+      }
+      w.it.kt = tc_first(w.it.seq, a.window);
+    }
+    tc_rows(w.it.seq, w.it.kt, group, a.window, w.it.row0, w.it.rows);
+    return true;
+  };
   auto given_up = [&]() { return __any_sync(0xffffffffu, cta_abort.raised()) != 0; };
 
   if (warp < 8) {
@@ -266,51 +341,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const float c = score_factor(1.0f, a.score_scale * kTcLog2e);
     uint32_t t = 0;  // row tiles so far
     bool lost = false;
-    TcItem it;
-    for (long long k = 0; item_at(k, it) && !given_up(); ++k) {
-      const int j = it.kt * kTcKeys + key_in;
+    // This thread's key of an item: what it has so far and its page are asked for an item ahead.
+    struct Key {
+      float* w;         // null: not this call's
+      float old;
+      int page;
+      int row0, rows;   // the item's
+      int see0, see1;   // the packed rows that see the key
+    };
+    auto key_of = [&](const TcItem& it) {
+      Key x;
+      const int j = it.kt * kTcKeys + key_in, before_rows = it.seq.kv - it.seq.rows;
       const bool there = j < it.seq.end && j >= it.seq.first_key(0, a.window);
-      const int before_rows = it.seq.kv - it.seq.rows;
-      float* w = a.weights + (static_cast<long long>(it.b) * a.num_kv_heads + it.h) * a.capacity + j;
-      float old = 0.0f;
-      bool draws = false;
+      x.w = nullptr;
+      x.old = 0.0f;
+      x.page = 0;
       if (there) {
-        const int page = __ldg(a.page_table + it.b * a.table_stride + j / a.page_size);
-        draws = page >= 0 && page < a.num_pages;
-        lost = lost || !draws;
-        if (j < before_rows) old = *w;
+        x.w = a.weights + (static_cast<long long>(it.b) * a.num_kv_heads + it.h) * a.capacity + j;
+        x.page = __ldg(a.page_table + it.b * a.table_stride + j / a.page_size);
+        if (j < before_rows) x.old = *x.w;
       }
-      // the packed rows that see this key: [see0, see1)
-      const int see0 = max(j - before_rows, 0) * group;
-      int see1 = it.row0 + it.rows;
+      x.row0 = it.row0, x.rows = it.rows;
+      x.see0 = max(j - before_rows, 0) * group;
+      x.see1 = it.row0 + it.rows;
       if (a.window > 0) {
         const long long i1 = static_cast<long long>(j) + a.window - before_rows;  // behind the last
-        if (i1 * group < see1) see1 = static_cast<int>(max(i1 * group, 0ll));
+        if (i1 * group < x.see1) x.see1 = static_cast<int>(max(i1 * group, 0ll));
       }
+      return x;
+    };
+    Walk walk;
+    bool more = first_item(walk);
+    Key next;
+    if (more) next = key_of(walk.it);
+    while (more && !given_up()) {
+      const Key key = next;
+      more = next_item(walk);
+      if (more) next = key_of(walk.it);
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      const int tiles = it.tiles();
-      for (int x = 0; x < tiles; ++x, ++t) {
+      for (int r0 = key.row0; r0 < key.row0 + key.rows; r0 += R, ++t) {
         const int buf = t & 1, slot = t % kTcAhead;
         cta_abort.wait(bar(sh.l_full[slot]), (t / kTcAhead) & 1);
         cta_abort.wait(bar(sh.s_full[buf]), (t >> 1) & 1);
         __syncwarp();
         tc_fence_after();
-        const int r0 = it.row0 + x * kTcRows;
-        const int lo = max(see0 - r0, 0), hi = min(see1 - r0, kTcRows);  // columns that count
-        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < kTcRows) || sh.odd[slot] != 0;
+        const int lo = max(key.see0 - r0, 0), hi = min(key.see1 - r0, R);  // columns that count
+        const uint4 adds = *reinterpret_cast<const uint4*>(sh.adds[slot]);
+        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < R) || (adds.x & adds.y & adds.z & adds.w) != ~0u;
         const uint32_t at = tS + buf * 2 * kTcRows;
-        const float* neg = sh.neg[slot];
+        const float4* neg = reinterpret_cast<const float4*>(sh.neg[slot]);
         if (!masked) {
-          uint32_t v[2][32];
-          tc_ld32_start(at, v[0]);
+          uint32_t v[2][16];
+          tc_ld16_start(at, v[0]);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t (&s)[32] = v[q & 1];
-            tc_ld32_wait(s);
-            if (q < 3) tc_ld32_start(at + 32 * (q + 1), v[(q + 1) & 1]);
+          for (int q = 0; q < 8; ++q) {
+            uint32_t (&s)[16] = v[q & 1];
+            tc_ld16_wait(s);
+            if (q < 7) tc_ld16_start(at + 16 * (q + 1), v[(q + 1) & 1]);
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 n = *reinterpret_cast<const float4*>(neg + 32 * q + e);
+            for (int e = 0; e < 16; e += 4) {
+              const float4 n = neg[4 * q + e / 4];
               float x0, x1, x2, x3;
               tc_fma2(x0, x1, s[e], s[e + 1], c, n.x, n.y);
               tc_fma2(x2, x3, s[e + 2], s[e + 3], c, n.z, n.w);
@@ -320,17 +410,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
         } else {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            if (!__any_sync(0xffffffffu, lo < 32 * q + 32 && hi > 32 * q)) continue;
-            uint32_t s[32];
-            tc_ld32_start(at + 32 * q, s);
-            tc_ld32_wait(s);
+          for (int q = 0; q < 8; ++q) {
+            const uint32_t four = (q & 4) ? ((q & 2) ? adds.w : adds.z) : ((q & 2) ? adds.y : adds.x);
+            const uint32_t see = (four >> (16 * (q & 1))) & low_bits(hi - 16 * q) & ~low_bits(lo - 16 * q) & 0xFFFFu;
+            if (!__any_sync(0xffffffffu, see != 0)) continue;
+            uint32_t s[16];
+            tc_ld16_start(at + 16 * q, s);
+            tc_ld16_wait(s);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float n = neg[32 * q + e];
-              const float x0 = exp2_approx(fmaf(__uint_as_float(s[e]), c, n));
-              const bool in = 32 * q + e >= lo && 32 * q + e < hi && n != -INFINITY;
-              sum[e & 3] += in ? x0 : 0.0f;
+            for (int e = 0; e < 16; e += 4) {
+              const float4 n = neg[4 * q + e / 4];
+              float x[4];
+              tc_fma2(x[0], x[1], s[e], s[e + 1], c, n.x, n.y);
+              tc_fma2(x[2], x[3], s[e + 2], s[e + 3], c, n.z, n.w);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float y = exp2_approx(x[i]);
+                sum[i] += (see >> (e + i)) & 1u ? y : 0.0f;
+              }
             }
           }
         }
@@ -338,149 +435,196 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
         if (lane == 0 && !cta_abort.raised()) mbar_arrive(bar(sh.s_empty[buf]));
       }
-      if (there && !cta_abort.raised())
-        *w = old + (draws ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.0f);
+      const bool draws = key.page >= 0 && key.page < a.num_pages;
+      lost = lost || !draws;
+      if (key.w && !cta_abort.raised())
+        *key.w = key.old + (draws ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.0f);
     }
     if (lost && a.status) atomicOr(a.status, kStatusBadSlot);
-  } else if (warp < 12) {
+  } else if (warp < 16) {
     // -------------------------------------------------------------- keys
     const int r = tid - 256;
     const int page_blocks = a.page_size / 16;
-    uint4 codes[2][D / 32];
-    uint32_t scales[2][D / 64];
-    auto load = [&](const TcItem& it) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int j = it.kt * kTcKeys + s * 128 + r;
-        const uint8_t* blk = nullptr;
-        if (j < it.seq.end && j >= it.seq.first_key(0, a.window)) {
-          const int pg = j / a.page_size, in = (j - pg * a.page_size) / 16;
-          const int page = __ldg(a.page_table + it.b * a.table_stride + pg);
-          if (page >= 0 && page < a.num_pages)
-            blk = a.cache + ((static_cast<long long>(page) * a.num_kv_heads + it.h) * page_blocks + in) * B::kBytes;
-        }
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c)
-          codes[s][c] = blk ? __ldg(reinterpret_cast<const uint4*>(blk + (j & 15) * B::kCodeRow) + c)
-                            : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          scales[s][c] = blk ? __ldg(reinterpret_cast<const uint32_t*>(blk + B::kKScale + (j & 15) * B::kScaleRow) + c)
-                             : 0u;
-      }
+    const long long page_bytes = static_cast<long long>(a.num_kv_heads) * page_blocks * B::kBytes;
+    // A walk two items ahead asks for the page of this thread's key, one ahead for its codes.
+    struct Codes {
+      bool used;
+      uint4 codes[D / 32];
+      uint32_t scales[D / 64];
     };
-    TcItem it;
+    Walk walk;
+    bool more = first_item(walk);
+    int page, in_page = 0;
+    bool exists, used = false;  // of the item looked up last
+    auto look_up = [&]() {
+      exists = more;
+      page = -1;
+      if (!more) return;
+      const TcItem& it = walk.it;
+      used = it.rows > 0;
+      const int j = it.kt * kTcKeys + r;
+      if (j < it.seq.end && j >= it.seq.first_key(0, a.window)) {
+        const int pg = j / a.page_size, in = j - pg * a.page_size;
+        page = __ldg(a.page_table + it.b * a.table_stride + pg);
+        in_page = (it.h * page_blocks + in / 16) * B::kBytes;
+      }
+      more = next_item(walk);
+    };
+    auto fetch = [&](Codes& x) -> bool {  // of the item looked up last; then the next is
+      x.used = used;
+      const bool there = exists;
+      const uint8_t* blk = page >= 0 && page < a.num_pages ? a.cache + page * page_bytes + in_page : nullptr;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c)  // (an item's keys begin at a multiple of 16)
+        x.codes[c] = blk ? __ldg(reinterpret_cast<const uint4*>(blk + (r & 15) * B::kCodeRow) + c)
+                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c)
+        x.scales[c] = blk ? __ldg(reinterpret_cast<const uint32_t*>(blk + B::kKScale + (r & 15) * B::kScaleRow) + c)
+                          : 0u;
+      look_up();
+      return there;
+    };
     uint32_t n = 0;  // items with products so far
-    bool more = item_at(0, it);
-    if (more) load(it);
-    for (long long k = 0; more && !given_up(); ++k) {
-      const bool used = it.rows > 0;
-      if (used) {
-        const int st = n & 1;
-        if (n >= 2) cta_abort.wait(bar(sh.k_empty[st]), ((n >> 1) - 1) & 1);
-        __syncwarp();
+    auto widen = [&](const Codes& x) {
+      if (!x.used) return;
+      const int st = n & 1;
+      if (n >= 2) cta_abort.wait(bar(sh.k_empty[st]), ((n >> 1) - 1) & 1);
+      __syncwarp();
+      unsigned char* tile = smem + (st * 2 + (r >> 7)) * kTile;
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          unsigned char* tile = smem + (st * 2 + s) * kTile;
+      for (int c = 0; c < D / 32; ++c) {  // 32 dimensions: two scales, four 16-byte chunks
+        const uint32_t h = e4m3x2_to_f16(x.scales[c / 2] >> (16 * (c & 1)));
+        const uint32_t f[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
+        const uint32_t y[4] = {x.codes[c].x, x.codes[c].y, x.codes[c].z, x.codes[c].w};
 #pragma unroll
-          for (int c = 0; c < D / 32; ++c) {  // 32 dimensions: two scales, four 16-byte chunks
-            const uint32_t h = e4m3x2_to_f16(scales[s][c / 2] >> (16 * (c & 1)));
-            const uint32_t f[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
-            const uint32_t x[4] = {codes[s][c].x, codes[s][c].y, codes[s][c].z, codes[s][c].w};
+        for (int e = 0; e < 4; ++e) {
+          uint32_t v[4];
+          e2m1x8_to_f16(y[e], v);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              uint32_t v[4];
-              e2m1x8_to_f16(x[e], v);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                v[i] = tc_hmul2(v[i], f[e / 2]);
-                if constexpr (!F16) {
-                  const float2 u = unpack_f16x2(v[i]);
-                  v[i] = pack_bf16x2(u.x, u.y);
-                }
-              }
-              const int ch = 4 * c + e;
-              *reinterpret_cast<uint4*>(tile + (ch >> 3) * kAtom + swz128(r, ch & 7)) =
-                  make_uint4(v[0], v[1], v[2], v[3]);
+          for (int i = 0; i < 4; ++i) {
+            v[i] = tc_hmul2(v[i], f[e / 2]);
+            if constexpr (!F16) {
+              const float2 u = unpack_f16x2(v[i]);
+              v[i] = pack_bf16x2(u.x, u.y);
             }
           }
+          const int ch = 4 * c + e;
+          *reinterpret_cast<uint4*>(tile + (ch >> 3) * kAtom + swz128(r & 127, ch & 7)) =
+              make_uint4(v[0], v[1], v[2], v[3]);
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0 && !cta_abort.raised()) mbar_arrive(bar(sh.k_full[st]));
-        ++n;
       }
-      more = item_at(k + 1, it);
-      if (more) load(it);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0 && !cta_abort.raised()) mbar_arrive(bar(sh.k_full[st]));
+      ++n;
+    };
+    Codes x[2];
+    look_up();
+    bool here = fetch(x[0]);
+    while (here && !given_up()) {
+      const bool then = fetch(x[1]);
+      widen(x[0]);
+      if (!then || given_up()) break;
+      here = fetch(x[0]);
+      widen(x[1]);
     }
-  } else if (warp < 15) {
+  } else if (warp > 16) {
     // -------------------------------------------------------------- rows
-    constexpr int CHUNKS = D / 8;  // 16-byte chunks of a row
-    const int r = tid - 384;
+    constexpr int CHUNKS = D / 8, AT_ONCE = 32 / CHUNKS;  // 16-byte chunks of a row, rows of a warp's copy
+    const int r = tid - 17 * 32, ch = lane % CHUNKS;
+    const uint32_t magic = ((1u << 20) + group - 1) / group;  // n / group = n * magic >> 20 for n < 2^9
     bool odd_path = false;
     uint32_t t = 0;
-    TcItem it;
-    for (long long k = 0; item_at(k, it) && !given_up(); ++k) {
-      const int tiles = it.tiles();
-      for (int x = 0; x < tiles; ++x, ++t) {
+    Walk walk;
+    for (bool more = first_item(walk); more && !given_up(); more = next_item(walk)) {
+      const TcItem& it = walk.it;
+      const uint16_t* q_head = a.q + static_cast<long long>(it.h) * group * D + 8 * ch;
+      for (int r0 = it.row0; r0 < it.row0 + it.rows; r0 += R, ++t) {
         const int st = t & 1, slot = t % kTcAhead;
+        const int cols = min(it.row0 + it.rows - r0, R);
+        const int i0 = r0 / group, g0 = r0 - i0 * group;  // the tile's first row and head
+        // the place of the tile's packed row c in q (below 0: none) and its head
+        auto place = [&](int c, int& head) {
+          const int i = static_cast<int>((static_cast<uint32_t>(g0 + c) * magic) >> 20);
+          head = g0 + c - i * group;
+          return it.seq.row_in_q(a, it.b, i0 + i);
+        };
+        float lse[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = r + u * kTcCopiers;
+          lse[u] = -INFINITY;
+          if (c < cols) {
+            int head;
+            const int at = place(c, head);
+            if (at >= 0) lse[u] = __ldg(a.lse + static_cast<long long>(at) * a.num_q_heads + it.h * group + head);
+            else odd_path = true;
+          }
+        }
         if (t >= 2) cta_abort.wait(bar(sh.q_empty[st]), ((t >> 1) - 1) & 1);
         __syncwarp();
-        const int r0 = it.row0 + x * kTcRows, cols = min(it.row0 + it.rows - r0, kTcRows);
-        const int padded = (cols + 15) & ~15;
-        for (int u = r; u < padded * CHUNKS; u += kTcRowThreads) {
-          const int c = u / CHUNKS, ch = u % CHUNKS, row = r0 + min(c, cols - 1);
-          const int i = row / group, head = it.h * group + row - i * group;
-          const int at = it.seq.row_in_q(a, it.b, i);
-          const bool real = c < cols && at >= 0;
-          cp_async_16(sbase + kOffQ + st * kTile + (ch >> 3) * kAtom + swz128(c, ch & 7),
-                      a.q + (real ? at : 0) * a.q_stride + head * D + 8 * ch, real);
-        }
-        // (the copies arrive themselves as they land; the products' warp fences)
-        if (!given_up()) cp_async_mbar_arrive(bar(sh.q_full[st]));
-        bool odd = false;
-        for (int c = r; c < kTcRows; c += kTcRowThreads) {
-          float lse = -INFINITY;
-          if (c < cols) {
-            const int row = r0 + c, i = row / group, head = it.h * group + row - i * group;
-            const int at = it.seq.row_in_q(a, it.b, i);
-            if (at >= 0) lse = __ldg(a.lse + static_cast<long long>(at) * a.num_q_heads + head);
-            else odd_path = true;
-            odd = odd || lse == -INFINITY;
+        const uint32_t to = sbase + kOffQ + st * kTile;
+        const bool stop = given_up();
+        if (p.by_tma) {
+          if (warp == 17 && !stop && tc_elect()) {
+            mbar_arrive_expect_tx(bar(sh.q_full[st]), static_cast<uint32_t>(ATOMS * R * 128));
+#pragma unroll
+            for (int x = 0; x < ATOMS; ++x)
+              tma_load_3d(to + x * kAtom, &params.q, 64 * x, it.h * group, it.seq.q0 + i0, bar(sh.q_full[st]));
           }
-          sh.neg[slot][c] = lse == -INFINITY ? -INFINITY : -(lse * kTcLog2e);
+          __syncwarp();
+        } else {
+          const int padded = (cols + 15) & ~15;
+#pragma unroll 4
+          for (int c = (warp - 17) * AT_ONCE + lane / CHUNKS; c < padded; c += 3 * AT_ONCE) {
+            int head;
+            const int at = place(min(c, cols - 1), head);
+            const bool real = c < cols && at >= 0;
+            cp_async_16(to + (ch >> 3) * kAtom + swz128(c, ch & 7), q_head + (real ? at : 0) * a.q_stride + head * D,
+                        real);
+          }
+          // (the copies arrive themselves as they land; the products' warp fences)
+          if (!stop) cp_async_mbar_arrive(bar(sh.q_full[st]));
         }
-        // (all three warps write the flag's word before any lane of another reads it: l_full)
-        odd = __any_sync(0xffffffffu, odd);
-        if (lane == 0) {
-          reinterpret_cast<volatile unsigned char*>(&sh.odd[slot])[warp - 12] = odd ? 1 : 0;
-          if (warp == 12) reinterpret_cast<volatile unsigned char*>(&sh.odd[slot])[3] = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int c = r + u * kTcCopiers;
+          if (c < kTcRows) {  // (a whole warp, or none of it)
+            sh.neg[slot][c] = lse[u] == -INFINITY ? -INFINITY : -(lse[u] * kTcLog2e);
+            const uint32_t adds = __ballot_sync(0xffffffffu, c >= cols || lse[u] != -INFINITY);
+            if (lane == 0) sh.adds[slot][c / 32] = adds;
+          }
         }
         __syncwarp();
-        if (lane == 0 && !cta_abort.raised()) mbar_arrive(bar(sh.l_full[slot]));
+        if (lane == 0 && !stop) mbar_arrive(bar(sh.l_full[slot]));
       }
     }
+    // (a call that gives up waits for the boxes that it has asked for)
+    if (p.by_tma && warp == 17 && lane == 0 && cta_abort.raised())
+      for (uint32_t x = t > 2 ? t - 2 : 0; x < t; ++x)
+        mbar_drain(bar(sh.q_full[x & 1]), (x >> 1) & 1, p.wait_limit_ns);
+    __syncwarp();
     if (odd_path && a.status) atomicOr(a.status, kStatusBadLength);
   } else {
     // -------------------------------------------------------------- products
     uint32_t t = 0, n = 0;
-    TcItem it;
+    Walk walk;
     bool ok = true;
-    for (long long k = 0; ok && item_at(k, it); ++k) {
-      const int tiles = it.tiles();
-      if (tiles == 0) continue;
+    for (bool more = first_item(walk); ok && more; more = next_item(walk)) {
+      const TcItem& it = walk.it;
+      if (it.rows == 0) continue;
       const int ka = n & 1;
       ok = __all_sync(0xffffffffu, cta_abort.wait(bar(sh.k_full[ka]), (n >> 1) & 1));
-      for (int x = 0; ok && x < tiles; ++x, ++t) {
+      for (int left = it.rows; ok && left > 0; left -= R, ++t) {
         const int st = t & 1;
         ok = cta_abort.wait(bar(sh.q_full[st]), (t >> 1) & 1);
         if (t >= 2) ok = cta_abort.wait(bar(sh.s_empty[st]), ((t >> 1) - 1) & 1) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        fence_proxy_async();  // the rows were written by copies of other threads
+        fence_proxy_async();  // (rows that copies of other threads wrote)
         tc_fence_after();
-        const int cols = min(it.rows - x * kTcRows, kTcRows);
-        const uint32_t idesc = kIdesc | (static_cast<uint32_t>((cols + 15) >> 4) << 18);
+        const uint32_t idesc = kIdesc | (static_cast<uint32_t>((min(left, R) + 15) >> 4) << 18);
         if (tc_elect()) {
           const uint64_t dq = umma_desc_sw128(sbase + kOffQ + st * kTile, 16, 1024);
 #pragma unroll
@@ -494,7 +638,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           }
           umma_commit(bar(sh.s_full[st]));
           umma_commit(bar(sh.q_empty[st]));
-          if (x + 1 == tiles) umma_commit(bar(sh.k_empty[ka]));
+          if (left <= R) umma_commit(bar(sh.k_empty[ka]));
         }
         __syncwarp();
       }
@@ -512,7 +656,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 15)
+  if (warp == 16)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(taddr), "r"(512u)
                  : "memory");
   if (tid == 0 && cta_abort.raised() && a.status) atomicOr(a.status, kStatusTimeout);
@@ -526,13 +670,18 @@ int launch_kv4_weights_tc(const Kv4WeightsArgs& a, int max_packed_rows, bool f16
                               : reinterpret_cast<const void*>(lora_kv4_weights_tc_kernel<128, false>));
   const size_t smem = 1024 + 6 * static_cast<size_t>(a.head_dim / 64) * 128 * 128 + sizeof(TcShared);
   if (ensure_smem_attr(fn, smem) != 0) return -6;
-  const int sms = device_sm_count();
+  const int sms = std::min(device_sm_count(), kTcCtasMax);
   if (sms <= 0) return -6;
-  TcParams p;
-  p.a = a;
-  p.max_packed_rows = max_packed_rows;
-  p.wait_fault = wait_fault() ? 1 : 0;
-  p.wait_limit_ns = p.wait_fault ? kTestWaitLimitNs : kWaitLimitNs;
+  TcParamsTma p;
+  p.p.a = a;
+  p.p.max_packed_rows = max_packed_rows;
+  const int group = a.num_q_heads / a.num_kv_heads;
+  p.p.tile_rows = group <= kTcRows ? kTcRows / group * group : kTcRows;
+  p.p.by_tma = !a.path && group <= kTcRows &&
+               make_tmap_3d(&p.q, a.q, a.head_dim, a.num_q_heads, a.max_num_tokens, a.head_dim * 2ll,
+                            a.q_stride * 2, group, kTcRows / group) == 0;
+  p.p.wait_fault = wait_fault() ? 1 : 0;
+  p.p.wait_limit_ns = p.p.wait_fault ? kTestWaitLimitNs : kWaitLimitNs;
   return launch_pdl(fn, dim3(sms), dim3(kTcThreads), smem, stream, 0, &p);
 }
 

@@ -148,8 +148,9 @@ int make_weight_tmap(CUtensorMap* map, const void* base, long long cols, long lo
   return make_tmap_2d(map, base, cols, rows, cols * 2, box_rows);
 }
 
-int make_tmap_2d(CUtensorMap* map, const void* base, long long cols, long long rows,
-                 long long row_stride_bytes, int box_rows) {
+namespace {
+int encode_tmap(CUtensorMap* map, const void* base, int rank, const cuuint64_t* dims,
+                const cuuint64_t* strides, const cuuint32_t* box) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   static std::once_flag once;
   std::call_once(once, [] {
@@ -161,15 +162,31 @@ int make_tmap_2d(CUtensorMap* map, const void* base, long long cols, long long r
       encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   });
   if (!encode) return -6;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride_bytes)};
-  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
                             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? 0 : -6;
+}
+}  // namespace
+
+int make_tmap_2d(CUtensorMap* map, const void* base, long long cols, long long rows,
+                 long long row_stride_bytes, int box_rows) {
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_stride_bytes)};
+  const cuuint32_t box[2] = {64, static_cast<cuuint32_t>(box_rows)};
+  return encode_tmap(map, base, 2, dims, strides, box);
+}
+
+int make_tmap_3d(CUtensorMap* map, const void* base, long long cols, long long rows, long long planes,
+                 long long row_stride_bytes, long long plane_stride_bytes, int box_rows, int box_planes) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(row_stride_bytes),
+                                 static_cast<cuuint64_t>(plane_stride_bytes)};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), static_cast<cuuint32_t>(box_planes)};
+  return encode_tmap(map, base, 3, dims, strides, box);
 }
 
 }  // namespace grg

@@ -47,6 +47,11 @@ int make_weight_tmap(CUtensorMap* map, const void* base, long long cols, long lo
 int make_tmap_2d(CUtensorMap* map, const void* base, long long cols, long long rows,
                  long long row_stride_bytes, int box_rows);
 
+// A 3-D tensor map over 16-bit [planes][rows][cols] with the given strides (multiples of 16
+// bytes), boxes of box_planes x box_rows x 64 columns with the 128-byte swizzle.
+int make_tmap_3d(CUtensorMap* map, const void* base, long long cols, long long rows, long long planes,
+                 long long row_stride_bytes, long long plane_stride_bytes, int box_rows, int box_planes);
+
 int launch_metadata(const int32_t* mapping, const int32_t* num_tokens, int max_num_tokens,
                     int num_loras, int32_t* sorted_ids, int32_t* counts, int32_t* starts,
                     void* workspace, cudaStream_t stream);

@@ -5,17 +5,17 @@
 // of the key head) that see one of them, 128 at a time:
 //   S_t = K_t Q^T (M = 128 keys, N = rows),  w[key] += sum over rows of 2^(S c - lse log2 e)
 // Keys are the lanes of TMEM, so a key's sum is one thread's: nothing is exchanged, no key's
-// sum is cut, and each is formed in the rows' order.  K stays in shared memory while
-// the rows pass by.  It is widened to q's own 16-bit type: a code times its e4m3 scale has at
+// sum is cut, and each is formed in the rows' order.  K stays in TMEM while the rows pass by
+// (from shared memory, K and the rows together take all of its bandwidth, 128 bytes a cycle:
+// 172 us for 6 chunks).  It is widened to q's own 16-bit type: a code times its e4m3 scale has at
 // most six significant bits, which bf16 holds too, so that q is copied as it is and c is
 // the same for all rows.
 //
 // Warp roles (20 warps of 96 registers, one CTA per SM, persistent):
 //  - warps 0-3 and 4-7: the sums of tile 0 and 1; a thread owns a key
-//  - warps 8-15: widen K into swizzled operand tiles, an item ahead of the products; a thread
-//    has a key, its codes asked for an item ahead, its page two
-//  - warp 16: issues the products; S is double-buffered in TMEM
-//  - warps 17-19: the rows' logarithms, and the rows of q, two tiles deep: by TMA, or, where a path
+//  - warps 8-15: widen K into TMEM; a thread has a key, its codes asked for an item ahead, its page two
+//  - warp 16: issues the products; S has three places in TMEM, which the tiles take in turn
+//  - warps 17-19: the rows' logarithms, and the rows of q, four tiles deep: by TMA, or, where a path
 //    picks them, by copies of 16 bytes
 // Work: few items a CTA (up to kTcDeal) are dealt out in rounds, those of most row tiles first, each
 // round to the CTAs with the least so far; many stay in their own order and are cut into equal runs.
@@ -36,7 +36,9 @@ constexpr int kTcKeys = 256;   // keys of an item
 constexpr int kTcRows = 128;   // packed rows of a tile, at most: whole rows where 128 heads hold one
 constexpr int kTcPairs = 512;  // (sequence, key tile) pairs that can be sorted
 constexpr int kTcDeal = 16;    // items a CTA up to which they are
-constexpr int kTcAhead = 4;    // row tiles' logarithms kept
+constexpr int kTcStages = 4;   // row tiles in shared memory
+constexpr int kTcAhead = 8;    // row tiles' logarithms kept
+constexpr int kTcPlaces = 3;   // of S in TMEM
 constexpr float kTcLog2e = 1.4426950408889634f;
 
 struct TcParams {
@@ -44,6 +46,7 @@ struct TcParams {
   int max_packed_rows;  // sequences with no more packed rows are not this kernel's
   int tile_rows;        // packed rows of a tile
   int by_tma;           // q's rows come by TMA
+  unsigned long long page_magic;  // ceil(2^36 / blocks of a page)
   unsigned long long wait_limit_ns;
   int wait_fault;
 };
@@ -54,10 +57,10 @@ struct TcParamsTma {
 };
 
 struct TcShared {
-  uint64_t q_full[2], q_empty[2];  // by row tile: the rows are there; their products are done
-  uint64_t l_full[kTcAhead];       // and their logarithms
-  uint64_t k_full[2], k_empty[2];  // by item
-  uint64_t s_full[2], s_empty[2];  // by row tile
+  uint64_t q_full[kTcStages], q_empty[kTcStages];  // by row tile: the rows are there; their products are done
+  uint64_t l_full[kTcAhead];                       // and their logarithms
+  uint64_t k_full, k_empty;                        // by item
+  uint64_t s_full[kTcPlaces], s_empty[kTcPlaces];  // by row tile and key tile
   uint64_t drain;
   __align__(16) float neg[kTcAhead][kTcRows];  // -lse log2 e of a tile's rows, -infinity: adds nothing
   __align__(16) uint32_t adds[kTcAhead][4];    // its rows that do (and what lies behind the last)
@@ -69,7 +72,8 @@ struct TcShared {
     int b, kt, row0, rows, q0, q_rows, seq_rows, kv, end;
   } pair[kTcPairs];
   int sorted[kTcPairs];
-  int load[kTcCtasMax], dealt[kTcDeal];  // row tiles of each CTA so far; this one's items
+  __align__(16) int load[kTcCtasMax];
+  int dealt[kTcDeal];  // row tiles of each CTA so far; this one's items
 };
 
 // An item: its keys [256 kt, ...) and the packed rows [row0, row0 + rows) that see one of them.
@@ -77,7 +81,6 @@ struct TcItem {
   int b, h, kt;
   WeightSeq seq;
   int row0, rows;
-  __device__ __forceinline__ int tiles(int tile_rows) const { return (rows + tile_rows - 1) / tile_rows; }
 };
 __device__ __forceinline__ bool tc_mine(const WeightSeq& s, int group, int max_packed_rows) {
   return s.rows > 0 && static_cast<long long>(s.take) * group > max_packed_rows;
@@ -123,6 +126,22 @@ __device__ __forceinline__ void tc_ld16_wait(uint32_t (&r)[16]) {
                  "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
                  "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[shared].
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
 // (s0, s1) * (c, c) + (n0, n1), and a sum, two fp32 at a time.
 __device__ __forceinline__ void tc_fma2(float& x, float& y, uint32_t s0, uint32_t s1, float c, float n0,
                                         float n1) {
@@ -147,8 +166,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int ATOMS = D / 64;                        // 128-byte atoms of a row
   constexpr uint32_t kAtom = 128 * 128;                // 128 rows of one
   constexpr uint32_t kTile = ATOMS * kAtom;            // an operand tile of 128 rows
-  constexpr uint32_t kOffQ = 4 * kTile;                // behind two items' K
-  constexpr uint32_t kOffShared = kOffQ + 2 * kTile;
+  constexpr uint32_t kOffShared = kTcStages * kTile;
+  constexpr uint32_t kColS = D;                        // TMEM columns: two tiles of K, then S
   constexpr uint32_t kIdesc = (1u << 4) | (F16 ? 0u : (1u << 7) | (1u << 10)) | (8u << 24);
 
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -163,14 +182,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int group = a.num_q_heads / a.num_kv_heads;
   auto bar = [&](uint64_t& b) { return smem_u32(&b); };
   if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kTcStages; ++i) {
       mbar_init(bar(sh.q_full[i]), (p.by_tma ? 1 : kTcCopiers) + (p.wait_fault ? 1 : 0));
       mbar_init(bar(sh.q_empty[i]), 1);
-      mbar_init(bar(sh.k_full[i]), 8);
-      mbar_init(bar(sh.k_empty[i]), 1);
-      mbar_init(bar(sh.s_full[i]), 1);
-      mbar_init(bar(sh.s_empty[i]), 8);
     }
+    for (int i = 0; i < kTcPlaces; ++i) {
+      mbar_init(bar(sh.s_full[i]), 1);
+      mbar_init(bar(sh.s_empty[i]), 4);
+    }
+    mbar_init(bar(sh.k_full), 8);
+    mbar_init(bar(sh.k_empty), 1);
     for (int i = 0; i < kTcAhead; ++i) mbar_init(bar(sh.l_full[i]), 3);
     mbar_init(bar(sh.drain), 1);
     fence_mbar_init();
@@ -186,9 +207,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const CtaAbort cta_abort{&sh.abort, p.wait_limit_ns};
   const int R = p.tile_rows;
   // what TMA never writes behind a tile's last row is read by the products all the same
-  for (int i = tid; i < 2 * ATOMS * (kTcRows - R) * 8; i += kTcThreads) {
+  for (int i = tid; i < kTcStages * ATOMS * (kTcRows - R) * 8; i += kTcThreads) {
     const int tile = i / ((kTcRows - R) * 8), in = i % ((kTcRows - R) * 8);
-    *reinterpret_cast<uint4*>(smem + kOffQ + tile * kAtom + R * 128 + in * 16) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(smem + tile * kAtom + R * 128 + in * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async();
   pdl_wait();
@@ -221,7 +242,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     pairs += sh.warp_sum[w];
   }
   if (tid < kTcLine) sh.prefix[tid] = before + run - mine;
-  if (tid < kTcCtasMax) sh.load[tid] = 0;
+  static_assert(4 * kTcCtasMax <= kTcThreads && kTcCtasMax % 16 == 0, "four lanes a CTA, in whole warps");
+  if (tid < kTcCtasMax) sh.load[tid] = tid < static_cast<int>(gridDim.x) ? 0 : 0x7fffffff;
   const long long items = pairs * a.num_kv_heads, G = gridDim.x;
   const bool sorted = pairs <= kTcPairs && items <= kTcDeal * G;
   __syncthreads();
@@ -248,11 +270,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       sh.pair[tid] = {it.b, it.kt, it.row0, it.rows, it.seq.q0, it.seq.q_rows, it.seq.rows, it.seq.kv, it.seq.end};
     }
     __syncthreads();
-    if (tid < pairs) {  // a pair's place: those of more tiles first, then in their own order
+    if (tid < pairs) {  // a pair's place: those of more rows first, then in their own order
       int place = 0;
+#pragma unroll 4
       for (int i = 0; i < static_cast<int>(pairs); ++i) {
-        const int m = (sh.pair[i].rows + R - 1) / R;
-        place += m > it.tiles(R) || (m == it.tiles(R) && i < tid) ? 1 : 0;
+        const int m = sh.pair[i].rows;
+        place += m > it.rows || (m == it.rows && i < tid) ? 1 : 0;
       }
       sh.sorted[place] = tid;
     }
@@ -260,20 +283,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // Rounds: the CTA with the least so far takes the round's largest item, and so on.  (6 chunks of
     // 800 to 2000 rows: 760 items, the longest CTA has 1.05 of the mean; to and fro, 1.17.)
     for (int k = 0; k * G < items; ++k) {
+      // (four lanes count a CTA's rank)
+      const int cta = tid / 4;
       int rank = 0, size = 0;
-      if (tid < G) {
-        const int own = sh.load[tid];
-        for (int i = 0; i < static_cast<int>(G); ++i) {
-          const int other = sh.load[i];
-          rank += other < own || (other == own && i < tid) ? 1 : 0;
+      if (cta < kTcCtasMax) {
+        const int own = sh.load[cta];
+#pragma unroll 5
+        for (int i = 4 * (tid & 3); i < kTcCtasMax; i += 16) {  // (CTAs that are not there count as full)
+          const int4 x = *reinterpret_cast<const int4*>(sh.load + i);
+          rank += (x.x < own || (x.x == own && i < cta) ? 1 : 0) + (x.y < own || (x.y == own && i + 1 < cta) ? 1 : 0) +
+                  (x.z < own || (x.z == own && i + 2 < cta) ? 1 : 0) + (x.w < own || (x.w == own && i + 3 < cta) ? 1 : 0);
         }
+        rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+        rank += __shfl_xor_sync(0xffffffffu, rank, 2);
         const long long e = k * G + rank;
-        const bool has = e < items;
-        if (has) size = (sh.pair[sh.sorted[static_cast<int>(e) / a.num_kv_heads]].rows + R - 1) / R + kTcFixed;
-        if (tid == blockIdx.x) sh.dealt[k] = has ? static_cast<int>(e) : -1;
+        const bool has = cta < G && e < items;
+        if (has && (tid & 3) == 0)
+          size = (sh.pair[sh.sorted[static_cast<int>(e) / a.num_kv_heads]].rows + R - 1) / R + kTcFixed;
+        if ((tid & 3) == 0 && cta == blockIdx.x) sh.dealt[k] = has ? static_cast<int>(e) : -1;
       }
       __syncthreads();
-      if (tid < G) sh.load[tid] += size;
+      if ((tid & 3) == 0 && cta < kTcCtasMax) sh.load[cta] += size;
       __syncthreads();
     }
   }
@@ -332,14 +362,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_rows(w.it.seq, w.it.kt, group, a.window, w.it.row0, w.it.rows);
     return true;
   };
+  auto page_of = [&](int j) {  // j / page_size, for j / 16 < 2^27 and pages of up to 64 blocks
+    return static_cast<int>((static_cast<unsigned long long>(j >> 4) * p.page_magic) >> 36);
+  };
   auto given_up = [&]() { return __any_sync(0xffffffffu, cta_abort.raised()) != 0; };
 
   if (warp < 8) {
     // -------------------------------------------------------------- sums
     const int sub = warp >> 2, key_in = sub * 128 + (warp & 3) * 32 + lane;
-    const uint32_t tS = taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + sub * kTcRows;
+    const uint32_t tS = taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + kColS;
     const float c = score_factor(1.0f, a.score_scale * kTcLog2e);
     uint32_t t = 0;  // row tiles so far
+    uint32_t place = sub, turn = 0;  // where S of (t, sub) is, and how often it was used before
     bool lost = false;
     // This thread's key of an item: what it has so far and its page are asked for an item ahead.
     struct Key {
@@ -358,7 +392,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       x.page = 0;
       if (there) {
         x.w = a.weights + (static_cast<long long>(it.b) * a.num_kv_heads + it.h) * a.capacity + j;
-        x.page = __ldg(a.page_table + it.b * a.table_stride + j / a.page_size);
+        x.page = __ldg(a.page_table + it.b * a.table_stride + page_of(j));
         if (j < before_rows) x.old = *x.w;
       }
       x.row0 = it.row0, x.rows = it.rows;
@@ -370,25 +404,24 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       return x;
     };
-    Walk walk;
-    bool more = first_item(walk);
-    Key next;
-    if (more) next = key_of(walk.it);
-    while (more && !given_up()) {
-      const Key key = next;
-      more = next_item(walk);
-      if (more) next = key_of(walk.it);
+    // A wait that looks at the flag only where the phase is not over yet.
+    auto over = [&](uint64_t& b, uint32_t parity) {
+      return mbar_try_wait(bar(b), parity) || cta_abort.wait(bar(b), parity);
+    };
+    auto item_sum = [&](const Key& key) {
       float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      // the packed rows that all of the warp's keys see, and those that some key does
+      const int all0 = __reduce_max_sync(0xffffffffu, key.see0), all1 = __reduce_min_sync(0xffffffffu, key.see1);
+      const int any0 = __reduce_min_sync(0xffffffffu, key.see0), any1 = __reduce_max_sync(0xffffffffu, key.see1);
       for (int r0 = key.row0; r0 < key.row0 + key.rows; r0 += R, ++t) {
-        const int buf = t & 1, slot = t % kTcAhead;
-        cta_abort.wait(bar(sh.l_full[slot]), (t / kTcAhead) & 1);
-        cta_abort.wait(bar(sh.s_full[buf]), (t >> 1) & 1);
-        __syncwarp();
+        const int slot = t % kTcAhead;
+        bool ok = over(sh.l_full[slot], (t / kTcAhead) & 1);
+        ok = over(sh.s_full[place], turn & 1) && ok;
+        ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
-        const int lo = max(key.see0 - r0, 0), hi = min(key.see1 - r0, R);  // columns that count
         const uint4 adds = *reinterpret_cast<const uint4*>(sh.adds[slot]);
-        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < R) || (adds.x & adds.y & adds.z & adds.w) != ~0u;
-        const uint32_t at = tS + buf * 2 * kTcRows;
+        const bool masked = r0 < all0 || r0 + R > all1 || (adds.x & adds.y & adds.z & adds.w) != ~0u;
+        const uint32_t at = tS + place * kTcRows;
         const float4* neg = reinterpret_cast<const float4*>(sh.neg[slot]);
         if (!masked) {
           uint32_t v[2][16];
@@ -409,36 +442,56 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
           }
         } else {
+          const int lo = key.see0 - r0, hi = min(key.see1 - r0, R);  // this key's columns
+          const int q1 = min(any1 - r0, R);
 #pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
-            const uint32_t four = (q & 4) ? ((q & 2) ? adds.w : adds.z) : ((q & 2) ? adds.y : adds.x);
-            const uint32_t see = (four >> (16 * (q & 1))) & low_bits(hi - 16 * q) & ~low_bits(lo - 16 * q) & 0xFFFFu;
-            if (!__any_sync(0xffffffffu, see != 0)) continue;
-            uint32_t s[16];
-            tc_ld16_start(at + 16 * q, s);
-            tc_ld16_wait(s);
+          for (int q = max(any0 - r0, 0) & ~31; q < q1; q += 32) {
+            const uint32_t four = (q & 64) ? ((q & 32) ? adds.w : adds.z) : ((q & 32) ? adds.y : adds.x);
+            const uint32_t see = four & low_bits(hi - q) & ~low_bits(lo - q);
+            uint32_t v[2][16];
+            tc_ld16_start(at + q, v[0]);
+            tc_ld16_start(at + q + 16, v[1]);
+            tc_ld16_wait(v[0]);
+            tc_ld16_wait(v[1]);
 #pragma unroll
-            for (int e = 0; e < 16; e += 4) {
-              const float4 n = neg[4 * q + e / 4];
+            for (int e = 0; e < 32; e += 4) {
+              uint32_t (&s)[16] = v[e / 16];
+              const float4 n = neg[q / 4 + e / 4];
               float x[4];
-              tc_fma2(x[0], x[1], s[e], s[e + 1], c, n.x, n.y);
-              tc_fma2(x[2], x[3], s[e + 2], s[e + 3], c, n.z, n.w);
+              tc_fma2(x[0], x[1], s[e % 16], s[e % 16 + 1], c, n.x, n.y);
+              tc_fma2(x[2], x[3], s[e % 16 + 2], s[e % 16 + 3], c, n.z, n.w);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const float y = exp2_approx(x[i]);
-                sum[i] += (see >> (e + i)) & 1u ? y : 0.0f;
+                if ((see >> (e + i)) & 1u) sum[i] += y;
               }
             }
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && !cta_abort.raised()) mbar_arrive(bar(sh.s_empty[buf]));
+        if (lane == 0 && ok) mbar_arrive(bar(sh.s_empty[place]));
+        place = place == 0 ? 2 : place - 1;  // two places on
+        if (place != 2) ++turn;
       }
       const bool draws = key.page >= 0 && key.page < a.num_pages;
       lost = lost || !draws;
-      if (key.w && !cta_abort.raised())
+      if (key.w && !cta_abort.raised()) 
         *key.w = key.old + (draws ? (sum[0] + sum[1]) + (sum[2] + sum[3]) : 0.0f);
+    };
+    // (two by turns: a copy of one whose loads are on their way would wait for them)
+    Walk walk;
+    Key x, y;
+    bool more = first_item(walk);
+    if (more) x = key_of(walk.it);
+    while (more && !given_up()) {
+      more = next_item(walk);
+      if (more) y = key_of(walk.it);
+      item_sum(x);
+      if (!more || given_up()) break;
+      more = next_item(walk);
+      if (more) x = key_of(walk.it);
+      item_sum(y);
     }
     if (lost && a.status) atomicOr(a.status, kStatusBadSlot);
   } else if (warp < 16) {
@@ -464,7 +517,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       used = it.rows > 0;
       const int j = it.kt * kTcKeys + r;
       if (j < it.seq.end && j >= it.seq.first_key(0, a.window)) {
-        const int pg = j / a.page_size, in = j - pg * a.page_size;
+        const int pg = page_of(j), in = j - pg * a.page_size;
         page = __ldg(a.page_table + it.b * a.table_stride + pg);
         in_page = (it.h * page_blocks + in / 16) * B::kBytes;
       }
@@ -486,37 +539,39 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       return there;
     };
     uint32_t n = 0;  // items with products so far
+    const uint32_t tK = taddr + (static_cast<uint32_t>((warp & 3) * 32) << 16) + ((warp - 8) >> 2) * (D / 2);
     auto widen = [&](const Codes& x) {
       if (!x.used) return;
-      const int st = n & 1;
-      if (n >= 2) cta_abort.wait(bar(sh.k_empty[st]), ((n >> 1) - 1) & 1);
-      __syncwarp();
-      unsigned char* tile = smem + (st * 2 + (r >> 7)) * kTile;
+      bool ok = true;
+      if (n >= 1) ok = cta_abort.wait(bar(sh.k_empty), (n - 1) & 1);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {  // 32 dimensions: two scales, four 16-byte chunks
+      for (int c = 0; c < D / 32; ++c) {  // 32 dimensions: two scales, 16 columns
         const uint32_t h = e4m3x2_to_f16(x.scales[c / 2] >> (16 * (c & 1)));
         const uint32_t f[2] = {__byte_perm(h, h, 0x1010), __byte_perm(h, h, 0x3232)};
         const uint32_t y[4] = {x.codes[c].x, x.codes[c].y, x.codes[c].z, x.codes[c].w};
+        uint32_t v[16];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t v[4];
-          e2m1x8_to_f16(y[e], v);
+          uint32_t u[4];
+          e2m1x8_to_f16(y[e], u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            v[i] = tc_hmul2(v[i], f[e / 2]);
+            u[i] = tc_hmul2(u[i], f[e / 2]);
             if constexpr (!F16) {
-              const float2 u = unpack_f16x2(v[i]);
-              v[i] = pack_bf16x2(u.x, u.y);
+              const float2 w = unpack_f16x2(u[i]);
+              u[i] = pack_bf16x2(w.x, w.y);
             }
+            v[4 * e + i] = u[i];
           }
-          const int ch = 4 * c + e;
-          *reinterpret_cast<uint4*>(tile + (ch >> 3) * kAtom + swz128(r & 127, ch & 7)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
         }
+        tc_st16(tK + 16 * c, v);
       }
-      fence_proxy_async();
+      asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
+      tc_fence_before();
       __syncwarp();
-      if (lane == 0 && !cta_abort.raised()) mbar_arrive(bar(sh.k_full[st]));
+      if (lane == 0 && ok) mbar_arrive(bar(sh.k_full));
       ++n;
     };
     Codes x[2];
@@ -541,7 +596,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const TcItem& it = walk.it;
       const uint16_t* q_head = a.q + static_cast<long long>(it.h) * group * D + 8 * ch;
       for (int r0 = it.row0; r0 < it.row0 + it.rows; r0 += R, ++t) {
-        const int st = t & 1, slot = t % kTcAhead;
+        const int st = t % kTcStages, slot = t % kTcAhead;
         const int cols = min(it.row0 + it.rows - r0, R);
         const int i0 = r0 / group, g0 = r0 - i0 * group;  // the tile's first row and head
         // the place of the tile's packed row c in q (below 0: none) and its head
@@ -562,9 +617,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             else odd_path = true;
           }
         }
-        if (t >= 2) cta_abort.wait(bar(sh.q_empty[st]), ((t >> 1) - 1) & 1);
+        if (t >= kTcStages) cta_abort.wait(bar(sh.q_empty[st]), (t / kTcStages - 1) & 1);
         __syncwarp();
-        const uint32_t to = sbase + kOffQ + st * kTile;
+        const uint32_t to = sbase + st * kTile;
         const bool stop = given_up();
         if (p.by_tma) {
           if (warp == 17 && !stop && tc_elect()) {
@@ -602,45 +657,46 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     // (a call that gives up waits for the boxes that it has asked for)
     if (p.by_tma && warp == 17 && lane == 0 && cta_abort.raised())
-      for (uint32_t x = t > 2 ? t - 2 : 0; x < t; ++x)
-        mbar_drain(bar(sh.q_full[x & 1]), (x >> 1) & 1, p.wait_limit_ns);
+      for (uint32_t x = t > kTcStages ? t - kTcStages : 0; x < t; ++x)
+        mbar_drain(bar(sh.q_full[x % kTcStages]), (x / kTcStages) & 1, p.wait_limit_ns);
     __syncwarp();
     if (odd_path && a.status) atomicOr(a.status, kStatusBadLength);
   } else {
     // -------------------------------------------------------------- products
-    uint32_t t = 0, n = 0;
+    uint32_t t = 0, n = 0, place = 0, turn = 0;
     Walk walk;
     bool ok = true;
     for (bool more = first_item(walk); ok && more; more = next_item(walk)) {
       const TcItem& it = walk.it;
       if (it.rows == 0) continue;
-      const int ka = n & 1;
-      ok = __all_sync(0xffffffffu, cta_abort.wait(bar(sh.k_full[ka]), (n >> 1) & 1));
+      ok = __all_sync(0xffffffffu, cta_abort.wait(bar(sh.k_full), n & 1));
       for (int left = it.rows; ok && left > 0; left -= R, ++t) {
-        const int st = t & 1;
-        ok = cta_abort.wait(bar(sh.q_full[st]), (t >> 1) & 1);
-        if (t >= 2) ok = cta_abort.wait(bar(sh.s_empty[st]), ((t >> 1) - 1) & 1) && ok;
-        ok = __all_sync(0xffffffffu, ok);
+        const int st = t % kTcStages;
+        ok = __all_sync(0xffffffffu, cta_abort.wait(bar(sh.q_full[st]), (t / kTcStages) & 1));
         if (!ok) break;
         fence_proxy_async();  // (rows that copies of other threads wrote)
-        tc_fence_after();
         const uint32_t idesc = kIdesc | (static_cast<uint32_t>((min(left, R) + 15) >> 4) << 18);
-        if (tc_elect()) {
-          const uint64_t dq = umma_desc_sw128(sbase + kOffQ + st * kTile, 16, 1024);
+        const uint64_t dq = umma_desc_sw128(sbase + st * kTile, 16, 1024);
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint64_t dk = umma_desc_sw128(sbase + (ka * 2 + s) * kTile, 16, 1024);
+        for (int s = 0; s < 2; ++s) {  // (one key tile's sums run under the other's products)
+          if (turn > 0) ok = __all_sync(0xffffffffu, cta_abort.wait(bar(sh.s_empty[place]), (turn - 1) & 1));
+          if (!ok) break;
+          tc_fence_after();
+          if (tc_elect()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
               const uint32_t off = ((kk >> 2) * kAtom + (kk & 3) * 32) >> 4;
-              umma_f16(taddr + (st * 2 + s) * kTcRows, dk + off, dq + off, idesc, kk != 0 ? 1u : 0u);
+              tc_mma_ts(taddr + kColS + place * kTcRows, taddr + s * (D / 2) + 8 * kk, dq + off, idesc, kk != 0 ? 1u : 0u);
+            }
+            umma_commit(bar(sh.s_full[place]));
+            if (s == 1) {
+              umma_commit(bar(sh.q_empty[st]));
+              if (left <= R) umma_commit(bar(sh.k_empty));
             }
           }
-          umma_commit(bar(sh.s_full[st]));
-          umma_commit(bar(sh.q_empty[st]));
-          if (left <= R) umma_commit(bar(sh.k_empty[ka]));
+          __syncwarp();
+          if (++place == kTcPlaces) place = 0, ++turn;
         }
-        __syncwarp();
       }
       ++n;
     }
@@ -668,7 +724,7 @@ int launch_kv4_weights_tc(const Kv4WeightsArgs& a, int max_packed_rows, bool f16
                               : reinterpret_cast<const void*>(lora_kv4_weights_tc_kernel<64, false>))
                        : (f16 ? reinterpret_cast<const void*>(lora_kv4_weights_tc_kernel<128, true>)
                               : reinterpret_cast<const void*>(lora_kv4_weights_tc_kernel<128, false>));
-  const size_t smem = 1024 + 6 * static_cast<size_t>(a.head_dim / 64) * 128 * 128 + sizeof(TcShared);
+  const size_t smem = 1024 + kTcStages * static_cast<size_t>(a.head_dim / 64) * 128 * 128 + sizeof(TcShared);
   if (ensure_smem_attr(fn, smem) != 0) return -6;
   const int sms = std::min(device_sm_count(), kTcCtasMax);
   if (sms <= 0) return -6;
@@ -680,6 +736,8 @@ int launch_kv4_weights_tc(const Kv4WeightsArgs& a, int max_packed_rows, bool f16
   p.p.by_tma = !a.path && group <= kTcRows &&
                make_tmap_3d(&p.q, a.q, a.head_dim, a.num_q_heads, a.max_num_tokens, a.head_dim * 2ll,
                             a.q_stride * 2, group, kTcRows / group) == 0;
+  const unsigned long long page_blocks = a.page_size / 16;
+  p.p.page_magic = ((1ull << 36) + page_blocks - 1) / page_blocks;
   p.p.wait_fault = wait_fault() ? 1 : 0;
   p.p.wait_limit_ns = p.p.wait_fault ? kTestWaitLimitNs : kWaitLimitNs;
   return launch_pdl(fn, dim3(sms), dim3(kTcThreads), smem, stream, 0, &p);

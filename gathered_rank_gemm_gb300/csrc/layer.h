@@ -161,7 +161,8 @@ struct Kv4EvictArgs {
   int recent;
   int32_t* kv_len_out;
   uint32_t* status;
-  int smem_keys;  // the launcher's: keys whose integers are kept in shared memory
+  int smem_keys;  // the launcher's: keys whose integers are kept in shared memory, and pages
+  int smem_pages;
 };
 int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream);
 

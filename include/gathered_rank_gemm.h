@@ -670,7 +670,7 @@ int lora_kv4_accept(uint8_t *cache, int64_t num_pages, int num_kv_heads, int pag
                     const int32_t *path, const int32_t *path_len, int64_t max_path,
                     int32_t *kv_len_out, uint32_t *status, void *stream);
 
-#define LORA_KV4_MAX_KEYS ((1ll << 31) - 4096)
+#define LORA_KV4_MAX_KEYS ((1ll << 31) - 65536)
 
 /*
  * The weight that each key has drawn: for every key head h and every key j of sequence b that

@@ -600,7 +600,8 @@ def test_evict(keys, heads, d, page, budget, sink, recent, kind):
 
 
 @pytest.mark.parametrize("kind", ["spread", "ties"])
-@pytest.mark.parametrize("keys,budget", [([15000], 7000), ([40000, 13000], 2000), ([14000], 13500), ([12289], 12288)])
+@pytest.mark.parametrize("keys,budget", [([15000], 7000), ([40000, 13000], 2000), ([14000], 13500), ([12289], 12288),
+                                         ([60000], 43000), ([4096], 2000), ([4097], 4000)])
 def test_evict_of_long_sequences(keys, budget, kind):
     """More keys than shared memory holds, more moves than are listed at a time."""
     c = _evict_case(keys, 2, 64, 64, kind, seed=budget, held=0.3)

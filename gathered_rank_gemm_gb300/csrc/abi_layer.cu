@@ -434,7 +434,7 @@ int lora_kv4_evict(uint8_t* cache, int64_t num_pages, int num_kv_heads, int page
   a.recent = static_cast<int>(recent);
   a.kv_len_out = kv_len_out;
   a.status = status;
-  a.smem_keys = a.smem_pages = 0;
+  a.smem_keys = a.smem_pages = a.cluster = 0;
   return grg::launch_kv4_evict(a, static_cast<cudaStream_t>(stream));
 }
 

@@ -3,12 +3,16 @@
 // those of the largest weight, ties to the lowest index; the kept keys from `budget` on take
 // the places of the others below it, the first the first, with their weights and positions.
 //
-// One CTA has a head of a sequence.  A key's rank is that of a 32-bit integer that orders like
-// its weight (protected keys above all, NaN below), so the budget-th largest is found by
-// counting digits of 11, 11 and 10 bits from the top (a radix selection).  Then each thread goes
-// over a run of neighbouring keys: one sum over the threads gives holes and movers their
-// numbers in the order of the indices, and D / 16 lanes move an entry.  Integers throughout:
-// the result is exact and does not depend on timing.
+// A key's rank is that of a 32-bit integer that orders like its weight (protected keys above
+// all, NaN below).  Then each thread goes over a run of neighbouring keys: one sum over the
+// threads gives holes and movers their numbers in the order of the indices, and D / 16 lanes
+// move an entry.  Integers throughout: the result is exact and does not depend on timing.
+//
+// The budget-th largest is found by counting digits of 11, 11 and 10 bits from the top (a radix
+// selection), until all keys with the digits so far stay.  A CTA of 256 threads has a head of up
+// to kEvictSmall keys, of 1024 beyond; where there are fewer such heads than SMs, a cluster of
+// CTAs has each: all select, each moves a part.  Integers past what shared memory holds are formed
+// again wherever they are looked at.
 #include <algorithm>
 
 #include "kv4_move.cuh"
@@ -19,13 +23,10 @@ namespace grg {
 
 namespace {
 constexpr int kEvictBins = 2048;  // of a digit
-constexpr int kEvictBatch = 8;    // keys that a thread asks for together
 constexpr int kEvictMoves = 4;    // entries that a lane has in flight
-// CTAs of 256 threads for up to kEvictSmall keys, of 1024 beyond.  Keys behind the last that
-// shared memory holds are formed again wherever they are looked at.
 constexpr int kEvictSmall = 4096;
 constexpr int kEvictKeysMax = 40960;
-constexpr int kEvictTable = 2048;  // pages whose numbers are kept in shared memory
+constexpr int kEvictTable = 2560;  // pages whose numbers are kept in shared memory
 
 template <int T>
 struct EvictShared {
@@ -38,18 +39,21 @@ struct EvictShared {
 };
 }  // namespace
 
-template <int D, int T>
+// ALL: shared memory holds all keys and pages.
+template <int D, int T, bool ALL>
 __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     lora_kv4_evict_kernel(const __grid_constant__ Kv4EvictArgs a) {
   using Entry = Kv4Entry<D>;
   using Shared = EvictShared<T>;
   constexpr int LANES = Entry::kLanes, WARPS = T / 32;
+  constexpr int KEYS = 8;  // keys that a thread asks for together
   extern __shared__ __align__(16) unsigned char smem[];
   Shared& sh = *reinterpret_cast<Shared*>(smem);
   int32_t* s_table = reinterpret_cast<int32_t*>(smem + sizeof(Shared));
   uint32_t* s_keys = reinterpret_cast<uint32_t*>(s_table + a.smem_pages);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / a.num_kv_heads, h = blockIdx.x - b * a.num_kv_heads;
+  const int item = blockIdx.x / a.cluster, rank_in = blockIdx.x - item * a.cluster;
+  const int b = item / a.num_kv_heads, h = item - b * a.num_kv_heads;
   for (int i = tid; i < kEvictBins / 4; i += T) reinterpret_cast<int4*>(sh.bins)[i] = make_int4(0, 0, 0, 0);
   pdl_wait();
   pdl_launch_dependents();
@@ -58,28 +62,21 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
   const long long room = min(a.table_stride * a.page_size, static_cast<long long>(a.capacity));
   const int n = static_cast<int>(min(static_cast<long long>(max(n0, 0)), room));
   const int budget = a.budget;
-  if (tid == 0 && h == 0) {
+  if (tid == 0 && h == 0 && rank_in == 0) {
     a.kv_len_out[b] = min(n, budget);
     if (n != n0 && a.status) atomicOr(a.status, kStatusBadLength);
   }
   float* weights = a.weights + (static_cast<long long>(b) * a.num_kv_heads + h) * a.capacity;
   int32_t* key_pos = a.key_pos + (static_cast<long long>(b) * a.num_kv_heads + h) * a.capacity;
+  const int32_t* table = a.page_table + b * a.table_stride;
   auto position = [&](int j, int held) {  // a key without a position was appended since the last eviction
     return held < 0 ? static_cast<int>(last - (static_cast<long long>(n) - 1 - j)) : held;
   };
-  if (n <= budget) {
-    for (int j0 = tid; j0 < n; j0 += T * kEvictBatch) {
-      int held[kEvictBatch];
-#pragma unroll
-      for (int u = 0; u < kEvictBatch; ++u) held[u] = j0 + u * T < n ? key_pos[j0 + u * T] : 0;
-#pragma unroll
-      for (int u = 0; u < kEvictBatch; ++u)
-        if (held[u] < 0) key_pos[j0 + u * T] = position(j0 + u * T, -1);
-    }
-    return;
-  }
+  const bool over = n > budget;
+  if (over)
+    for (int i = tid; i < min((n + a.page_size - 1) / a.page_size, a.smem_pages); i += T) s_table[i] = __ldg(table + i);
 
-  // ---- the keys' integers, and how often each first digit comes
+  // ---- the keys' integers (of a sequence over its budget), new keys' positions
   const long long newest = static_cast<long long>(last) - a.recent;  // positions above are protected
   auto rank_key = [&](float w, int pos) -> uint32_t {
     if (pos < a.sink || pos > newest) return 0xFFFFFFFFu;
@@ -87,33 +84,34 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     const uint32_t u = __float_as_uint(w + 0.0f);  // (-0 as 0)
     return u >> 31 ? ~u : u | 0x80000000u;
   };
-  const int32_t* table = a.page_table + b * a.table_stride;
-  for (int i = tid; i < min((n + a.page_size - 1) / a.page_size, a.smem_pages); i += T) s_table[i] = __ldg(table + i);
-  __syncthreads();
-  for (int j0 = tid; j0 < n; j0 += T * kEvictBatch) {
-    int held[kEvictBatch];
-    float w[kEvictBatch];
+  __syncthreads();  // the bins are empty
+  for (int j0 = tid; j0 < n; j0 += T * KEYS) {
+    int held[KEYS];
+    float w[KEYS];
 #pragma unroll
-    for (int u = 0; u < kEvictBatch; ++u) {
+    for (int u = 0; u < KEYS; ++u) {
       const bool in = j0 + u * T < n;
       held[u] = in ? key_pos[j0 + u * T] : 0;
-      w[u] = in ? weights[j0 + u * T] : 0.0f;
+      w[u] = in && over ? weights[j0 + u * T] : 0.0f;
     }
 #pragma unroll
-    for (int u = 0; u < kEvictBatch; ++u) {
+    for (int u = 0; u < KEYS; ++u) {
       const int j = j0 + u * T;
       if (j < n) {
         const int pos = position(j, held[u]);
+        if (held[u] < 0 && j < budget && rank_in == 0) key_pos[j] = pos;
         const uint32_t key = rank_key(w[u], pos);
-        if (j < a.smem_keys) s_keys[j] = key;
-        if (held[u] < 0 && j < budget) key_pos[j] = pos;
-        atomicAdd(&sh.bins[key >> 21], 1);
+        if (ALL || j < a.smem_keys) s_keys[j] = key;
+        if (over) atomicAdd(&sh.bins[key >> 21], 1);
       }
     }
   }
-  __syncthreads();
+  if (!over) return;
+  if (a.cluster > 1) cluster_sync_all();  // (and a barrier) before any of the CTAs moves something
+  else __syncthreads();
   auto key_of = [&](int j) -> uint32_t {
-    return j < a.smem_keys ? s_keys[j] : rank_key(weights[j], position(j, key_pos[j]));
+    if (ALL || j < a.smem_keys) return s_keys[j];
+    return rank_key(weights[j], position(j, key_pos[j]));
   };
 
   // Sums over the threads in front of this one, and over all, of two counts.
@@ -138,46 +136,44 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
                      __shfl_sync(0xffffffffu, to.y - w.y, warp) + run.y - mine.y);
   };
 
-  // ---- the budget-th largest: its digits from the top, until all keys with those stay
-  uint32_t least = 0;  // the digits so far; in the end, the least that stays
-  int rank = budget, equal = 0;
-#pragma unroll
-  for (int pass = 0; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-    constexpr int kBinsOf[3] = {2048, 2048, 1024};
-    const int bins = kBinsOf[pass];
+  // ---- the budget-th largest, or a bound below it with as many keys
+  uint32_t least = 0;
+  int rank = budget, equal = 0;  // of the keys equal to it, how many stay, and how many there are
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {  // digits of 11, 11 and 10 bits
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
     if (pass > 0) {
       const int above = pass == 1 ? 21 : 10;
-      for (int j0 = tid; j0 < n; j0 += T * kEvictBatch) {
-        uint32_t key[kEvictBatch];
-#pragma unroll
-        for (int u = 0; u < kEvictBatch; ++u) key[u] = j0 + u * T < n ? key_of(j0 + u * T) : ~least;
-#pragma unroll
-        for (int u = 0; u < kEvictBatch; ++u)
-          if (key[u] >> above == least >> above) atomicAdd(&sh.bins[(key[u] >> shift) & (bins - 1)], 1);
+#pragma unroll 4
+      for (int j = tid; j < n; j += T) {
+        const uint32_t k = key_of(j);
+        if (k >> above == least >> above) atomicAdd(&sh.bins[(k >> shift) & (bins - 1)], 1);
       }
       __syncthreads();
     }
     // each thread has a run of bins, from the top, which it leaves empty
     constexpr int PER = kEvictBins / T;  // 8 or 2
-    int c[PER], sum = 0;
-    int* own = sh.bins + bins - PER - tid * PER;
+    int2 c[PER / 2];
+    int sum = 0;
+    int2* own = reinterpret_cast<int2*>(sh.bins + bins - PER - tid * PER);
     const bool has = tid * PER < bins;
 #pragma unroll
-    for (int i = 0; i < PER; i += 2) {
-      const int2 x = has ? *reinterpret_cast<const int2*>(own + PER - 2 - i) : make_int2(0, 0);
-      c[i] = x.y, c[i + 1] = x.x;
-      if (has) *reinterpret_cast<int2*>(own + PER - 2 - i) = make_int2(0, 0);
-      sum += x.x + x.y;
+    for (int i = 0; i < PER / 2; ++i) {
+      c[i] = has ? own[PER / 2 - 1 - i] : make_int2(0, 0);
+      if (has) own[PER / 2 - 1 - i] = make_int2(0, 0);
+      sum += c[i].x + c[i].y;
     }
     int2 all;
     int seen = sums(make_int2(sum, 0), all).x;
     if (seen < rank && rank <= seen + sum) {  // one thread's
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        if (seen < rank && rank <= seen + c[i])
-          sh.digit = bins - 1 - (tid * PER + i), sh.rank = rank - seen, sh.equal = c[i];
-        seen += c[i];
+      for (int i = 0; i < PER / 2; ++i) {
+        if (seen < rank && rank <= seen + c[i].x + c[i].y) {
+          const bool second = rank > seen + c[i].y;
+          sh.digit = bins - 1 - tid * PER - 2 * i - (second ? 1 : 0);
+          sh.rank = rank - seen - (second ? c[i].y : 0), sh.equal = second ? c[i].x : c[i].y;
+        }
+        seen += c[i].x + c[i].y;
       }
     }
     __syncthreads();
@@ -192,7 +188,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
   if (rank < equal) {
     const int run = (n / T + 1) | 1, j0 = min(tid * run, n), j1 = j0 + min(run, n - j0);
     int count = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int j = j0; j < j1; ++j) count += key_of(j) == least ? 1 : 0;
     int2 all;
     int seen = sums(make_int2(count, 0), all).x;
@@ -212,7 +208,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
   // Of up to 32 keys from j on, those that stay, as bits.
   auto staying = [&](int j, int count) {
     uint32_t bits = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int i = 0; i < count; ++i) bits |= (stays(j + i) ? 1u : 0u) << i;
     return bits;
   };
@@ -239,13 +235,16 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
   const Kv4Pages pages{a.cache, table, a.num_pages, a.num_kv_heads, a.page_size};
   auto block_of = [&](int j) {
     const int pg = j / a.page_size;
-    return pages.block_of_page<D>(pg < a.smem_pages ? s_table[pg] : __ldg(table + pg), j - pg * a.page_size, h);
+    return pages.block_of_page<D>(ALL || pg < a.smem_pages ? s_table[pg] : __ldg(table + pg), j - pg * a.page_size, h);
   };
   bool lost = false;
+  // this CTA's share of the moves
+  const int share = (all.x + a.cluster - 1) / a.cluster, share0 = min(rank_in * share, all.x);
+  const int share1 = min(share0 + share, all.x);
   // where this thread's lists go on: the 32 keys' bits that are left, their first key, the next number
   int hole_j = h0, hole_i = first.x, mover_j = m0, mover_i = first.y;
-  for (int from = 0; from < all.x; from += Shared::kList) {  // the moves [from, from + kList)
-    const int to = min(from + Shared::kList, all.x);
+  for (int from = share0; from < share1; from += Shared::kList) {  // the moves [from, from + kList)
+    const int to = min(from + Shared::kList, share1);
     while (hole_i < to && hole_j < h1) {
       if (hole_bits == 0) {
         hole_j += 32;
@@ -255,7 +254,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
         }
         continue;
       }
-      sh.hole[hole_i++ - from] = hole_j + __ffs(hole_bits) - 1;
+      if (hole_i >= from) sh.hole[hole_i - from] = hole_j + __ffs(hole_bits) - 1;
+      ++hole_i;
       hole_bits &= hole_bits - 1;
     }
     while (mover_i < to && mover_j < m1) {
@@ -264,7 +264,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
         if (mover_j < m1) mover_bits = staying(mover_j, min(m1 - mover_j, 32));
         continue;
       }
-      sh.mover[mover_i++ - from] = mover_j + __ffs(mover_bits) - 1;
+      if (mover_i >= from) sh.mover[mover_i - from] = mover_j + __ffs(mover_bits) - 1;
+      ++mover_i;
       mover_bits &= mover_bits - 1;
     }
     __syncthreads();
@@ -302,18 +303,25 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     }
     __syncthreads();
   }
-  for (int j = budget + tid; j < n; j += T) key_pos[j] = -1;
+  if (a.cluster > 1) cluster_sync_all();  // the movers' positions have been read
+  for (int j = budget + rank_in * T + tid; j < n; j += T * a.cluster) key_pos[j] = -1;
   if (lost && a.status) atomicOr(a.status, kStatusBadSlot);
 }
 
 namespace {
-template <int D, int T>
+template <int D, int T, bool ALL>
 int run_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
-  const void* fn = reinterpret_cast<const void*>(lora_kv4_evict_kernel<D, T>);
+  const void* fn = reinterpret_cast<const void*>(lora_kv4_evict_kernel<D, T, ALL>);
   const size_t smem = sizeof(EvictShared<T>) + (static_cast<size_t>(a.smem_keys) + a.smem_pages) * 4;
   if (ensure_smem_attr(fn, smem) != 0) return -6;
   Kv4EvictArgs p = a;
-  return launch_pdl(fn, dim3(a.num_seqs * a.num_kv_heads), dim3(T), smem, stream, 0, &p);
+  return launch_pdl(fn, dim3(a.num_seqs * a.num_kv_heads * a.cluster), dim3(T), smem, stream,
+                    a.cluster > 1 ? a.cluster : 0, &p);
+}
+template <int D>
+int run_evict(const Kv4EvictArgs& a, int most, cudaStream_t stream) {
+  if (most <= kEvictSmall) return run_evict<D, 256, true>(a, stream);
+  return most <= kEvictKeysMax ? run_evict<D, 1024, true>(a, stream) : run_evict<D, 1024, false>(a, stream);
 }
 }  // namespace
 
@@ -322,9 +330,14 @@ int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
   const int most = static_cast<int>(std::min<long long>(a.capacity, a.table_stride * a.page_size));
   p.smem_keys = std::min(most, kEvictKeysMax);
   p.smem_pages = std::min((most + a.page_size - 1) / a.page_size, kEvictTable);
-  if (most <= kEvictSmall)
-    return a.head_dim == 128 ? run_evict<128, 256>(p, stream) : run_evict<64, 256>(p, stream);
-  return a.head_dim == 128 ? run_evict<128, 1024>(p, stream) : run_evict<64, 1024>(p, stream);
+  const int sms = device_sm_count();
+  if (sms <= 0) return -6;
+  p.cluster = 1;
+  const long long items = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
+  // (integers that are formed again must not see another CTA's moves)
+  if (most > kEvictSmall && most <= kEvictKeysMax)
+    while (p.cluster < 8 && 2 * p.cluster * items <= sms) p.cluster *= 2;
+  return a.head_dim == 128 ? run_evict<128>(p, most, stream) : run_evict<64>(p, most, stream);
 }
 
 }  // namespace grg

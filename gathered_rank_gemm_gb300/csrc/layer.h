@@ -163,6 +163,7 @@ struct Kv4EvictArgs {
   uint32_t* status;
   int smem_keys;  // the launcher's: keys whose integers are kept in shared memory, and pages
   int smem_pages;
+  int cluster;  // CTAs of a head
 };
 int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream);
 

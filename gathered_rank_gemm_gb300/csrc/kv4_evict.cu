@@ -14,6 +14,7 @@
 // CTAs has each: all select, each moves a part.  Integers past what shared memory holds are formed
 // again wherever they are looked at.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv4_move.cuh"
 #include "launch.h"
@@ -23,7 +24,7 @@ namespace grg {
 
 namespace {
 constexpr int kEvictBins = 2048;  // of a digit
-constexpr int kEvictMoves = 4;    // entries that a lane has in flight
+constexpr int kEvictMoves = 2;    // entries that a lane has in flight (4: 42.5 us for 6 prompts, 37.7 with 2)
 constexpr int kEvictSmall = 4096;
 constexpr int kEvictKeysMax = 40960;
 constexpr int kEvictTable = 2560;  // pages whose numbers are kept in shared memory
@@ -33,7 +34,7 @@ struct EvictShared {
   static constexpr int kList = 2 * T;  // holes, and movers, listed at a time
   __align__(16) int bins[kEvictBins];
   int hole[kList], mover[kList];
-  int2 warp_sum[32];
+  int warp_sum[2][32];
   int digit, rank, equal;  // the bin in which the rank falls, the rank within it, its keys
   int cut;
 };
@@ -41,7 +42,7 @@ struct EvictShared {
 
 // ALL: shared memory holds all keys and pages.
 template <int D, int T, bool ALL>
-__global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
+__global__ void __launch_bounds__(T, T == 256 ? 6 : 1)
     lora_kv4_evict_kernel(const __grid_constant__ Kv4EvictArgs a) {
   using Entry = Kv4Entry<D>;
   using Shared = EvictShared<T>;
@@ -77,7 +78,9 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     for (int i = tid; i < min((n + a.page_size - 1) / a.page_size, a.smem_pages); i += T) s_table[i] = __ldg(table + i);
 
   // ---- the keys' integers (of a sequence over its budget), new keys' positions
-  const long long newest = static_cast<long long>(last) - a.recent;  // positions above are protected
+  // positions above are protected (where none reach, down to the least, so are all but that one: a
+  // position there was never given)
+  const int newest = static_cast<int>(max(static_cast<long long>(last) - a.recent, -(1ll << 31)));
   auto rank_key = [&](float w, int pos) -> uint32_t {
     if (pos < a.sink || pos > newest) return 0xFFFFFFFFu;
     if (w != w) return 0u;
@@ -114,26 +117,19 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     return rank_key(weights[j], position(j, key_pos[j]));
   };
 
-  // Sums over the threads in front of this one, and over all, of two counts.
-  auto sums = [&](int2 mine, int2& all) {
-    int2 run = mine;
+  // The sum over the threads in front of this one, and over all.
+  auto sums = [&](int mine, int& all, int* turn) {
+    int run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, run.x, o), y = __shfl_up_sync(0xffffffffu, run.y, o);
-      if (lane >= o) run.x += x, run.y += y;
+      const int x = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += x;
     }
-    if (lane == 31) sh.warp_sum[warp] = run;
+    if (lane == 31) turn[warp] = run;
     __syncthreads();
-    const int2 w = lane < WARPS ? sh.warp_sum[lane] : make_int2(0, 0);
-    int2 to = w;
-#pragma unroll
-    for (int o = 1; o < WARPS; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, to.x, o), y = __shfl_up_sync(0xffffffffu, to.y, o);
-      if (lane >= o) to.x += x, to.y += y;
-    }
-    all = make_int2(__shfl_sync(0xffffffffu, to.x, WARPS - 1), __shfl_sync(0xffffffffu, to.y, WARPS - 1));
-    return make_int2(__shfl_sync(0xffffffffu, to.x - w.x, warp) + run.x - mine.x,
-                     __shfl_sync(0xffffffffu, to.y - w.y, warp) + run.y - mine.y);
+    const int w = lane < WARPS ? turn[lane] : 0;
+    all = __reduce_add_sync(0xffffffffu, w);
+    return __reduce_add_sync(0xffffffffu, lane < warp ? w : 0) + run - mine;
   };
 
   // ---- the budget-th largest, or a bound below it with as many keys
@@ -163,8 +159,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
       if (has) own[PER / 2 - 1 - i] = make_int2(0, 0);
       sum += c[i].x + c[i].y;
     }
-    int2 all;
-    int seen = sums(make_int2(sum, 0), all).x;
+    int all;
+    int seen = sums(sum, all, sh.warp_sum[0]);
     if (seen < rank && rank <= seen + sum) {  // one thread's
 #pragma unroll
       for (int i = 0; i < PER / 2; ++i) {
@@ -190,8 +186,8 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     int count = 0;
 #pragma unroll 4
     for (int j = j0; j < j1; ++j) count += key_of(j) == least ? 1 : 0;
-    int2 all;
-    int seen = sums(make_int2(count, 0), all).x;
+    int all;
+    int seen = sums(count, all, sh.warp_sum[0]);
     if (seen < rank && rank <= seen + count)
       for (int j = j0; j < j1; ++j)
         if (key_of(j) == least && ++seen == rank) {
@@ -217,32 +213,32 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
   const int hrun = (budget / T + 1) | 1, h0 = min(tid * hrun, budget), h1 = h0 + min(hrun, budget - h0);
   const int mrun = ((n - budget) / T + 1) | 1;
   const int m0 = budget + min(tid * mrun, n - budget), m1 = m0 + min(mrun, n - m0);
-  int2 count = make_int2(0, 0), all;
+  int holes = 0, movers = 0, all;
   uint32_t hole_bits = 0, mover_bits = 0;  // those of the first 32 keys of a run
   for (int j = h0; j < h1; j += 32) {
     const int some = min(h1 - j, 32);
     const uint32_t bits = staying(j, some) ^ (some == 32 ? ~0u : (1u << some) - 1u);
     if (j == h0) hole_bits = bits;
-    count.x += __popc(bits);
+    holes += __popc(bits);
   }
   for (int j = m0; j < m1; j += 32) {
     const uint32_t bits = staying(j, min(m1 - j, 32));
     if (j == m0) mover_bits = bits;
-    count.y += __popc(bits);
+    movers += __popc(bits);
   }
-  const int2 first = sums(count, all);
+  const int first_mover = sums(movers, all, sh.warp_sum[1]), first_hole = sums(holes, all, sh.warp_sum[0]);
 
   const Kv4Pages pages{a.cache, table, a.num_pages, a.num_kv_heads, a.page_size};
   auto block_of = [&](int j) {
-    const int pg = j / a.page_size;
+    const int pg = static_cast<int>((static_cast<unsigned long long>(j >> 4) * a.page_magic) >> 36);
     return pages.block_of_page<D>(ALL || pg < a.smem_pages ? s_table[pg] : __ldg(table + pg), j - pg * a.page_size, h);
   };
   bool lost = false;
   // this CTA's share of the moves
-  const int share = (all.x + a.cluster - 1) / a.cluster, share0 = min(rank_in * share, all.x);
-  const int share1 = min(share0 + share, all.x);
+  const int share = (all + a.cluster - 1) / a.cluster, share0 = min(rank_in * share, all);
+  const int share1 = min(share0 + share, all);
   // where this thread's lists go on: the 32 keys' bits that are left, their first key, the next number
-  int hole_j = h0, hole_i = first.x, mover_j = m0, mover_i = first.y;
+  int hole_j = h0, hole_i = first_hole, mover_j = m0, mover_i = first_mover;
   for (int from = share0; from < share1; from += Shared::kList) {  // the moves [from, from + kList)
     const int to = min(from + Shared::kList, share1);
     while (hole_i < to && hole_j < h1) {
@@ -271,25 +267,26 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
     __syncthreads();
     constexpr int EACH = T / LANES;
     const int part = tid % LANES;
-    for (int i0 = tid / LANES; i0 < to - from; i0 += kEvictMoves * EACH) {
-      Entry e[kEvictMoves];
-      uint32_t state[kEvictMoves];  // lane 0: the weight, lane 1: the position
-      uint8_t* source[kEvictMoves];
-      int j[kEvictMoves];
+    auto move = [&](auto several, int i0) {  // that many entries in flight per lane
+      constexpr int MOVES = decltype(several)::value;
+      Entry e[MOVES];
+      uint32_t state[MOVES];  // lane 0: the weight, lane 1: the position
+      uint8_t* source[MOVES];
+      int j[MOVES];
 #pragma unroll
-      for (int u = 0; u < kEvictMoves; ++u) {
+      for (int u = 0; u < MOVES; ++u) {
         j[u] = sh.mover[min(i0 + u * EACH, to - from - 1)];
         source[u] = block_of(j[u]);
       }
 #pragma unroll
-      for (int u = 0; u < kEvictMoves; ++u) {
+      for (int u = 0; u < MOVES; ++u) {
         if (source[u]) e[u].load(source[u], j[u] % 16, part);
         if (part < 2)
           asm volatile("ld.global.u32 %0, [%1];\n" : "=r"(state[u])
                        : "l"(part == 0 ? static_cast<const void*>(weights + j[u]) : static_cast<const void*>(key_pos + j[u])));
       }
 #pragma unroll
-      for (int u = 0; u < kEvictMoves; ++u) {
+      for (int u = 0; u < MOVES; ++u) {
         const int i = i0 + u * EACH;
         if (i < to - from) {
           const int to_j = sh.hole[i];
@@ -299,6 +296,15 @@ __global__ void __launch_bounds__(T, T == 256 ? 4 : 1)
           if (part == 0) weights[to_j] = __uint_as_float(state[u]);
           if (part == 1) key_pos[to_j] = position(j[u], static_cast<int>(state[u]));
         }
+      }
+    };
+    for (int i0 = tid / LANES; i0 < to - from;) {
+      if (to - from - i0 > EACH) {
+        move(std::integral_constant<int, kEvictMoves>(), i0);
+        i0 += kEvictMoves * EACH;
+      } else {
+        move(std::integral_constant<int, 1>(), i0);
+        i0 += EACH;
       }
     }
     __syncthreads();
@@ -332,6 +338,8 @@ int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
   p.smem_pages = std::min((most + a.page_size - 1) / a.page_size, kEvictTable);
   const int sms = device_sm_count();
   if (sms <= 0) return -6;
+  const unsigned long long page_blocks = a.page_size / 16;
+  p.page_magic = ((1ull << 36) + page_blocks - 1) / page_blocks;
   p.cluster = 1;
   const long long items = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
   // (integers that are formed again must not see another CTA's moves)

@@ -164,6 +164,7 @@ struct Kv4EvictArgs {
   int smem_keys;  // the launcher's: keys whose integers are kept in shared memory, and pages
   int smem_pages;
   int cluster;  // CTAs of a head
+  unsigned long long page_magic;  // ceil(2^36 / blocks of a page)
 };
 int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream);
 

@@ -201,6 +201,7 @@ int kv4_attention(const uint16_t* q, int64_t q_row_stride, uint16_t* out, int64_
   a.window = static_cast<int>(window);
   a.tree_mask = tree_mask;
   a.tree_words = tree_words;
+  a.short_rows = a.short_keys = 0;
   a.workspace = workspace;
   a.status = status;
   return grg::launch_kv4_attention(a, f16, static_cast<cudaStream_t>(stream));

@@ -31,6 +31,13 @@ struct Kv4Seq {
     return window > 0 && at >= window ? at - window + 1 : 0;
   }
 
+  // Whether the decode kernel takes the sequence: few packed rows, or a short tree.
+  template <bool TREE>
+  __device__ __forceinline__ bool few(const Kv4AttnArgs& a, int group, int max_packed_rows) const {
+    const long long packed = static_cast<long long>(take) * group;
+    return packed <= max_packed_rows || (TREE && packed <= a.short_rows && kv <= a.short_keys);
+  }
+
   // Which keys rows see.  A row of a sequence sees a run of keys that ends at its own
   // position; a row of a tree (TREE) those in front of all rows' own, from its window's
   // first on, and of the rows' own what its mask names.

@@ -197,8 +197,7 @@ __global__ void __launch_bounds__(DecShape<D, NT, ONE>::kWarps * 32, DecShape<D,
   const int per_thread = (a.num_seqs + kDecThreads - 1) / kDecThreads;
   auto seq_at = [&](int b) { return per_thread == 1 ? s_seq[b] : Kv4Seq::of(a, b); };
   auto groups_of = [&](const Kv4Seq& s) {  // row groups; 0: no rows, or not this kernel's
-    return static_cast<long long>(s.take) * group > p.max_packed_rows ? 0
-                                                                      : (s.take * group + ROWS - 1) / ROWS;
+    return s.few<TREE>(a, group, p.max_packed_rows) ? (s.take * group + ROWS - 1) / ROWS : 0;
   };
   auto units_of = [&](const Kv4Seq& s, int& most) {  // of one key head
     long long n = 0;

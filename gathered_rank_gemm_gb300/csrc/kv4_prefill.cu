@@ -1,4 +1,6 @@
 // The prefill attention of causal rows (kv4_prefill.cuh), and which kernel takes what.
+#include <algorithm>
+
 #include "kv4_prefill.cuh"
 
 namespace grg {
@@ -11,6 +13,14 @@ namespace {
 // packed rows of 128 110 and 131 us, with 64 186 and 131 us; 16 of 2000 with 48 rows 55.1
 // and 48.0 us.
 constexpr int kDecodeRows = 32;
+// Trees of few sequences go by the decode kernel up to kTreeRows packed rows, where every group of
+// 16 rows and every key head has an SM of its own and the keys of all groups together are at most
+// kTreeWork (kTreeWork64 for heads of 64): one tree of 15 rows, 32 / 8
+// heads of 128, over 700 keys 11.6 us, 21.6 us by the prefill kernel; over 32000 55.6 and 66.0; over
+// 64000 88.9 and 85.2; four trees (128 groups) over 6000 keys 38.8 and 42.4, over 8000 48.7 and 46.9;
+// heads of 64, 128 groups over 700 keys 11.2 and 16.7, over 4000 30.6 and 24.2.
+constexpr int kTreeRows = 256;  // (the decode kernel's division of packed rows)
+constexpr long long kTreeWork = 800000, kTreeWork64 = 300000;
 
 long long packed_bound(long long max_q_len, int num_q_heads, int num_kv_heads) {
   return max_q_len * (num_q_heads / num_kv_heads);
@@ -47,7 +57,15 @@ int launch_both(const Kv4AttnArgs& a, bool f16, cudaStream_t stream) {
 }  // namespace
 
 int launch_kv4_attention(const Kv4AttnArgs& a, bool f16, cudaStream_t stream) {
-  return a.tree_mask ? launch_both<true>(a, f16, stream) : launch_both<false>(a, f16, stream);
+  if (!a.tree_mask) return launch_both<false>(a, f16, stream);
+  Kv4AttnArgs b = a;
+  const long long packed = packed_bound(a.max_q_len, a.num_q_heads, a.num_kv_heads);
+  const long long items = (std::min<long long>(packed, kTreeRows) + 15) / 16 * a.num_seqs * a.num_kv_heads;
+  b.short_rows = items <= device_sm_count() ? kTreeRows : 0;
+  b.short_keys = static_cast<int>((a.head_dim == 64 ? kTreeWork64 : kTreeWork) / items);
+  if (packed <= b.short_rows && a.table_stride * a.page_size <= b.short_keys)
+    return launch_kv4_decode<true>(b, kDecodeRows, kPreCounterBytes, f16, stream);
+  return launch_both<true>(b, f16, stream);
 }
 
 }  // namespace grg

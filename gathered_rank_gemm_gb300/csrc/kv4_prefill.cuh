@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   int group_lanes = 1;
   while (group_lanes < 32 && 2 * group_lanes * a.num_seqs <= kPreThreads) group_lanes *= 2;
   auto mine_of = [&](const Kv4Seq& s) {
-    return s.take * group > p.max_packed_rows;
+    return !s.few<TREE>(a, group, p.max_packed_rows);
   };
   auto tiles_of = [&](const Kv4Seq& s) {
     return (s.take * group + kPreRows - 1) / kPreRows;
@@ -902,15 +902,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const int page_blocks = a.page_size / 16;
       const long long page_bytes = static_cast<long long>(a.num_kv_heads) * page_blocks * B::kBytes;
       uint32_t tiles = 0;  // two bits for this key tile, two for the next
-      int page = -1, in_page = 0;  // of this thread's key in the tile looked up last; -2: no such key
+      int page = -1, in_page = -1;  // of this thread's key in the tile looked up last; in_page -1: no such key
       auto look_up = [&](int shift) -> bool {  // tile wj of part w; then on to the next
-        page = -2;
+        in_page = -1;
         if (!more) return false;
         tiles |= (live_rows(w) > 128 ? 3u : 1u) << shift;
         const int key = (w.item.kt0() + w.o + wj) * kPreKeys + r;
         if (key >= w.item.lo && key < w.item.hi) {  // (pages in front of the window may be gone)
           const int pg = key / a.page_size, in = key - pg * a.page_size;
-          page = max(__ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride + pg), -1);
+          page = __ldg(a.page_table + static_cast<long long>(w.b) * a.table_stride + pg);
           in_page = (w.h * page_blocks + in / 16) * B::kBytes;
         }
         if (++wj == w.take) {
@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         return true;
       };
       auto block = [&]() -> const uint8_t* {  // of the key looked up last
-        if (page == -2) return nullptr;
+        if (in_page < 0) return nullptr;
         if (page < 0 || page >= a.num_pages) {
           if (a.status) atomicOr(a.status, kStatusBadSlot);
           return nullptr;

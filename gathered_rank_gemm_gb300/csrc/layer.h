@@ -88,6 +88,8 @@ struct Kv4AttnArgs {
   int window;  // 0: none
   const uint32_t* tree_mask;  // [max_num_tokens][tree_words], null for causal rows
   int tree_words;
+  int short_rows;  // trees of up to so many packed rows over up to so many keys go by the decode kernel
+  int short_keys;
   void* workspace;
   uint32_t* status;
 };

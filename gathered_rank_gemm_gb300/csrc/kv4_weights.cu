@@ -16,6 +16,10 @@ namespace grg {
 namespace {
 constexpr int kWtsWarps = 8, kWtsThreads = kWtsWarps * 32;
 constexpr int kWtsBatch = 4;  // blocks whose codes are asked for together
+// CTAs of an SM (256 sequences of up to 4096 keys, heads of 128: 89 us by two of 4 blocks, 110 us of 2,
+// 102 us by three; of 64: 73 us by two, 66 us by three).
+template <int D>
+constexpr int kWtsCtas = D == 64 ? 3 : 2;
 constexpr float kWtsLog2e = 1.4426950408889634f;
 
 struct WtsParams {
@@ -35,7 +39,7 @@ __device__ __forceinline__ uint32_t wts_both(uint32_t a, bool high) {
 }  // namespace
 
 template <int D, int NT, bool F16>
-__global__ void __launch_bounds__(kWtsThreads, 2)
+__global__ void __launch_bounds__(kWtsThreads, kWtsCtas<D>)
     lora_kv4_weights_kernel(const __grid_constant__ WtsParams p) {
   using B = Kv4Block<D>;
   constexpr int KS = D / 16, ROWS = 8 * NT, W = D / 32;  // W: words of a thread's codes of a key
@@ -283,7 +287,7 @@ int run_weights(const WtsParams& q, bool wide, cudaStream_t stream) {
                         : reinterpret_cast<const void*>(lora_kv4_weights_kernel<D, 1, F16>);
   const int sms = device_sm_count();
   if (sms <= 0) return -6;
-  return launch_pdl(fn, dim3(2 * sms), dim3(kWtsThreads), 0, stream, 0, &p);
+  return launch_pdl(fn, dim3(kWtsCtas<D> * sms), dim3(kWtsThreads), 0, stream, 0, &p);
 }
 }  // namespace
 
@@ -293,12 +297,11 @@ constexpr int kFewRows = 32;
 
 int launch_kv4_weights(const Kv4WeightsArgs& a, bool f16, cudaStream_t stream) {
   const long long packed = static_cast<long long>(a.max_q_len) * (a.num_q_heads / a.num_kv_heads);
-  const bool wide = packed > 8;
   WtsParams p;
   p.a = a;
   p.max_packed_rows = kFewRows;
-  const int rc = a.head_dim == 64 ? (f16 ? run_weights<64, true>(p, wide, stream) : run_weights<64, false>(p, wide, stream))
-                                  : (f16 ? run_weights<128, true>(p, wide, stream) : run_weights<128, false>(p, wide, stream));
+  const int rc = a.head_dim == 64 ? (f16 ? run_weights<64, true>(p, packed > 8, stream) : run_weights<64, false>(p, packed > 8, stream))
+                                  : (f16 ? run_weights<128, true>(p, packed > 8, stream) : run_weights<128, false>(p, packed > 8, stream));
   return rc == 0 && packed > kFewRows ? launch_kv4_weights_tc(a, kFewRows, f16, stream) : rc;
 }
 

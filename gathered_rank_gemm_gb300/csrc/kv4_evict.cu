@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(T, T == 256 ? 6 : 1)
   int32_t* key_pos = a.key_pos + (static_cast<long long>(b) * a.num_kv_heads + h) * a.capacity;
   const int32_t* table = a.page_table + b * a.table_stride;
   auto position = [&](int j, int held) {  // a key without a position was appended since the last eviction
-    return held < 0 ? static_cast<int>(last - (static_cast<long long>(n) - 1 - j)) : held;
+    return held < 0 ? static_cast<int>(static_cast<uint32_t>(last) - static_cast<uint32_t>(n - 1 - j)) : held;
   };
   const bool over = n > budget;
   if (over)

@@ -822,6 +822,40 @@ def test_a_step_of_a_server_under_a_graph():
     assert evicted > 10
 
 
+@pytest.mark.parametrize("rows", [3, 100])
+def test_a_tree_attention_that_gives_up_says_so_and_the_next_is_whole(rows):
+    c = _tree_case([(rows, 900), (2, 300)], 8, 2, 128, 16, "bf16", seed=40)
+    status = _status()
+    assert B.lora_testing_inject_timeout(True) is False
+    try:
+        ws = _tree(c, status=status)
+        torch.cuda.synchronize()
+    finally:
+        assert B.lora_testing_inject_timeout(False) is True
+    assert B.lora_read_status(status) == B.LORA_STATUS_TIMEOUT
+    assert (c["out"] == 7).all()
+    _tree(c, workspace=ws, status=status)
+    _tree_check(c, some=30)
+    assert B.lora_read_status(status) == 0
+
+
+@pytest.mark.parametrize("paths", [False, True])
+def test_key_weights_that_give_up_say_so_and_the_next_are_whole(paths):
+    c = _weights_case([(60, 900), (300, 700)], 8, 2, 128, 16, "bf16", seed=41, paths=paths)
+    status = _status()
+    assert B.lora_testing_inject_timeout(True) is False
+    try:
+        _weights(c, status=status)
+        torch.cuda.synchronize()
+    finally:
+        assert B.lora_testing_inject_timeout(False) is True
+    assert B.lora_read_status(status) == B.LORA_STATUS_TIMEOUT
+    assert np.array_equal(c["w"].cpu().numpy(), c["w_np"])
+    _weights(c, status=status)
+    _weights_check(c)
+    assert B.lora_read_status(status) == 0
+
+
 def test_two_streams():
     """Calls on two streams at once, and on a stream given by its handle: each has its own results."""
     one, two = (_weights_case([(1, 3000), (60, 500)], 8, 2, 128, 16, "bf16", seed=s) for s in (97, 98))

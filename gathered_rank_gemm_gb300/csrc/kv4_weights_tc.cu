@@ -72,8 +72,9 @@ struct TcShared {
     int b, kt, row0, rows, q0, q_rows, seq_rows, kv, end;
   } pair[kTcPairs];
   int sorted[kTcPairs];
-  __align__(16) int load[kTcCtasMax];
-  int dealt[kTcDeal];  // row tiles of each CTA so far; this one's items
+  uint32_t order[kTcPairs];
+  __align__(16) int load[kTcCtasMax];  // row tiles of each CTA so far, and its number in the low 8 bits
+  int dealt[kTcDeal];                  // this CTA's items
 };
 
 // An item: its keys [256 kt, ...) and the packed rows [row0, row0 + rows) that see one of them.
@@ -243,7 +244,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   if (tid < kTcLine) sh.prefix[tid] = before + run - mine;
   static_assert(4 * kTcCtasMax <= kTcThreads && kTcCtasMax % 16 == 0, "four lanes a CTA, in whole warps");
-  if (tid < kTcCtasMax) sh.load[tid] = tid < static_cast<int>(gridDim.x) ? 0 : 0x7fffffff;
+  if (tid < kTcCtasMax) sh.load[tid] = tid < static_cast<int>(gridDim.x) ? tid : 0x7fffffff;
   const long long items = pairs * a.num_kv_heads, G = gridDim.x;
   const bool sorted = pairs <= kTcPairs && items <= kTcDeal * G;
   __syncthreads();
@@ -265,19 +266,28 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   };
   if (sorted) {
     TcItem it;
+    it.rows = 0;
     if (tid < pairs) {
       pair_of(tid, it);
       sh.pair[tid] = {it.b, it.kt, it.row0, it.rows, it.seq.q0, it.seq.q_rows, it.seq.rows, it.seq.kv, it.seq.end};
     }
     __syncthreads();
-    if (tid < pairs) {  // a pair's place: those of more rows first, then in their own order
+    // a pair's place: those of more row tiles first, then in their own order (both in one number;
+    // four lanes count a pair's place where there are threads for it)
+    if (tid < kTcPairs)
+      sh.order[tid] = tid < pairs ? static_cast<uint32_t>(min((it.rows + R - 1) / R, 1 << 21)) << 9 | (kTcPairs - 1 - tid) : 0u;
+    __syncthreads();
+    const int lanes = 4 * pairs <= kTcThreads ? 4 : 1, own_pair = tid / lanes;
+    if (own_pair < (static_cast<int>(pairs) + 31) / 32 * 32) {  // (whole warps)
+      const uint32_t own = sh.order[min(own_pair, kTcPairs - 1)];
       int place = 0;
 #pragma unroll 4
-      for (int i = 0; i < static_cast<int>(pairs); ++i) {
-        const int m = sh.pair[i].rows;
-        place += m > it.rows || (m == it.rows && i < tid) ? 1 : 0;
+      for (int i = tid & (lanes - 1); i < static_cast<int>(pairs); i += lanes) place += sh.order[i] > own ? 1 : 0;
+      if (lanes == 4) {
+        place += __shfl_xor_sync(0xffffffffu, place, 1);
+        place += __shfl_xor_sync(0xffffffffu, place, 2);
       }
-      sh.sorted[place] = tid;
+      if (own_pair < pairs && (tid & (lanes - 1)) == 0) sh.sorted[place] = own_pair;
     }
     __syncthreads();
     // Rounds: the CTA with the least so far takes the round's largest item, and so on.  (6 chunks of
@@ -291,19 +301,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll 5
         for (int i = 4 * (tid & 3); i < kTcCtasMax; i += 16) {  // (CTAs that are not there count as full)
           const int4 x = *reinterpret_cast<const int4*>(sh.load + i);
-          rank += (x.x < own || (x.x == own && i < cta) ? 1 : 0) + (x.y < own || (x.y == own && i + 1 < cta) ? 1 : 0) +
-                  (x.z < own || (x.z == own && i + 2 < cta) ? 1 : 0) + (x.w < own || (x.w == own && i + 3 < cta) ? 1 : 0);
+          rank += (x.x < own ? 1 : 0) + (x.y < own ? 1 : 0) + (x.z < own ? 1 : 0) + (x.w < own ? 1 : 0);
         }
         rank += __shfl_xor_sync(0xffffffffu, rank, 1);
         rank += __shfl_xor_sync(0xffffffffu, rank, 2);
         const long long e = k * G + rank;
         const bool has = cta < G && e < items;
         if (has && (tid & 3) == 0)
-          size = (sh.pair[sh.sorted[static_cast<int>(e) / a.num_kv_heads]].rows + R - 1) / R + kTcFixed;
+          size = min((sh.pair[sh.sorted[static_cast<int>(e) / a.num_kv_heads]].rows + R - 1) / R + kTcFixed, 1 << 18);
         if ((tid & 3) == 0 && cta == blockIdx.x) sh.dealt[k] = has ? static_cast<int>(e) : -1;
       }
       __syncthreads();
-      if ((tid & 3) == 0 && cta < kTcCtasMax) sh.load[cta] += size;
+      if ((tid & 3) == 0 && cta < kTcCtasMax) sh.load[cta] += size << 8;
       __syncthreads();
     }
   }

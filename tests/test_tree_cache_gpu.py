@@ -179,6 +179,15 @@ def test_tree_attention_over_long_keys(lengths):
         assert torch.equal(c["out"], first[0]) and torch.equal(c["lse"], first[1])
 
 
+@pytest.mark.parametrize("window", [0, 400])
+def test_trees_that_go_by_either_kernel(window):
+    """Few sequences, in a table with room for many keys: short ones, long ones and single rows, each by the
+    kernel that its own length calls for."""
+    c = _tree_case([(40, 300), (1, 30000), (40, 30000), (3, 5000), (0, 9), (37, 40)], 4, 1, 128, 64, "bf16", seed=21)
+    _tree(c, window)
+    _tree_check(c, window, some=8)
+
+
 def test_tree_attention_of_many_sequences_and_strided_rows():
     rng = np.random.default_rng(18)
     lengths = [(int(rng.integers(0, 20)), int(rng.integers(0, 90))) for _ in range(400)]
@@ -662,6 +671,81 @@ def test_evict_of_what_only_the_data_shows():
         c["last_np"], c["last"] = [last], _i32([last])
         _evict(c, 50, 5, 20)
         assert c["out"].tolist() == [50]
+
+
+# ------------------------------------------------------------------ sizes at the ends
+
+HEADS = [  # (q heads, key heads): packed rows that fill no tile, or more heads than a tile has rows
+    (100, 1), (130, 1), (256, 1), (14, 2), (128, 128)]
+
+
+@pytest.mark.parametrize("qh,kvh", HEADS)
+def test_tree_attention_of_many_heads(qh, kvh):
+    c = _tree_case([(1, 60), (3, 200), (9, 30)], qh, kvh, 64, 16, "bf16", seed=qh)
+    _tree(c)
+    _tree_check(c)
+
+
+@pytest.mark.parametrize("paths", [False, True])
+@pytest.mark.parametrize("qh,kvh", HEADS)
+def test_key_weights_of_many_heads(qh, kvh, paths):
+    c = _weights_case([(1, 60), (3, 600), (9, 30), (40, 300)], qh, kvh, 64, 16, "bf16", seed=qh, paths=paths)
+    _weights(c)
+    _weights_check(c)
+
+
+@pytest.mark.parametrize("seqs", [1500, 3000])
+def test_many_sequences(seqs):
+    """Of every operator, more sequences than a CTA has threads."""
+    rng = np.random.default_rng(seqs)
+    lengths = [(int(rng.integers(0, 9)), int(rng.integers(0, 40))) for _ in range(seqs)]
+    lengths[1] = (45, 60)
+    c = _tree_case(lengths, 2, 1, 64, 16, "bf16", seed=seqs)
+    _tree(c)
+    _tree_check(c)
+    c = _weights_case(lengths, 2, 1, 64, 16, "bf16", seed=seqs)
+    _weights(c)
+    _weights_check(c)
+    c = _evict_case([n for _, n in lengths], 1, 64, 16, seed=seqs)
+    _evict(c, 17, 1, 3)
+    assert _evict_check(c, 17, 1, 3) > seqs
+    paths = [[int(x) for x in rng.permutation(m)[:rng.integers(0, m + 1)]] for m, _ in lengths]
+    c = _path_case(paths, 2, 64, 16, [m for m, _ in lengths], [m + n for m, n in lengths], seed=seqs)
+    _accept(c)
+    _accept_check(c)
+
+
+def test_pages_past_four_gigabytes():
+    """The same work on the last pages of a cache whose offsets pass 32 bits: the same bits."""
+    far = 62000
+    big = torch.empty(far + 300, 8, 4, 18 * 128, dtype=torch.uint8, device="cuda")
+    assert far * big[0].numel() > 1 << 32
+    t = _tree_case([(5, 700), (60, 900)], 16, 8, 128, 64, "bf16", seed=1)
+    w = _weights_case([(5, 700), (60, 900), (1, 300)], 16, 8, 128, 64, "bf16", seed=2)
+    a = _path_case([[1, 3], list(range(5, 45)), [3, 2, 1]], 8, 128, 64, [5, 60, 4], [700, 900, 100], seed=3)
+    e = _evict_case([700, 5000], 8, 128, 64, seed=4)
+
+    def moved(c):
+        pages = c["cache"].shape[0]
+        big[far:far + pages] = c["cache"]
+        return {**c, "cache": big, "table": torch.where(c["table"] >= 0, c["table"] + far, c["table"])}, slice(far, far + pages)
+
+    _tree(t)
+    want = t["out"].clone()
+    t["out"].fill_(7)
+    _tree(moved(t)[0])
+    assert torch.equal(t["out"], want)
+    _weights(w)
+    want = w["w"].clone()
+    w["w"].copy_(torch.tensor(w["w_np"]))
+    _weights(moved(w)[0])
+    assert torch.equal(w["w"], want)
+    m, at = moved(a)
+    _accept(m)
+    _accept_check({**a, "cache": big[at]})
+    m, at = moved(e)
+    _evict(m, 600, 4, 50)
+    _evict_check({**e, "cache": big[at]}, 600, 4, 50)
 
 
 # ------------------------------------------------------------------ the wrappers' refusals

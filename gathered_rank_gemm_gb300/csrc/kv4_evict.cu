@@ -9,10 +9,15 @@
 // move an entry.  Integers throughout: the result is exact and does not depend on timing.
 //
 // The budget-th largest is found by counting digits of 11, 11 and 10 bits from the top (a radix
-// selection), until all keys with the digits so far stay.  A CTA of 256 threads has a head of up
-// to kEvictSmall keys, of 1024 beyond; where there are fewer such heads than SMs, a cluster of
-// CTAs has each: all select, each moves a part.  Integers past what shared memory holds are formed
-// again wherever they are looked at.
+// selection), until all keys with the digits so far stay.  A CTA has a head; where heads are few and
+// many keys may move, a cluster of CTAs has it: all select, each moves a part.  Integers past what
+// shared memory holds are formed again wherever they are looked at.
+//
+// What bounds it: steps that follow one another, each with a barrier or a trip to memory (the
+// weights, three counts, two sums, rounds of moves), not bytes: 2048 heads of 2000 to 2100 keys,
+// budget 2048, take 34 us, where reading weights and positions once would take 5; 48 heads of 10000
+// to 30000 keys, budget 2000, 38 us.  Hence the threads of a CTA: many where a head has an SM to
+// itself, few where other heads fill the waits.
 #include <algorithm>
 #include <type_traits>
 
@@ -25,7 +30,9 @@ namespace grg {
 namespace {
 constexpr int kEvictBins = 2048;  // of a digit
 constexpr int kEvictMoves = 2;    // entries that a lane has in flight (4: 42.5 us for 6 prompts, 37.7 with 2)
-constexpr int kEvictSmall = 4096;
+constexpr int kEvictShort = 2048;  // keys of a head
+constexpr int kEvictLong = 16384;
+constexpr int kEvictCluster = 512;  // keys that move
 constexpr int kEvictKeysMax = 40960;
 constexpr int kEvictTable = 2560;  // pages whose numbers are kept in shared memory
 
@@ -42,7 +49,7 @@ struct EvictShared {
 
 // ALL: shared memory holds all keys and pages.
 template <int D, int T, bool ALL>
-__global__ void __launch_bounds__(T, T == 256 ? 6 : 1)
+__global__ void __launch_bounds__(T, T == 256 ? 6 : T == 512 ? 3 : 1)
     lora_kv4_evict_kernel(const __grid_constant__ Kv4EvictArgs a) {
   using Entry = Kv4Entry<D>;
   using Shared = EvictShared<T>;
@@ -325,8 +332,9 @@ int run_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
                     a.cluster > 1 ? a.cluster : 0, &p);
 }
 template <int D>
-int run_evict(const Kv4EvictArgs& a, int most, cudaStream_t stream) {
-  if (most <= kEvictSmall) return run_evict<D, 256, true>(a, stream);
+int run_evict(const Kv4EvictArgs& a, int threads, int most, cudaStream_t stream) {
+  if (threads == 256) return run_evict<D, 256, true>(a, stream);
+  if (threads == 512) return run_evict<D, 512, true>(a, stream);
   return most <= kEvictKeysMax ? run_evict<D, 1024, true>(a, stream) : run_evict<D, 1024, false>(a, stream);
 }
 }  // namespace
@@ -342,10 +350,27 @@ int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
   p.page_magic = ((1ull << 36) + page_blocks - 1) / page_blocks;
   p.cluster = 1;
   const long long items = static_cast<long long>(a.num_seqs) * a.num_kv_heads;
+  const int moves = std::min(a.budget, most - std::min(a.budget, most));  // of a head, at most
+  // Measured, us by CTAs of 256 / 512 / 1024 threads (keys = budget + those that go):
+  //   8 heads of 1000 + 24 keys 9.0 / 8.5 / 9.2, of 500 + 3500 17.1 / 12.1 / 11.5
+  //   152 heads of 4096 + 104 17.7 / 13.0 / 11.4; 304 of them 21.2 / 16.8 / 21.3
+  //   304 heads of 2000 + 6000 30.5 / 23.1 / 28.4; 608 heads of 2000 + 100 21.8 / 26.8 / 38.1
+  //   608 heads of 8192 + 100 40.0 / 44.8 / 54.5; of 20000 + 200 (one or two CTAs an SM) 122 / - / 81
+  // Clusters against none: 8 heads of 2000 + 28000 keys 22.8 (eight CTAs) and 31.7, 48 heads of
+  // them 37.8 (two) and 43.8, 8 heads of 4096 + 4 11.4 and 10.1.
+  int threads = 1024;
+  if (most <= kEvictLong) {
+    if (items > 3ll * sms) {
+      threads = 256;
+    } else if (items > sms || most <= kEvictShort) {
+      threads = 512;
+    }
+  }
   // (integers that are formed again must not see another CTA's moves)
-  if (most > kEvictSmall && most <= kEvictKeysMax)
+  if (threads == 1024 && moves >= kEvictCluster && most <= kEvictKeysMax)
     while (p.cluster < 8 && 2 * p.cluster * items <= sms) p.cluster *= 2;
-  return a.head_dim == 128 ? run_evict<128>(p, most, stream) : run_evict<64>(p, most, stream);
+  return a.head_dim == 128 ? run_evict<128>(p, threads, most, stream)
+                           : run_evict<64>(p, threads, most, stream);
 }
 
 }  // namespace grg

@@ -25,7 +25,7 @@
 // of its CTAs to finish (as in kv4_decode.cuh).  Short items stay whole.
 //
 // Measured (GB300, bf16): 6 chunks of 700 to 2000 rows over 2000 to 5000 keys, 32 / 8
-// heads of 128: 319 us, 1080 TFLOP/s (0.56 of measured), fp16 304 us; heads of 64 264 and
+// heads of 128: 314 us, 1095 TFLOP/s (0.57 of measured), fp16 304 us; heads of 64 264 and
 // 257 us; one prompt of 8192 tokens, 32 / 32 heads of 128: 462 us, 1190 TFLOP/s.  Bound by
 // the chain softmax (1400 cycles a tile of
 // 128 x 128), barrier and issue, two products (1024 at the tensor core's rate): 3390
@@ -35,7 +35,9 @@
 // row (96 registers) took 361 us.  An item's start and end cost about five key tiles.
 //
 // TREE (rows that see what their masks name) differs where tiles are masked: a thread's row
-// takes 32 keys' bits from its mask.
+// takes 32 keys' bits from its mask.  32 trees of 64 rows over up to 4000 keys, 32 / 8 heads of 128: 100
+// us; 2 of 60 over up to 100000, 32 / 32 heads: 387 us.  Trees pack to one or two row tiles, so that
+// the warps that widen keys (2600 to 3000 cycles a tile of 128) are what most wait for, not the products.
 #pragma once
 
 #include "kv4_attention.cuh"

@@ -532,6 +532,24 @@ def test_key_weights_of_rows_without_lse_and_of_nan(rows):
     assert not got[0].any() and got[1, :at + 1].all() and not got[1, at + 1:].any()
 
 
+@pytest.mark.parametrize("paths", [None, True])
+@pytest.mark.parametrize("lengths", [[(5, 200), (4, 90), (7, 60)], [(90, 300), (70, 200), (131, 140)]])
+def test_key_weights_of_a_sequence_beside_rows_of_nan(lengths, paths):
+    """Another sequence's rows, those off the path, and those of no sequence may hold anything."""
+    c = _weights_case(lengths, 6, 2, 64, 16, "bf16", seed=96, paths=paths)
+    _weights(c)
+    first = c["w"].clone()
+    own = np.concatenate([c["rows_of"][0], c["rows_of"][2]])
+    others = torch.tensor(np.setdiff1d(np.arange(c["rows"]), own)).cuda()
+    assert len(others) > lengths[1][0]
+    for q, lse in ((math.nan, 1.0), (math.inf, 1.0), (1.0, math.nan), (1.0, math.inf), (math.nan, math.nan)):
+        c["q"][others], c["lse"][others] = q, lse
+        c["w"].copy_(torch.tensor(c["w_np"]))
+        _weights(c)
+        for b in (0, 2):
+            assert torch.equal(c["w"][b].view(torch.int32), first[b].view(torch.int32)), (q, lse, b)
+
+
 def test_key_weights_behind_the_attention():
     """lse as lora_kv4_attention leaves it: every row gives away a weight of one."""
     c = _weights_case([(1, 3000), (5, 700), (200, 260), (1, 1)], 8, 2, 128, 64, "bf16", seed=96)
@@ -616,6 +634,21 @@ def test_evict_of_long_sequences(keys, budget, kind):
     c = _evict_case(keys, 2, 64, 64, kind, seed=budget, held=0.3)
     _evict(c, budget, 16, 100)
     assert _evict_check(c, budget, 16, 100) > 0
+
+
+@pytest.mark.parametrize("kind", ["spread", "ties"])
+@pytest.mark.parametrize("seqs,most,budget", [(20, 2600, 1200), (20, 900, 300), (62, 700, 300), (16, 3000, 900),
+                                              (17, 5000, 4900)])
+def test_evict_of_many_heads(seqs, most, budget, kind):
+    """As many heads as SMs, some more and some fewer; of one sequence one key goes, of another all but the budget."""
+    rng = np.random.default_rng(seqs + most)
+    keys = [int(x) for x in rng.integers(1, most + 1, seqs)]
+    keys[0], keys[-1], keys[3] = most, budget + 1, budget
+    c = _evict_case(keys, 8, 64, 16, kind, seed=budget)
+    status = _status()
+    _evict(c, budget, 4, 20, status=status)
+    assert _evict_check(c, budget, 4, 20) > 0
+    assert status[0].item() == 0
 
 
 def test_evict_again_and_again():

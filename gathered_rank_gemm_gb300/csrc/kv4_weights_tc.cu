@@ -692,7 +692,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         ok = __all_sync(0xffffffffu, cta_abort.wait(bar(sh.q_full[st]), (t / kTcStages) & 1));
         if (!ok) break;
         fence_proxy_async();  // (rows that copies of other threads wrote)
-        const uint32_t idesc = kIdesc | (static_cast<uint32_t>((min(left, R) + 15) >> 4) << 18);
+        // (of a full tile, all columns are summed, those behind its last row too: products of zeros)
+        const int columns = left >= R ? kTcRows : (left + 15) & ~15;
+        const uint32_t idesc = kIdesc | (static_cast<uint32_t>(columns >> 3) << 17);
         const uint64_t dq = umma_desc_sw128(sbase + st * kTile, 16, 1024);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {  // (one key tile's sums run under the other's products)

@@ -550,6 +550,21 @@ def test_key_weights_of_a_sequence_beside_rows_of_nan(lengths, paths):
             assert torch.equal(c["w"][b].view(torch.int32), first[b].view(torch.int32)), (q, lse, b)
 
 
+@pytest.mark.parametrize("paths", [None, True])
+@pytest.mark.parametrize("qh,kvh", [(100, 1), (65, 1), (44, 2), (26, 1), (34, 1), (6, 1), (130, 1)])
+def test_key_weights_behind_a_call_of_nan(qh, kvh, paths):
+    """What an earlier call has left in a tile's columns behind the last row is not read."""
+    c = _weights_case([(60, 300), (1, 90), (30, 100)], qh, kvh, 64, 16, "bf16", seed=97, paths=paths)
+    c["q"][c["rows"] - 1] = 2.0
+    for value in (math.nan, 3e38, -3e38):
+        e = _weights_case([(150, 6000)], 8, 8, 64, 16, "bf16", seed=98)  # more items than SMs, full tiles
+        e["q"][:] = value
+        _weights(e)
+        c["w"].copy_(torch.tensor(c["w_np"]))
+        _weights(c)
+        _weights_check(c)
+
+
 def test_key_weights_behind_the_attention():
     """lse as lora_kv4_attention leaves it: every row gives away a weight of one."""
     c = _weights_case([(1, 3000), (5, 700), (200, 260), (1, 1)], 8, 2, 128, 64, "bf16", seed=96)

@@ -752,7 +752,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           uint32_t nan_blocks = 0;  // 16-dimension blocks with a NaN scale at a key of the row
           if (*reinterpret_cast<volatile int*>(&sh.poison)) {
             const int32_t* table = a.page_table + static_cast<long long>(done.b) * a.table_stride;
-            const int k0 = max(done_lo, (done.item.kt0() + done.o) * kPreKeys);
+            // (a row of a tree sees its ancestors however far back: its run may begin behind them)
+            const int k0 = max(TREE ? done.item.lo : done_lo, (done.item.kt0() + done.o) * kPreKeys);
             const int k1 = min(TREE ? done.seq.kv - 1 : done_pos,
                                (done.item.kt0() + done.o + done.take - 1) * kPreKeys + kPreKeys - 1);
             for (int key = k0; key <= k1; ++key) {

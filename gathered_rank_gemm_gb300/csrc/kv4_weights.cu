@@ -160,9 +160,9 @@ __global__ void __launch_bounds__(kWtsThreads, kWtsCtas<D>)
           qf[nt][j][0] = pack_f16x2(v[4 * j] * up, v[4 * j + 1] * up);
           qf[nt][j][1] = pack_f16x2(v[4 * j + 2] * up, v[4 * j + 3] * up);
         }
-        // A row that adds nothing sees nothing: no key makes it a NaN.  (Those behind the last
-        // row see what the first does, whose NaN theirs would be.)
-        const int my_pos = r < packed && !adds ? -1 : seq.pos(i), my_lo = seq.first_key(i, a.window);
+        // What adds nothing sees nothing, a row without lse or what lies behind the last row: no
+        // key of NaN makes it one.
+        const int my_pos = r < packed && adds ? seq.pos(i) : -1, my_lo = seq.first_key(i, a.window);
         if (r < packed) pos_min = min(pos_min, my_pos), lo_max = max(lo_max, my_lo);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {

@@ -684,7 +684,8 @@ int lora_kv4_accept(uint8_t *cache, int64_t num_pages, int num_kv_heads, int pag
  * all rows of the sequence.
  *
  *   weights       fp32[num_seqs][num_kv_heads][capacity], in and out
- *   lse           fp32[max_num_tokens][num_q_heads]; -inf: the row adds nothing
+ *   lse           fp32[max_num_tokens][num_q_heads]; -inf: the row adds nothing, to a key of
+ *                 NaN neither
  *   path, path_len  NULL, or int32[num_seqs][max_path] and int32[num_seqs]
  * Sums are fp32, for every key in an order that its sequence's rows and max_q_len settle, whatever
  * else is in the batch; products as in lora_kv4_attention.  lse is fp32, so a weight of a score

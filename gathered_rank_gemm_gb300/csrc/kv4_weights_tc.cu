@@ -104,7 +104,7 @@ __device__ __forceinline__ void tc_rows(const WeightSeq& s, int kt, int group, i
   const int key0 = kt * kTcKeys, key1 = min(key0 + kTcKeys, s.end) - 1;
   const int i0 = max(key0 - before, 0);
   long long i1 = s.take - 1;
-  if (window > 0) i1 = min(i1, static_cast<long long>(key1) + window - 1 - before);
+  if (window > 0 && !(s.path && key1 >= before)) i1 = min(i1, static_cast<long long>(key1) + window - 1 - before);
   row0 = i0 * group;
   rows = i1 >= i0 ? static_cast<int>(i1 - i0 + 1) * group : 0;
 }
@@ -339,6 +339,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     w.it.h = e % a.num_kv_heads;
     w.it.b = x.b, w.it.kt = x.kt, w.it.row0 = x.row0, w.it.rows = x.rows;
     w.it.seq.q0 = x.q0, w.it.seq.q_rows = x.q_rows, w.it.seq.rows = x.seq_rows, w.it.seq.kv = x.kv, w.it.seq.end = x.end;
+    w.it.seq.path = a.path != nullptr;
     return true;
   };
   auto first_item = [&](Walk& w) -> bool {
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       x.row0 = it.row0, x.rows = it.rows;
       x.see0 = max(j - before_rows, 0) * group;
       x.see1 = it.row0 + it.rows;
-      if (a.window > 0) {
+      if (a.window > 0 && !(it.seq.path && j >= before_rows)) {
         const long long i1 = static_cast<long long>(j) + a.window - before_rows;  // behind the last
         if (i1 * group < x.see1) x.see1 = static_cast<int>(max(i1 * group, 0ll));
       }

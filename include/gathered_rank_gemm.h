@@ -619,7 +619,9 @@ int lora_kv4_attention_f16(const uint16_t *q, int64_t q_row_stride, uint16_t *ou
  *     p = kv_len[b] - m + max(named - 1, 0) with the number of rows that its mask names), and
  *   key kv_len[b] - m + c where bit c of its mask is set: bit c % 32 of word c / 32, c < m.
  * A mask names a row's ancestors and the row itself, so that p is the row's position; nothing
- * else is assumed of it, and a row that sees no key gets 0 and lse = -inf.
+ * else is assumed of it, and a row that sees no key gets 0 and lse = -inf.  The window hides keys
+ * in front of the tree only: where it is shorter than the tree is deep, a row sees ancestors that
+ * a row of lora_kv4_attention at its position would not.
  *
  *   tree_mask     device uint32[max_num_tokens][mask_words], 4-byte aligned; bits from m on
  *                 count for nothing
@@ -680,8 +682,9 @@ int lora_kv4_accept(uint8_t *cache, int64_t num_pages, int num_kv_heads, int pag
  * with x and the rows' sight as in lora_kv4_attention (causal, window), q and lse those of
  * that call.  The rows' own keys are new: their weight begins at 0, so weights needs no clearing.
  * With a path, the m rows are the tree's rows path[b][0 .. path_len[b]) in their order (q and lse
- * at q_start[b] + path[b][i]), and kv_len is that after lora_kv4_accept; without one, they are
- * all rows of the sequence.
+ * at q_start[b] + path[b][i]), and kv_len is that after lora_kv4_accept; they see what
+ * lora_kv4_tree_attention has shown them: all rows of the path up to their own, and of the keys in front
+ * what the window leaves.  Without one, they are all rows of the sequence.
  *
  *   weights       fp32[num_seqs][num_kv_heads][capacity], in and out
  *   lse           fp32[max_num_tokens][num_q_heads]; -inf: the row adds nothing, to a key of

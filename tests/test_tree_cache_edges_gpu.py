@@ -7,8 +7,9 @@ import pytest
 
 from gathered_rank_gemm_gb300 import binding as B
 from tests import tree_ref as T
-from tests.test_layer_gpu import _np, lib  # noqa: F401
-from tests.test_tree_cache_gpu import _set_masks, _status, _tree, _tree_case, _weights, _weights_case
+from tests.test_layer_gpu import FP32, K_SCALE, _i32, _np, lib  # noqa: F401
+from tests.test_tree_cache_gpu import (_accept, _formula, _keys, _set_masks, _status, _tree, _tree_case, _weights,
+                                       _weights_case)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -70,3 +71,66 @@ def test_a_key_of_nan_and_paths_that_name_no_row(rows):
     assert B.lora_read_status(status) == B.LORA_STATUS_BAD_LENGTH
     got = c["w"].cpu().numpy()
     assert np.array_equal(got[0, :, :300 - rows], c["w_np"][0, :, :300 - rows]) and (got[0, :, 300 - rows:300] == 0).all()
+
+
+# ------------------------------------------------------------------ paths and windows
+
+def _path_visible(n, m, window):
+    """What the rows of a path see: as the tree's attention has it, which hides keys in front of the tree only."""
+    return T.tree_visible(n, np.tril(np.ones((m, m), bool)), window)
+
+
+@pytest.mark.parametrize("window", [1, 2, 5, 30, 300])
+@pytest.mark.parametrize("lengths,qh,kvh,d", [
+    ([(9, 60), (3, 40), (1, 7), (6, 6), (0, 20)], 2, 2, 64), ([(12, 200), (40, 300), (7, 30)], 8, 2, 128),
+    ([(300, 900), (100, 110), (64, 700)], 4, 1, 64), ([(130, 100), (70, 70)], 5, 1, 128)])
+def test_paths_longer_than_the_window(lengths, qh, kvh, d, window):
+    """Rows of a path give weight to what their lse counts: all of their ancestors, and the keys in front that the
+    window leaves."""
+    c = _weights_case(lengths, qh, kvh, d, 16, "bf16", seed=320 + window, paths=True)
+    c["window"] = window
+    q, lse, want, size = _np(c["q"]), c["lse"].cpu().numpy(), [], []
+    for b, (m, n) in enumerate(lengths):
+        r, k = c["rows_of"][b], _keys(c, b)[0]
+        if m:
+            visible = _path_visible(n, m, window)
+            x = np.einsum("rhd,khd->rhk", q[r], np.repeat(k, qh // kvh, 1)) / math.sqrt(d)
+            x = np.where(visible[:, None], x, -np.inf)
+            with np.errstate(divide="ignore"):
+                lse[r] = np.log(np.exp(x).sum(-1))
+            full = np.zeros((kvh, max(n, c["capacity"])))
+            full[:, :c["capacity"]] = c["w_np"][b]
+            w, s = _formula(q[r], lse[r].astype(np.float64), k, 1 / math.sqrt(d), visible, full)
+        else:
+            w, s = c["w_np"][b].astype(np.float64), np.zeros(c["w_np"][b].shape)
+        want.append(w), size.append(s)
+    c["lse"].copy_(torch.tensor(lse))
+    _weights(c)
+    got = c["w"].cpu().numpy()
+    for b, (m, n) in enumerate(lengths):
+        tol = FP32 * size[b] + 2.0 ** -22 * np.abs(want[b])
+        bad = ~(np.abs(got[b] - want[b]) <= tol)
+        assert not bad.any(), (b, m, n, bad.sum(), np.argwhere(bad)[:4], got[b][bad][:4], want[b][bad][:4])
+
+
+@pytest.mark.parametrize("rows", [10, 90])
+def test_a_row_of_a_path_gives_away_a_weight_of_one_in_any_window(rows):
+    """Tree attention, acceptance and weights one behind the other: every row on the path gives one a head."""
+    for window in (0, 1, 3, 50):
+        c = _tree_case([(rows, 60 + rows), (rows // 2, 200)], 8, 2, 128, 16, "bf16", seed=330 + rows)
+        rng = np.random.default_rng(rows)
+        c["sees"] = [T.tree(rng, m, deep=0.9) for m, _ in c["lengths"]]
+        _set_masks(c)
+        _tree(c, window)
+        paths = [np.nonzero(s[s.sum(1).argmax()])[0].tolist() for s in c["sees"]]
+        assert len(paths[0]) > rows // 3
+        wide = max(map(len, paths))
+        path, length, kv = _i32([p + [-1] * (wide - len(p)) for p in paths]), _i32([len(p) for p in paths]), _i32([0, 0])
+        _accept(dict(c, path=path, len=length, out=kv))
+        w = torch.zeros(2, 2, 200, device="cuda")
+        B.lora_kv4_key_weights(w, c["cache"], c["q"], c["lse"], c["start"], kv, c["table"], c["max_q"], 1 / math.sqrt(128),
+                               window=window, k_scale=K_SCALE, path=path, path_len=length)
+        total = w.double().sum(-1).cpu()
+        want = torch.tensor([4.0 * len(p) for p in paths])[:, None].expand(-1, 2)
+        # lse and the scores are off by 2^-16 of sum |q k|, at most 60 here with 1 + |lse|
+        assert ((total - want).abs() <= want * FP32 * 64).all(), (window, total, want)

@@ -133,7 +133,7 @@ bool path_ok(int64_t max_path) { return max_path >= 1 && max_path <= LORA_KV4_MA
 bool capacity_ok(int64_t capacity) { return capacity >= 1 && capacity <= LORA_KV4_MAX_KEYS; }
 bool seqs_ok(int64_t num_seqs) { return num_seqs >= 1 && num_seqs <= LORA_KV4_MAX_SEQS; }
 // Whether an array of n words and one of m have one in common.
-bool overlap(const int32_t* a, int64_t n, const int32_t* b, int64_t m) {
+bool overlap(const void* a, int64_t n, const void* b, int64_t m) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + static_cast<uintptr_t>(m) * 4 && y < x + static_cast<uintptr_t>(n) * 4;
 }
@@ -374,7 +374,9 @@ int lora_kv4_accept(uint8_t* cache, int64_t num_pages, int num_kv_heads, int pag
       !table_ok(table_stride, page_size) || !path_ok(max_path) ||
       overlap(kv_len, num_seqs, kv_len_out, num_seqs) ||
       overlap(path_len, num_seqs, kv_len_out, num_seqs) ||
-      overlap(q_start, num_seqs + 1, kv_len_out, num_seqs))
+      overlap(q_start, num_seqs + 1, kv_len_out, num_seqs) ||
+      overlap(path, num_seqs * max_path, kv_len_out, num_seqs) ||
+      overlap(page_table, num_seqs * table_stride, kv_len_out, num_seqs))
     return LORA_ERR_SHAPE;
   if (!aligned(cache, 16) || !aligned(q_start, 4) || !aligned(kv_len, 4) ||
       !aligned(page_table, 4) || !aligned(path, 4) || !aligned(path_len, 4) ||
@@ -410,7 +412,10 @@ int lora_kv4_evict(uint8_t* cache, int64_t num_pages, int num_kv_heads, int page
       !table_ok(table_stride, page_size) || !capacity_ok(capacity) || budget < 1 ||
       budget >= (1ll << 31) || sink < 0 || recent < 0 || sink > budget || recent > budget - sink ||
       overlap(kv_len, num_seqs, kv_len_out, num_seqs) ||
-      overlap(last_pos, num_seqs, kv_len_out, num_seqs))
+      overlap(last_pos, num_seqs, kv_len_out, num_seqs) ||
+      overlap(page_table, num_seqs * table_stride, kv_len_out, num_seqs) ||
+      overlap(weights, num_seqs * num_kv_heads * capacity, kv_len_out, num_seqs) ||
+      overlap(key_pos, num_seqs * num_kv_heads * capacity, kv_len_out, num_seqs))
     return LORA_ERR_SHAPE;
   if (!aligned(cache, 16) || !aligned(weights, 4) || !aligned(key_pos, 4) || !aligned(kv_len, 4) ||
       !aligned(last_pos, 4) || !aligned(page_table, 4) || !aligned(kv_len_out, 4) ||

@@ -734,7 +734,7 @@ int lora_kv4_key_weights_f16(float *weights, int64_t capacity, const uint16_t *q
  *   key_pos       int32, the same; filled with -1 where a sequence begins
  *   last_pos      device int32[num_seqs]: the position of the last key's token
  *   budget        at least 1; sink + recent <= budget, both at least 0
- *   kv_len_out    device int32[num_seqs], apart from kv_len and last_pos
+ *   kv_len_out    device int32[num_seqs], apart from the other arrays
  * A sequence's pages hold no other sequence's.  Data that does not fit: kv_len is clamped to
  * the table and the capacity (LORA_STATUS_BAD_LENGTH); keys are not moved from or to a page
  * outside the cache (LORA_STATUS_BAD_SLOT), though their weights and positions are.

@@ -691,9 +691,12 @@ int lora_kv4_accept(uint8_t *cache, int64_t num_pages, int num_kv_heads, int pag
  *                 NaN neither
  *   path, path_len  NULL, or int32[num_seqs][max_path] and int32[num_seqs]
  * Sums are fp32, for every key in an order that its sequence's rows and max_q_len settle, whatever
- * else is in the batch; products as in lora_kv4_attention.  lse is fp32, so a weight of a score
- * x is known to within a factor of e^(|x| 2^-23).  A NaN in a row's q or lse makes the weights
- * that it adds to NaN, one in a key that key's; q and lse of rows of no sequence may hold anything.  Data that does not fit: as in lora_kv4_attention; keys from capacity
+ * else is in the batch; products as in lora_kv4_attention.  A term exp(x - lse) is known to within 2^-16
+ * of it times 1 + |lse| + softmax_scale * sum_d |q_d K_d| (an lse held in fp32 alone takes 2^-24 |lse|);
+ * one below 2^-126 counts as 0; a sum of n terms and the weight before, none negative, loses n 2^-24 of it at
+ * most.  A NaN in a row's q or lse makes the weights that it adds to NaN, one in a key that key's; q and
+ * lse of rows of no sequence may hold anything.
+ * Data that does not fit: as in lora_kv4_attention; keys from capacity
  * on have no weight, rows beyond max_q_len add nothing, nor does a path's row outside the
  * sequence's rows (LORA_STATUS_BAD_LENGTH).  A key whose page is outside the cache draws no
  * weight (LORA_STATUS_BAD_SLOT).

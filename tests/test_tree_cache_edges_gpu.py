@@ -6,8 +6,9 @@ import numpy as np
 import pytest
 
 from gathered_rank_gemm_gb300 import binding as B
+from tests import layer_ref as R
 from tests import tree_ref as T
-from tests.test_layer_gpu import FP32, K_SCALE, _i32, _np, lib  # noqa: F401
+from tests.test_layer_gpu import DTYPES, FP32, K_SCALE, _i32, _np, lib  # noqa: F401
 from tests.test_tree_cache_gpu import (_accept, _formula, _keys, _set_masks, _status, _tree, _tree_case, _weights,
                                        _weights_case)
 
@@ -134,3 +135,90 @@ def test_a_row_of_a_path_gives_away_a_weight_of_one_in_any_window(rows):
         want = torch.tensor([4.0 * len(p) for p in paths])[:, None].expand(-1, 2)
         # lse and the scores are off by 2^-16 of sum |q k|, at most 60 here with 1 + |lse|
         assert ((total - want).abs() <= want * FP32 * 64).all(), (window, total, want)
+
+
+def _random_case(lengths, qh, kvh, d, page, dtype, seed=0, window=0, paths=False, capacity=None, grow=1.0):
+    """As _weights_case, with codes drawn as such (quick for many keys) and keys of about 1.4 K_SCALE * 32."""
+    rng = np.random.default_rng(seed)
+    per = [-(-n // page) for _, n in lengths]
+    order, wide = rng.permutation(sum(per) + 3), max(1, max(per))
+    table = np.full((len(per), wide), -7, np.int64)
+    at = 0
+    for b, x in enumerate(per):
+        table[b, :x] = order[at:at + x]
+        at += x
+    cache = rng.integers(0, 256, (len(order), kvh, page // 16, 18 * d), dtype=np.uint8)
+    cache[..., 16 * d:] = rng.integers(0x50, 0x5C, cache[..., 16 * d:].shape, dtype=np.uint8)  # scales of 8 to 22
+    behind = 8 if paths else 0
+    start = np.concatenate([[0], np.cumsum([m + behind for m, _ in lengths])])
+    rows = int(start[-1]) + 2
+    q = torch.tensor(rng.standard_normal((rows, qh, d)) * grow, dtype=torch.float32).to(DTYPES[dtype]).cuda()
+    capacity = capacity or max(1, max(n for _, n in lengths))
+    w = rng.random((len(lengths), kvh, capacity)).astype(np.float32)
+    c = dict(lengths=lengths, q=q, cache_np=cache, cache=torch.tensor(cache).cuda(), table_np=table, table=_i32(table),
+             start=_i32(start), start_np=start, kv=_i32([n for _, n in lengths]), page=page, dtype=dtype, rows=rows, qh=qh,
+             kvh=kvh, d=d, max_q=max(1, max(m for m, _ in lengths)), out=torch.full_like(q, 7), window=window, path=None,
+             len=None, capacity=capacity, w_np=w, w=torch.tensor(w).cuda(),
+             rows_of=[np.arange(a, a + m) for a, (m, _) in zip(start, lengths)])
+    if paths:
+        spread = [np.sort(rng.permutation(m + behind)[:m]) for m, _ in lengths]
+        path = np.full((len(lengths), c["max_q"] + 1), -3, np.int64)
+        for b, p in enumerate(spread):
+            path[b, :len(p)] = p
+        c["path"], c["len"] = _i32(path), _i32([m for m, _ in lengths])
+        c["rows_of"] = [a + p for a, p in zip(start, spread)]
+    c["lse"] = torch.full((rows, qh), 7.0, device="cuda")
+    return c
+
+
+def _sight(c, b):
+    m, n = c["lengths"][b]
+    return T.tree_visible(n, np.tril(np.ones((m, m), bool)), c["window"]) if c["path"] is not None else \
+        T.causal_visible(n, m, c["window"])
+
+
+def _random_weights_check(c, some=None):
+    """_weights_check of every key head (or of those in `some`) by itself, with the lse that the rows have."""
+    g, d = c["qh"] // c["kvh"], c["d"]
+    heads = range(c["kvh"]) if some is None else some
+    q, lse = _np(c["q"]), c["lse"].cpu().numpy()
+    keys = {(b, h): R.read_cache(c["cache_np"][:, h:h + 1], c["table_np"][b][:-(-n // c["page"])], n, c["page"], d)[0] * K_SCALE
+            for b, (m, n) in enumerate(c["lengths"]) if m and n for h in heads}
+    for b, h in keys:
+        r, see = c["rows_of"][b], _sight(c, b)
+        for i in range(h * g, h * g + g):
+            x = np.where(see, q[r, i] @ keys[b, h][:, 0].T / math.sqrt(d), -np.inf)
+            top = np.where(see.any(1), x.max(1), 0)
+            with np.errstate(divide="ignore"):
+                lse[r, i] = top + np.log(np.exp(x - top[:, None]).sum(1))
+    c["lse"].copy_(torch.tensor(lse))
+    status = _status()
+    _weights(c, status=status)
+    assert status[0].item() == 0
+    got = c["w"].cpu().numpy()
+    for b, (m, n) in enumerate(c["lengths"]):
+        for h in heads:
+            if not (m and n):
+                assert np.array_equal(got[b, h], c["w_np"][b, h])
+                continue
+            r = c["rows_of"][b]
+            full = c["w_np"][b, h:h + 1].astype(np.float64)
+            want, size = _formula(q[r, h * g:h * g + g], lse[r, h * g:h * g + g].astype(np.float64), keys[b, h],
+                                  1 / math.sqrt(d), _sight(c, b), full)
+            # (fp32 holds no term below 2^-126: the exponential gives 0 there, m * g times at most)
+            bad = ~(np.abs(got[b, h] - want[0]) <= FP32 * size[0] + 2.0 ** -22 * np.abs(want[0]) + m * g * 2.0 ** -126)
+            assert not bad.any(), (b, h, m, n, bad.sum(), np.argwhere(bad)[:4], got[b, h][bad][:4], want[0][bad][:4])
+            assert np.array_equal(got[b, h, n:], c["w_np"][b, h, n:])
+
+
+# ------------------------------------------------------------------ scores of tens and hundreds
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("lengths,qh,kvh,d", [([(1, 900), (3, 400), (8, 300)], 4, 1, 128), ([(60, 700), (100, 130)], 4, 2, 64)])
+@pytest.mark.parametrize("grow", [30.0, 200.0])
+def test_key_weights_of_large_scores(lengths, qh, kvh, d, grow, dtype):
+    """Scores of tens and hundreds whose products cancel: each term of a weight is known to within 2^-16 of
+    1 + |lse| + sum |q k|, which the check allows."""
+    c = _random_case(lengths, qh, kvh, d, 16, dtype, seed=370, grow=grow)
+    _random_weights_check(c)
+    assert c["lse"][:c["start_np"][-1]].abs().max() > 2 * grow

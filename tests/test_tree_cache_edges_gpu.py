@@ -222,3 +222,46 @@ def test_key_weights_of_large_scores(lengths, qh, kvh, d, grow, dtype):
     c = _random_case(lengths, qh, kvh, d, 16, dtype, seed=370, grow=grow)
     _random_weights_check(c)
     assert c["lse"][:c["start_np"][-1]].abs().max() > 2 * grow
+
+
+# ------------------------------------------------------------------ the same bits
+
+@pytest.mark.parametrize("paths", [None, True])
+@pytest.mark.parametrize("lengths,qh,kvh", [
+    ([(1, 900), (3, 333), (8, 700), (1, 50), (2, 350)], 8, 2), ([(1, 900), (3, 333), (64, 700), (1, 50), (200, 350)], 8, 2),
+    ([(1 + b % 3 * 20, 300 + 7 * b) for b in range(40)], 4, 1)])
+def test_a_sequences_weights_are_the_same_bits_in_any_batch(lengths, qh, kvh, paths):
+    """Alone with the batch's bound on the rows, a sequence's weights are what they are in the batch."""
+    c = _weights_case(lengths, qh, kvh, 128, 16, "bf16", seed=340, paths=paths)
+    _weights(c)
+    some = range(len(lengths)) if len(lengths) < 10 else (0, 1, 2, 20, 39)
+    for b in some:
+        r = torch.arange(int(c["start_np"][b]), int(c["start_np"][b + 1]), device="cuda")
+        q, lse = torch.zeros_like(c["q"]), torch.zeros_like(c["lse"])
+        q[:len(r)], lse[:len(r)] = c["q"][r], c["lse"][r]
+        w = torch.tensor(c["w_np"][b:b + 1]).cuda()
+        _weights({**c, "w": w, "q": q, "lse": lse, "start": _i32([0, len(r)]), "kv": c["kv"][b:b + 1],
+                  "table": c["table"][b:b + 1], "path": c["path"][b:b + 1] if paths else None,
+                  "len": c["len"][b:b + 1] if paths else None})
+        assert torch.equal(w[0].view(torch.int32), c["w"][b].view(torch.int32)), b
+
+
+@pytest.mark.parametrize("lengths,qh,kvh,d,window,dtype", [
+    ([(15, 700)], 32, 8, 128, 0, "bf16"), ([(9 + b % 56, 500 + 100 * b) for b in range(32)], 32, 8, 128, 0, "bf16"),
+    ([(33 + b % 5, 200 + 240 * b) for b in range(20)], 24, 4, 64, 2048, "f16"), ([(60, 30000), (50, 20000)], 8, 8, 128, 0, "bf16")])
+def test_tree_attention_repeats_itself(lengths, qh, kvh, d, window, dtype):
+    """In one workspace and in others, behind calls that leave other data on the chip."""
+    c = _random_case(lengths, qh, kvh, d, 16, dtype, seed=350)
+    c["sees"], c["words"] = [T.tree(np.random.default_rng(b), m) for b, (m, _) in enumerate(lengths)], 2
+    _set_masks(c)
+    ws = _tree(c, window)
+    first = c["out"].clone(), c["lse"].clone()
+    other = _random_case([(70, 900), (3, 4000)], 8, 2, 64, 16, "f16", seed=351)
+    other["sees"], other["words"] = [np.tril(np.ones((m, m), bool)) for m, _ in other["lengths"]], 3
+    _set_masks(other)
+    for i in range(8):
+        _tree(other)
+        c["out"].fill_(7)
+        _tree(c, window, **({} if i % 2 else dict(workspace=ws)))
+        assert torch.equal(c["out"].view(torch.int16), first[0].view(torch.int16)), i
+        assert torch.equal(c["lse"].view(torch.int32), first[1].view(torch.int32)), i

@@ -265,3 +265,73 @@ def test_tree_attention_repeats_itself(lengths, qh, kvh, d, window, dtype):
         _tree(c, window, **({} if i % 2 else dict(workspace=ws)))
         assert torch.equal(c["out"].view(torch.int16), first[0].view(torch.int16)), i
         assert torch.equal(c["lse"].view(torch.int32), first[1].view(torch.int32)), i
+
+
+# ------------------------------------------------------------------ how items of many rows are shared out
+
+def _items(c, few=32, keys=256):
+    """Pairs of a sequence and a tile of 256 keys, and items a CTA: pairs times key heads over the SMs."""
+    pairs = 0
+    for m, n in c["lengths"]:
+        if m * (c["qh"] // c["kvh"]) > few:
+            first = max(0, n - m - c["window"] + 1) if c["window"] else 0
+            pairs += max(0, -(-n // keys) - first // keys)
+    return pairs, pairs * c["kvh"] / torch.cuda.get_device_properties(0).multi_processor_count
+
+
+def _ragged(seqs, rows=40, least=300, spread=401):
+    """Sequences of `rows` rows, some with few and some without any between them."""
+    return [((0, 1, 2, rows, rows, rows, rows - 3)[b % 7] if b else 0, least + b * 131 % spread) for b in range(seqs)]
+
+
+@pytest.mark.parametrize("paths", [False, True])
+def test_more_pairs_than_are_sorted(paths):
+    """Equal runs of all items: across key tiles and sequences."""
+    c = _random_case(_ragged(420), 2, 1, 64, 16, "bf16", seed=360, paths=paths)
+    pairs, each = _items(c)
+    assert pairs > 512 and 2 < each <= 16
+    _random_weights_check(c)
+
+
+@pytest.mark.parametrize("paths", [False, True])
+def test_more_pairs_than_are_sorted_in_a_window(paths):
+    c = _random_case(_ragged(700, least=500), 3, 1, 64, 32, "f16", seed=361, paths=paths, window=170)
+    assert _items(c)[0] > 512
+    _random_weights_check(c)
+
+
+def test_more_pairs_than_are_sorted_of_many_heads():
+    """... across the heads of a sequence, whose tiles are cut by the ends of runs."""
+    c = _random_case(_ragged(420, least=280, spread=300), 4, 4, 64, 16, "bf16", seed=362)
+    pairs, each = _items(c)
+    assert pairs > 512 and 4 < each <= 16
+    _random_weights_check(c, some=(0, 1, 3))
+
+
+@pytest.mark.parametrize("paths,window", [(False, 0), (True, 0), (False, 6000)])
+def test_more_items_than_are_dealt(paths, window):
+    """Few pairs, so many heads that a CTA has more than 16 items: runs across tiles and heads."""
+    c = _random_case([(40, 9000), (2, 400), (34, 7000), (0, 90), (50, 6000)], 32, 32, 64, 64, "bf16", seed=363, paths=paths,
+                     window=window)
+    pairs, each = _items(c)
+    assert pairs <= 512 and (each > 16) == (window == 0)
+    _random_weights_check(c, some=(0, 1, 13, 30, 31))
+
+
+@pytest.mark.parametrize("paths,window", [(False, 0), (True, 0), (True, 90), (False, 90)])
+def test_pairs_that_one_lane_each_places(paths, window):
+    """161 to 512 pairs in order of their rows, and a few rounds of dealing."""
+    c = _random_case(_ragged(240, rows=70), 2, 2, 64, 16, "bf16", seed=364, paths=paths, window=window)
+    pairs, each = _items(c)
+    assert 160 < pairs <= 512 and 2 < each <= 16
+    _random_weights_check(c)
+
+
+@pytest.mark.parametrize("paths,window", [(False, 0), (True, 0), (False, 2000)])
+def test_several_rounds_of_dealing(paths, window):
+    """Items of one to eight row tiles, up to 16 rounds of them."""
+    c = _random_case([(500, 6000), (40, 9000), (3, 700), (200, 3000), (90, 2000)], 16, 16, 64, 64, "f16", seed=365,
+                     paths=paths, window=window)
+    pairs, each = _items(c)
+    assert pairs <= 160 and 3 < each <= 16
+    _random_weights_check(c, some=(0, 7, 15))

@@ -313,7 +313,7 @@ __device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap* map
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
       : "memory");
 }
-// tma_load_2d with an L2 cache policy (createpolicy) for the loaded lines.
+// The same of box (x, y, z) of a 3-D tensor map: the whole box's bytes count, filled ones too.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z,
                                             uint32_t bar) {
   asm volatile(
@@ -322,6 +322,7 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
+// tma_load_2d with an L2 cache policy (createpolicy) for the loaded lines.
 __device__ __forceinline__ void tma_load_2d_hint(uint32_t dst, const CUtensorMap* map, int x,
                                                  int y, uint32_t bar, uint64_t pol) {
   asm volatile(

@@ -162,7 +162,8 @@ __global__ void __launch_bounds__(kWtsThreads, kWtsCtas<D>)
         }
         // What adds nothing sees nothing, a row without lse or what lies behind the last row: no
         // key of NaN makes it one.
-        const int my_pos = r < packed && adds ? seq.pos(i) : -1, my_lo = seq.first_key(i, a.window);
+        const int my_pos = r < packed && adds ? seq.pos(i) : -1;
+        const int in_window = seq.first_key(i, a.window), my_lo = a.path ? min(in_window, fresh) : in_window;
         if (r < packed) pos_min = min(pos_min, my_pos), lo_max = max(lo_max, my_lo);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {

@@ -14,7 +14,6 @@ struct WeightSeq {
   int take;    // those that are summed: the first max_q_len
   int kv;      // keys
   int end;     // keys that have a weight to go to
-  bool path;   // the rows are a path's
   bool odd;    // something had to be clamped
   __device__ __forceinline__ static WeightSeq of(const Kv4WeightsArgs& p, int b) {
     const int a = p.q_start[b], e = p.q_start[b + 1], k = p.kv_len[b];
@@ -23,8 +22,7 @@ struct WeightSeq {
     s.q_rows = min(max(e, s.q0), p.max_num_tokens) - s.q0;
     s.odd = a != s.q0 || e != s.q0 + s.q_rows;
     s.rows = s.q_rows;
-    s.path = p.path != nullptr;
-    if (s.path) {
+    if (p.path) {
       const int len = p.path_len[b];
       s.rows = min(max(len, 0), min(s.q_rows, p.max_path));
       s.odd = s.odd || s.rows != len;
@@ -36,11 +34,11 @@ struct WeightSeq {
     return s;
   }
   __device__ __forceinline__ int pos(int i) const { return kv - rows + i; }
-  // The first key that row i sees.  A path's row sees all of its ancestors, as the tree's attention
-  // had it: the window hides keys in front of the path only.
+  // The first key in row i's window.  A path's row sees all of its ancestors besides, as the tree's
+  // attention had it: the window hides keys in front of the path only.  (The first row has none.)
   __device__ __forceinline__ int first_key(int i, int window) const {
-    const int at = pos(i), lo = window > 0 && at >= window ? at - window + 1 : 0;
-    return path ? min(lo, max(kv - rows, 0)) : lo;
+    const int at = pos(i);
+    return window > 0 && at >= window ? at - window + 1 : 0;
   }
   // Blocks of 16 keys that some row sees or that are the rows' own: [first, first + count).
   __device__ __forceinline__ int first_block(int window) const { return first_key(0, window) / 16; }

@@ -42,6 +42,12 @@ __device__ __forceinline__ uint32_t f32x8_to_e2m1(const float* f) {
       : "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]));
   return w;
 }
+// Products of two fp16 pairs (of a code and its scale: exact).
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 // Two e4m3 bytes (low one first) as an fp16 pair.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t w) {
   uint32_t h;

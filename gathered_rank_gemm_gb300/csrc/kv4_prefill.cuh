@@ -125,11 +125,6 @@ struct PreShared {
   int most;  // key tiles of the longest item
 };
 
-__device__ __forceinline__ uint32_t pre_hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t pre_prmt(uint32_t a, uint32_t sel) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(r) : "r"(a), "r"(sel));
@@ -953,8 +948,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             e2m1x8_to_f16(x[e], f);
             const int ch = 4 * c + e;
             *reinterpret_cast<uint4*>(tile + (ch >> 3) * kAtom + swz128(r, ch & 7)) =
-                make_uint4(pre_hmul2(f[0], s[e / 2]), pre_hmul2(f[1], s[e / 2]),
-                           pre_hmul2(f[2], s[e / 2]), pre_hmul2(f[3], s[e / 2]));
+                make_uint4(hmul2(f[0], s[e / 2]), hmul2(f[1], s[e / 2]),
+                           hmul2(f[2], s[e / 2]), hmul2(f[3], s[e / 2]));
           }
         }
       };

@@ -33,11 +33,6 @@ struct WtsParams {
   Kv4WeightsArgs a;
   int max_packed_rows;  // sequences with more packed rows are not this kernel's
 };
-__device__ __forceinline__ uint32_t wts_hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t wts_both(uint32_t a, bool high) {
   uint32_t r;
   asm("prmt.b32 %0, %1, %1, %2;\n" : "=r"(r) : "r"(a), "r"(high ? 0x3232u : 0x1010u));
@@ -240,8 +235,8 @@ __global__ void __launch_bounds__(kWtsThreads, kWtsCtas<D>)
             const uint32_t xa = wts_both(ha, D == 128 && w >= 2), xb = wts_both(hb, D == 128 && w >= 2);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t frag[4] = {wts_hmul2(fa[2 * j], xa), wts_hmul2(fb[2 * j], xb),
-                                        wts_hmul2(fa[2 * j + 1], xa), wts_hmul2(fb[2 * j + 1], xb)};
+              const uint32_t frag[4] = {hmul2(fa[2 * j], xa), hmul2(fb[2 * j], xb),
+                                        hmul2(fa[2 * j + 1], xa), hmul2(fb[2 * j + 1], xb)};
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma_f16(sc[nt], frag, qf[nt][2 * w + j][0], qf[nt][2 * w + j][1]);

@@ -109,11 +109,6 @@ __device__ __forceinline__ void tc_rows(const WeightSeq& s, int kt, int group, i
   row0 = i0 * group;
   rows = i1 >= i0 ? static_cast<int>(i1 - i0 + 1) * group : 0;
 }
-__device__ __forceinline__ uint32_t tc_hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;\n" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ bool tc_elect() {
   uint32_t r;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
@@ -578,7 +573,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           e2m1x8_to_f16(y[e], u);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            u[i] = tc_hmul2(u[i], f[e / 2]);
+            u[i] = hmul2(u[i], f[e / 2]);
             if constexpr (!F16) {
               const float2 w = unpack_f16x2(u[i]);
               u[i] = pack_bf16x2(w.x, w.y);

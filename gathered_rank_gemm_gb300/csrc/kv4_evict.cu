@@ -14,9 +14,10 @@
 // shared memory holds are formed again wherever they are looked at.
 //
 // What bounds it: steps that follow one another, each with a barrier or a trip to memory (the
-// weights, three counts, two sums, rounds of moves), not bytes: 2048 heads of 2000 to 2100 keys,
-// budget 2048, take 34 us, where reading weights and positions once would take 5; 48 heads of 10000
-// to 30000 keys, budget 2000, 38 us.  Hence the threads of a CTA: many where a head has an SM to
+// weights, three counts, two sums, rounds of moves), and instructions where heads are many, not
+// bytes: 2048 heads of 2000 to 2100 keys, budget 2048, take 34 us, where reading weights and
+// positions once would take 5 (19.0 million warp instructions, 59 % of the issue slots); 48 heads of
+// 10000 to 30000 keys, budget 2000, 38 us.  Hence the threads of a CTA: many where a head has an SM to
 // itself, few where other heads fill the waits.
 #include <algorithm>
 #include <type_traits>
@@ -356,6 +357,8 @@ int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
   //   152 heads of 4096 + 104 17.7 / 13.0 / 11.4; 304 of them 21.2 / 16.8 / 21.3
   //   304 heads of 2000 + 6000 30.5 / 23.1 / 28.4; 608 heads of 2000 + 100 21.8 / 26.8 / 38.1
   //   608 heads of 8192 + 100 40.0 / 44.8 / 54.5; of 20000 + 200 (one or two CTAs an SM) 122 / - / 81
+  // The host knows the buffers' widths, not the lengths: 2048 heads of 2100 keys take 31 us with a
+  // capacity of 2100, 49 us of 16384, 73 us of 16400 to 40960.
   // Clusters against none: 8 heads of 2000 + 28000 keys 22.8 (eight CTAs) and 31.7, 48 heads of
   // them 37.8 (two) and 43.8, 8 heads of 4096 + 4 11.4 and 10.1.
   int threads = 1024;

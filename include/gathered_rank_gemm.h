@@ -690,6 +690,8 @@ int lora_kv4_accept(uint8_t *cache, int64_t num_pages, int num_kv_heads, int pag
  *   lse           fp32[max_num_tokens][num_q_heads]; -inf: the row adds nothing, to a key of
  *                 NaN neither
  *   path, path_len  NULL, or int32[num_seqs][max_path] and int32[num_seqs]
+ *   max_q_len     a bound on the rows that count (host): of the paths, where there are some; it picks
+ *                 the kernels
  * Sums are fp32, for every key in an order that its sequence's rows and max_q_len settle, whatever
  * else is in the batch; products as in lora_kv4_attention.  A term exp(x - lse) is known to within 2^-16
  * of it times 1 + |lse| + softmax_scale * sum_d |q_d K_d| (an lse held in fp32 alone takes 2^-24 |lse|);

@@ -9,8 +9,9 @@ from gathered_rank_gemm_gb300 import binding as B
 from tests import layer_ref as R
 from tests import tree_ref as T
 from tests.test_layer_gpu import DTYPES, FP32, K_SCALE, _i32, _np, lib  # noqa: F401
-from tests.test_tree_cache_gpu import (_accept, _formula, _keys, _set_masks, _status, _tree, _tree_case, _weights,
-                                       _weights_case)
+from tests.test_tree_cache_gpu import (_accept, _evict, _evict_case, _evict_check, _formula, _keys, _set_masks,
+                                       _status, _tree, _tree_case, _tree_check, _weights, _weights_case,
+                                       _weights_check)
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -335,3 +336,50 @@ def test_several_rounds_of_dealing(paths, window):
     pairs, each = _items(c)
     assert pairs <= 160 and 3 < each <= 16
     _random_weights_check(c, some=(0, 7, 15))
+
+
+# ------------------------------------------------------------------ captured calls
+
+def _captured(call, before, after, check):
+    """Captures call(before), replays it over the tensors of `after`, which are of the same shapes, and checks those."""
+    call(before)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(before)
+    for name in ("cache", "q", "start", "kv", "table", "mask", "path", "len", "lse", "w", "out", "pos", "last"):
+        if isinstance(before.get(name), torch.Tensor):
+            before[name].copy_(after[name])
+    graph.replay()
+    check({**after, **{n: before[n] for n in ("cache", "out", "lse", "w", "pos") if n in before}})
+
+
+@pytest.mark.parametrize("first,then", [([(140, 300), (20, 200)], [(60, 295), (100, 200)]), ([(30, 40), (1, 16)], [(1, 33), (30, 7)])])
+def test_tree_attention_in_a_graph_over_other_lengths(first, then):
+    a, b = (_tree_case(x, 4, 2, 128, 16, "bf16", seed=380 + i, words=5) for i, x in enumerate((first, then)))
+    a["max_q"] = b["max_q"] = max(m for m, _ in first)
+    space = torch.zeros(B.lora_kv4_attention_workspace_size(2, a["rows"], a["max_q"], 4, 2, 128), dtype=torch.uint8, device="cuda")
+    _captured(lambda c: _tree(c, workspace=space), a, b, _tree_check)
+
+
+@pytest.mark.parametrize("paths", [None, True])
+@pytest.mark.parametrize("first,then", [([(140, 300), (20, 200)], [(60, 295), (100, 200)]), ([(300, 700), (3, 90)], [(3, 699), (300, 90)])])
+def test_key_weights_of_many_rows_in_a_graph_over_other_lengths(first, then, paths):
+    a, b = (_weights_case(x, 8, 2, 64, 16, "f16", seed=390 + i, paths=paths, capacity=700) for i, x in enumerate((first, then)))
+    assert a["max_q"] >= b["max_q"] and a["q"].shape == b["q"].shape
+    if paths:  # as wide as the first's paths
+        b["path"] = torch.nn.functional.pad(b["path"], (0, a["path"].shape[1] - b["path"].shape[1]), value=-3)
+    b["max_q"] = a["max_q"]
+    _captured(_weights, a, b, _weights_check)
+
+
+@pytest.mark.parametrize("first,then,heads,budget", [([9000, 40], [40, 9000], 2, 2000), ([300, 2100], [2090, 305], 8, 300)])
+def test_eviction_in_a_graph_over_other_lengths(first, then, heads, budget):
+    """By a cluster of CTAs a head, and by single ones."""
+    a, b = (_evict_case(x, heads, 64, 16, seed=400 + i, capacity=max(first)) for i, x in enumerate((first, then)))
+    for x in (a, b):  # pages for the longest in every sequence
+        wide = -(-max(first) // 16)
+        x["table_np"] = np.arange(2 * wide).reshape(2, wide)
+        x["cache_np"] = np.random.default_rng(wide).integers(0, 256, (2 * wide, heads, 1, 18 * 64), dtype=np.uint8)
+        x["table"], x["cache"] = _i32(x["table_np"]), torch.tensor(x["cache_np"]).cuda()
+    b["out"] = a["out"]
+    _captured(lambda c: _evict(c, budget, 4, 30), a, b, lambda c: _evict_check(c, budget, 4, 30))

@@ -357,8 +357,8 @@ int launch_kv4_evict(const Kv4EvictArgs& a, cudaStream_t stream) {
   //   152 heads of 4096 + 104 17.7 / 13.0 / 11.4; 304 of them 21.2 / 16.8 / 21.3
   //   304 heads of 2000 + 6000 30.5 / 23.1 / 28.4; 608 heads of 2000 + 100 21.8 / 26.8 / 38.1
   //   608 heads of 8192 + 100 40.0 / 44.8 / 54.5; of 20000 + 200 (one or two CTAs an SM) 122 / - / 81
-  // The host knows the buffers' widths, not the lengths: 2048 heads of 2100 keys take 31 us with a
-  // capacity of 2100, 49 us of 16384, 73 us of 16400 to 40960.
+  // The host knows the buffers' widths, not the lengths: 2048 heads of 2100 keys (one state over
+  // and over) take 31 us with a capacity of 2100, 49 us of 16384, 73 us of 16400 to 40960.
   // Clusters against none: 8 heads of 2000 + 28000 keys 22.8 (eight CTAs) and 31.7, 48 heads of
   // them 37.8 (two) and 43.8, 8 heads of 4096 + 4 11.4 and 10.1.
   int threads = 1024;
